@@ -4,10 +4,10 @@ A fine-tuning step of adapted 4-bit projections runs three things besides the
 projections themselves, and each is a family of cases here:
 
   ckpt   8-bit activation checkpoints: X [M, K] kept as one byte per value and
-         one bf16 absolute maximum per 64 values of a row.
-             int8:  q = round(127 x / absmax),           x^ = bf16(q absmax / 127)
-             e4m3:  q = E4M3(256 x / absmax),            x^ = bf16(q absmax / 256)
-         (round: ties to even; a block of zeros has absmax 0 and x^ = 0).
+         one bf16 step per 64 values of a row.
+             int8:  step = bf16(absmax / 127),  q = round(x / step),  x^ = bf16(q step)
+             e4m3:  step = bf16(absmax / 256),  q = E4M3(x / step),   x^ = bf16(q step)
+         (round: ties to even; a block of zeros has step 0 and x^ = 0).
   linear the backward of Y = X W^T + s (X A^T) B^T from such a checkpoint:
              V = dY B,  dX = dY W + s V A,  dA = s V^T X^,  dB = s dY^T U
          with U = X A^T as the forward saved it, or X^ A^T recomputed.
@@ -134,20 +134,19 @@ def _activations(g, M, K):
 
 
 def _checkpoint(x, fmt):
-    """(stored codes, absmax): the definition at the top of this file."""
-    top = 127.0 if fmt == "int8" else 256.0
+    """(stored codes, steps): the definition at the top of this file."""
     v = x.float().view(x.shape[0], -1, BLOCK)
-    absmax = v.abs().amax(2, keepdim=True)
-    q = v * top / torch.where(absmax > 0, absmax, torch.ones_like(absmax))
+    step = (v.abs().amax(2) / (127.0 if fmt == "int8" else 256.0)).to(torch.bfloat16)
+    d = step.float().unsqueeze(2)
+    q = v / torch.where(d > 0, d, torch.ones_like(d))
     q = torch.round(q).to(torch.int8) if fmt == "int8" else q.to(torch.float8_e4m3fn)
-    return q.view(torch.uint8).view(x.shape), absmax.squeeze(2).to(torch.bfloat16)
+    return q.view(torch.uint8).view(x.shape), step
 
 
-def _checkpoint_values(codes, absmax, fmt, dtype=torch.float32):
-    """The bf16 values that a checkpoint stands for, in `dtype`."""
-    q = codes.view(torch.int8 if fmt == "int8" else torch.float8_e4m3fn).to(dtype).view(codes.shape[0], -1, BLOCK)
-    v = q * absmax.to(dtype).unsqueeze(2) / (127.0 if fmt == "int8" else 256.0)
-    return v.to(torch.bfloat16).to(dtype).view(codes.shape)
+def _checkpoint_values(codes, step, fmt):
+    """The bf16 values that a checkpoint stands for, in 32 bits."""
+    q = codes.view(torch.int8 if fmt == "int8" else torch.float8_e4m3fn).float().view(codes.shape[0], -1, BLOCK)
+    return (q * step.float().unsqueeze(2)).to(torch.bfloat16).float().view(codes.shape)
 
 
 def prepare(case, seed):
@@ -165,7 +164,7 @@ def prepare(case, seed):
         s["A"], s["B"] = _randn(g, r, K, std=0.02), _randn(g, N, r, std=0.02)
         x = _activations(g, M, K)
         s["dy"] = _randn(g, M, N)
-        s["codes"], s["absmax"] = _checkpoint(x, case["fmt"])
+        s["codes"], s["step"] = _checkpoint(x, case["fmt"])
         s["u"] = x.float() @ s["A"].float().t() if case["saved_u"] else None
         s["scale"] = 32.0 / r
     elif op in ("norm_fwd", "norm_bwd"):
@@ -292,10 +291,10 @@ def _plain(s):
     c = s["case"]
     op = c["op"]
     if op == "ckpt":
-        codes, absmax = _checkpoint(s["x"], c["fmt"])
-        return {"values": _checkpoint_values(codes, absmax, c["fmt"]).to(torch.bfloat16), "absmax": absmax}
+        codes, step = _checkpoint(s["x"], c["fmt"])
+        return {"values": _checkpoint_values(codes, step, c["fmt"]).to(torch.bfloat16), "step": step}
     if op == "linear":
-        x = _checkpoint_values(s["codes"], s["absmax"], c["fmt"])
+        x = _checkpoint_values(s["codes"], s["step"], c["fmt"])
         dy, A, B = s["dy"].float(), s["A"].float(), s["B"].float()
         u = s["u"] if s["u"] is not None else x @ A.t()
         v = dy @ B
@@ -309,7 +308,7 @@ def _plain(s):
         if c["post"]:
             out["rstd_post"] = rstd_post
         if c["ckpt"]:
-            codes, out["absmax"] = _checkpoint(out["x"], "e4m3")
+            codes, out["step"] = _checkpoint(out["x"], "e4m3")
             out["codes"] = codes.view(torch.float8_e4m3fn)
         return out
     if op == "norm_bwd":
@@ -341,7 +340,7 @@ def _buffers(s):
     elif op == "linear":
         M, N, K, r = (c[k] for k in ("M", "N", "K", "r"))
         b["w"] = q.NF4Weight(N, K, s["packed"], s["qscale"], s["c2"], s["mu"])
-        b["act"] = q.Act8(M, K, s["codes"], s["absmax"], fmt)
+        b["act"] = q.Act8(M, K, s["codes"], s["step"], fmt)
         b["ws"] = torch.empty(q.qlora_linear_ws_bytes(M, N, K, r), dtype=torch.uint8, device=DEVICE)
         q.qlora_workspace_reset(b["ws"])
         b["dX"] = torch.empty((M, K), dtype=torch.bfloat16, device=DEVICE) if c["dx"] else None
@@ -379,7 +378,7 @@ def _own(s):
     if op == "ckpt":
         q.qlora_act8_quantize(s["x"], b["act"])
         q.qlora_act8_dequantize(b["act"], b["values"])
-        return {"values": b["values"], "absmax": b["act"].absmax.view(c["M"], -1)}
+        return {"values": b["values"], "step": b["act"].step.view(c["M"], -1)}
     if op == "linear":
         q.qlora_linear_bwd_act8(b["w"], b["act"], s["dy"], s["A"], s["B"], c["r"], s["scale"], b["dX"], 0, b["dA"],
                                 b["dB"], b["ws"], U=s["u"])
@@ -389,7 +388,7 @@ def _own(s):
                                   b["h_out"], b["x"], b["act"], b["rstd_post"], b["rstd_pre"])
         out = {k: b[k] for k in ("h_out", "x", "rstd_pre") + (("rstd_post",) if c["post"] else ())}
         if c["ckpt"]:
-            out["absmax"] = b["act"].absmax.view(c["M"], -1)
+            out["step"] = b["act"].step.view(c["M"], -1)
             out["codes"] = b["act"].codes.view(torch.float8_e4m3fn).view(c["M"], -1)
         return out
     if op == "norm_bwd":
@@ -454,22 +453,22 @@ def _exact_bf16(v):
 
 
 def _exact_codes(x, fmt):
-    """(code values, absmax) of rows x in 64 bits."""
+    """(code values, steps) of the rows' blocks in 64 bits."""
     v = x.double().reshape(-1, BLOCK)
-    absmax = v.abs().max(1, keepdim=True).values
-    q = v * (127.0 if fmt == "int8" else 256.0) / absmax.clamp(min=1e-300)
+    step = _exact_bf16(v.abs().max(1, keepdim=True).values / (127.0 if fmt == "int8" else 256.0))
+    q = torch.nan_to_num(v / step, nan=0.0)  # 0 / 0 in a block of zeros
     if fmt == "int8":
-        return torch.round(q), absmax
+        return torch.round(q), step
     _, e = torch.frexp(q)
     unit = torch.ldexp(torch.ones_like(q), e.clamp(min=-5) - 4)  # 4 significant bits, down to 2^-9
-    return torch.round(q / unit) * unit, absmax
+    return torch.round(q / unit) * unit, step
 
 
 def _exact_linear(s, c):
     N, K, r = c["N"], c["K"], c["r"]
     M = c["M"]
     q = s["codes"].view(torch.int8 if c["fmt"] == "int8" else torch.float8_e4m3fn).double().view(-1, BLOCK)
-    x = _exact_bf16(q * s["absmax"].double().view(-1, 1) / (127.0 if c["fmt"] == "int8" else 256.0)).view(M, K)
+    x = _exact_bf16(q * s["step"].double().view(-1, 1)).view(M, K)
     A, B, dy = s["A"].double(), s["B"].double(), s["dy"].double()
     v = dy.matmul(B)
     u = s["u"].double() if s["u"] is not None else x.matmul(A.t())
@@ -499,8 +498,8 @@ def _exact_norm_forward(s, c):
     out["rstd_pre"] = (total.square().sum(1) / D + s["eps"]).rsqrt()
     out["x"] = torch.einsum("md,m,d->md", total, out["rstd_pre"], s["w_pre"].double())
     if c["ckpt"]:
-        q, absmax = _exact_codes(_exact_bf16(out["x"]), "e4m3")
-        out["codes"], out["absmax"] = q.view(c["M"], D), absmax.view(c["M"], -1)
+        q, step = _exact_codes(_exact_bf16(out["x"]), "e4m3")
+        out["codes"], out["step"] = q.view(c["M"], D), step.view(c["M"], -1)
     return out
 
 
@@ -562,9 +561,8 @@ def exact(case, seed):
     s, c = prepare(case, seed), dict(case)
     op = c["op"]
     if op == "ckpt":
-        q, absmax = _exact_codes(s["x"], c["fmt"])
-        values = _exact_bf16(q * absmax / (127.0 if c["fmt"] == "int8" else 256.0))
-        return {"values": values.view(c["M"], c["K"]), "absmax": absmax.view(c["M"], -1)}
+        q, step = _exact_codes(s["x"], c["fmt"])
+        return {"values": _exact_bf16(q * step).view(c["M"], c["K"]), "step": step.view(c["M"], -1)}
     if op == "linear":
         return _exact_linear(s, c)
     if op == "norm_fwd":
