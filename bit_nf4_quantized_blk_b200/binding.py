@@ -53,6 +53,9 @@ EXPORTED = [
     "qlora_selftest_mbarrier_ring",
     "qlora_selftest_checks",
     "qlora_linear_bwd",
+    "qlora_act8_quantize",
+    "qlora_act8_dequantize",
+    "qlora_linear_bwd_act8",
     "qlora_timing_enable",
     "qlora_timing_read",
 ]
@@ -69,6 +72,7 @@ CODEBOOK_NF4, CODEBOOK_FP4 = 0, 1
 SCALES_DQ_INT8, SCALES_DQ_FP8, SCALES_FP32 = 0, 1, 2
 INPUT_FP32, INPUT_BF16, INPUT_FP16 = 0, 1, 2
 WEIGHT_PATH_FUSED, WEIGHT_PATH_DENSE = 0, 1  # qlora_weight_path
+ACT8_INT8, ACT8_E4M3 = 0, 1  # qlora_act8_format
 _INPUT_OF_DTYPE = {torch.float32: INPUT_FP32, torch.bfloat16: INPUT_BF16, torch.float16: INPUT_FP16}
 
 
@@ -83,6 +87,16 @@ class QloraNf4WeightC(ctypes.Structure):
         ("codebook", ctypes.c_int32),
         ("scale_format", ctypes.c_int32),
         ("absmax", ctypes.c_void_p),
+    ]
+
+
+class QloraAct8C(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("step", ctypes.c_void_p),
+        ("format", ctypes.c_int32),
     ]
 
 
@@ -102,6 +116,7 @@ def lib() -> ctypes.CDLL:
     P = ctypes.c_void_p
     i32, i64, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     W = ctypes.POINTER(QloraNf4WeightC)
+    C8 = ctypes.POINTER(QloraAct8C)
     sig = {
         "qlora_status_string": (ctypes.c_char_p, [i32]),
         "qlora_nf4_sizes": (i32, [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz),
@@ -125,6 +140,9 @@ def lib() -> ctypes.CDLL:
         "qlora_selftest_mbarrier_ring": (i32, [i32, i32, i32, i32, P, P]),
         "qlora_selftest_checks": (i32, [P, P]),
         "qlora_linear_bwd": (i32, [W, P, P, i64, P, P, i32, f32, P, P, i32, P, P, P, sz, P]),
+        "qlora_act8_quantize": (i32, [P, C8, P]),
+        "qlora_act8_dequantize": (i32, [C8, P, P]),
+        "qlora_linear_bwd_act8": (i32, [W, C8, P, P, P, i32, f32, P, P, i32, P, P, P, sz, P]),
         "qlora_timing_enable": (i32, [i32]),
         "qlora_timing_read": (i32, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]),
     }
@@ -246,6 +264,43 @@ class NF4Weight:
             self.codebook,
             self.scale_format,
             _dev_opt(self.absmax, "absmax", _F32, blocks),
+        )
+
+
+_CODES = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+
+
+@dataclass
+class Act8:
+    """Device buffers of one 8-bit activation checkpoint (caller-owned torch tensors)."""
+
+    rows: int
+    cols: int
+    codes: torch.Tensor  # uint8 [rows*cols] (int8 or E4M3 codes)
+    step: torch.Tensor  # bf16 [rows*cols/64]
+    fmt: int = ACT8_INT8
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda", fmt: int = ACT8_INT8) -> "Act8":
+        if rows < 1 or cols < 64 or cols % 64:
+            raise ValueError(f"a checkpoint is [rows >= 1, cols a positive multiple of 64], got [{rows}, {cols}]")
+        return cls(rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                   torch.empty((rows, cols // 64), dtype=torch.bfloat16, device=device), fmt)
+
+    @property
+    def numel(self) -> int | None:
+        """rows * cols, or None when the shape is one the library refuses."""
+        ok = self.rows >= 1 and self.cols >= 64 and self.cols % 64 == 0
+        return self.rows * self.cols if ok else None
+
+    def c_struct(self) -> QloraAct8C:
+        n = self.numel
+        return QloraAct8C(
+            self.rows,
+            self.cols,
+            _dev(self.codes, "codes", _CODES, n),
+            _dev(self.step, "step", _BF16_BITS, None if n is None else n // 64),
+            self.fmt,
         )
 
 
@@ -478,6 +533,38 @@ def qlora_linear_bwd(w: NF4Weight, X, dY, A, B, r: int, scale: float, dX, accumu
     _check("qlora_linear_bwd",
            lib().qlora_linear_bwd(ctypes.byref(st), xp, gp, M, ap, bp, r, float(scale), up, dxp, int(accumulate), dap,
                                   dbp, wsp, wsb, _stream(stream)))
+
+
+def qlora_act8_quantize(X, out: Act8, stream=None) -> None:
+    st = out.c_struct()
+    xp = _dev(X, "X", _BF16_BITS, out.numel)
+    _check("qlora_act8_quantize", lib().qlora_act8_quantize(xp, ctypes.byref(st), _stream(stream)))
+
+
+def qlora_act8_dequantize(a: Act8, X, stream=None) -> None:
+    st = a.c_struct()
+    xp = _dev(X, "X", _BF16_BITS, a.numel)
+    _check("qlora_act8_dequantize", lib().qlora_act8_dequantize(ctypes.byref(st), xp, _stream(stream)))
+
+
+def qlora_linear_bwd_act8(w: NF4Weight, X: Act8, dY, A, B, r: int, scale: float, dX, accumulate: int, dA, dB, ws,
+                          U=None, stream=None) -> None:
+    """qlora_linear_bwd with X an 8-bit checkpoint."""
+    st, sx = w.c_struct(), X.c_struct()
+    M, N, K = X.rows, w.rows, w.cols
+    known = w.numel is not None and M >= 1
+    sized = known and _rank_ok(r)
+    gp = _dev(dY, "dY", _BF16_BITS, M * N if known else None)
+    ap = _dev(A, "A", _BF16_BITS, r * K if sized else None)
+    bp = _dev(B, "B", _BF16_BITS, N * r if sized else None)
+    up = _dev_opt(U, "U", _F32, M * r if sized else None)
+    dxp = _dev_opt(dX, "dX", _BF16_BITS, M * K if known else None)
+    dap = _dev_opt(dA, "dA", _F32, r * K if sized else None)
+    dbp = _dev_opt(dB, "dB", _F32, N * r if sized else None)
+    wsp, wsb = _ws(ws)
+    _check("qlora_linear_bwd_act8",
+           lib().qlora_linear_bwd_act8(ctypes.byref(st), ctypes.byref(sx), gp, ap, bp, r, float(scale), up, dxp,
+                                       int(accumulate), dap, dbp, wsp, wsb, _stream(stream)))
 
 
 def qlora_timing_enable(enable: bool) -> None:

@@ -192,8 +192,8 @@ const Nf4DecisionTable* decision_table(int codebook) {
 // Kernel timing (instrumentation): CUDA events around each launch family.
 // ---------------------------------------------------------------------------
 
-enum Family { kFamQuant, kFamDequant, kFamGemv, kFamSide, kFamGemm, kFamMerge, kFamCount };
-const char* const kFamNames[kFamCount] = {"quantize", "dequant", "gemv", "side", "gemm", "merge"};
+enum Family { kFamQuant, kFamDequant, kFamGemv, kFamSide, kFamGemm, kFamMerge, kFamAct8, kFamCount };
+const char* const kFamNames[kFamCount] = {"quantize", "dequant", "gemv", "side", "gemm", "merge", "act8"};
 
 // Shared by every host thread: `mu` guards the event pool and the records.
 struct TimingState {
@@ -370,7 +370,7 @@ LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
   l.vlo = take(mr * 2);
   l.bpad = take(static_cast<size_t>(N) * kRankPad * 2);
   const size_t p1 = colsum_partial_bytes(M, N), p2 = colsum_partial_bytes(M, K);
-  l.part = take(p1 > p2 ? p1 : p2);
+  l.part = take(std::max({p1, p2, act8_colsum_partial_bytes(M, K)}));
   const size_t s1 = skinny_partial_bytes(M, N), s2 = skinny_partial_bytes(M, K);
   l.skpart = take(s1 > s2 ? s1 : s2);
   // The tensor-core V / dB pass: its partials and the transposed B and U split.
@@ -429,6 +429,16 @@ qlora_status check_linear_shape(int64_t M, int64_t N, int64_t K, int32_t r) {
     return QLORA_ERR_UNSUPPORTED;
   return QLORA_OK;
 }
+
+qlora_status check_act8(const qlora_act8* a) {
+  if (a == nullptr || a->rows < 1 || a->cols < kBlock || a->cols % kBlock != 0) return QLORA_ERR_INVALID_ARG;
+  if (a->rows > (int64_t{1} << 40) / a->cols) return QLORA_ERR_UNSUPPORTED;
+  if (a->format != QLORA_ACT8_INT8 && a->format != QLORA_ACT8_E4M3) return QLORA_ERR_INVALID_ARG;
+  if (!a->codes || !a->step) return QLORA_ERR_INVALID_ARG;
+  return aligned(a->codes, 16) && aligned(a->step, 2) ? QLORA_OK : QLORA_ERR_ALIGNMENT;
+}
+
+Act8View view_of(const qlora_act8* a) { return Act8View{a->codes, a->step, a->rows, a->cols, a->format}; }
 
 // Weight path of the tensor-core linear calls (process-wide, read once per call).
 std::atomic<int> g_weight_path{QLORA_WEIGHT_PATH_FUSED};
@@ -857,16 +867,20 @@ extern "C" qlora_status qlora_selftest_checks(int32_t* d_result, void* stream) {
   return from_cuda(launch_checks_selftest(d_result, static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const uint16_t* dY, int64_t M,
-                                         const uint16_t* A, const uint16_t* B, int32_t r, float scale, const float* U,
-                                         uint16_t* dX, int32_t accumulate, float* dA, float* dB, void* ws,
-                                         size_t ws_bytes, void* stream) {
+namespace {
+
+// The backward from the layer's input X, given as bf16 (x8 null) or as an
+// 8-bit checkpoint (X null; checked by the caller).
+qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlora_act8* x8, const uint16_t* dY,
+                        int64_t M, const uint16_t* A, const uint16_t* B, int32_t r, float scale, const float* U,
+                        uint16_t* dX, int32_t accumulate, float* dA, float* dB, void* ws, size_t ws_bytes,
+                        void* stream) {
   const bool dense = dense_weight_path();
   qlora_status st = check_linear_args(w, M, r, ws_bytes, ws, dense);
   if (st != QLORA_OK) return st;
-  if (!X || !dY || !A || !B) return QLORA_ERR_INVALID_ARG;
+  if ((!X && !x8) || !dY || !A || !B) return QLORA_ERR_INVALID_ARG;
   if (accumulate != 0 && accumulate != 1) return QLORA_ERR_INVALID_ARG;
-  if (!aligned(X, 16) || !aligned(dY, 16) || !aligned(A, 16) || !aligned(B, 2) || (dX && !aligned(dX, 16)) ||
+  if ((X && !aligned(X, 16)) || !aligned(dY, 16) || !aligned(A, 16) || !aligned(B, 2) || (dX && !aligned(dX, 16)) ||
       (dA && !aligned(dA, 4)) || (dB && !aligned(dB, 4)) || (U && !aligned(U, 4)))
     return QLORA_ERR_ALIGNMENT;
   if (!std::isfinite(scale)) return QLORA_ERR_INVALID_ARG;
@@ -899,6 +913,7 @@ extern "C" qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const uint16
     uo.olo = at<uint16_t>(ws, lay.ulo);
     uo.scale = 1.0f;
     Timed tm(kFamSide, s, 2);
+    if (x8 != nullptr) return launch_act8_skinny(view_of(x8), A, r, at<float>(ws, lay.skpart), uo, s);
     return launch_skinny(X, M, K, A, true, r, 0, at<float>(ws, lay.skpart), uo, status, s);
   };
   BlockScalesJob bs{};  // the dX GEMM's block scales, when a kernel before it carries them
@@ -976,13 +991,63 @@ extern "C" qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const uint16
   if (dA != nullptr) {  // dA = s V^T X
     {
       Timed tm(kFamSide, s, 2);
-      e = launch_colsum(X, M, K, at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
-                        at<float>(ws, lay.part), dA, true, status, s);
+      if (x8 != nullptr)
+        e = launch_act8_colsum(view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
+                               at<float>(ws, lay.part), dA, s);
+      else
+        e = launch_colsum(X, M, K, at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
+                          at<float>(ws, lay.part), dA, true, status, s);
     }
     if (e != cudaSuccess) return from_cuda(e);
   }
   return QLORA_OK;
 }
+
+}  // namespace
+
+extern "C" qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const uint16_t* dY, int64_t M,
+                                         const uint16_t* A, const uint16_t* B, int32_t r, float scale, const float* U,
+                                         uint16_t* dX, int32_t accumulate, float* dA, float* dB, void* ws,
+                                         size_t ws_bytes, void* stream) {
+  return linear_bwd(w, X, nullptr, dY, M, A, B, r, scale, U, dX, accumulate, dA, dB, ws, ws_bytes, stream);
+}
+
+extern "C" qlora_status qlora_linear_bwd_act8(const qlora_nf4_weight* w, const qlora_act8* X, const uint16_t* dY,
+                                              const uint16_t* A, const uint16_t* B, int32_t r, float scale,
+                                              const float* U, uint16_t* dX, int32_t accumulate, float* dA, float* dB,
+                                              void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_act8(X);
+  if (st != QLORA_OK) return st;
+  st = check_weight(w);
+  if (st != QLORA_OK) return st;
+  if (X->cols != w->cols) return QLORA_ERR_INVALID_ARG;
+  return linear_bwd(w, nullptr, X, dY, X->rows, A, B, r, scale, U, dX, accumulate, dA, dB, ws, ws_bytes, stream);
+}
+
+extern "C" qlora_status qlora_act8_quantize(const uint16_t* X, const qlora_act8* out, void* stream) {
+  qlora_status st = check_act8(out);
+  if (st != QLORA_OK) return st;
+  if (X == nullptr) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(X, 16)) return QLORA_ERR_ALIGNMENT;
+  st = check_device();
+  if (st != QLORA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(kFamAct8, s);
+  return from_cuda(launch_act8_quantize(X, out->rows * out->cols, out->format, out->codes, out->step, s));
+}
+
+extern "C" qlora_status qlora_act8_dequantize(const qlora_act8* a, uint16_t* X, void* stream) {
+  qlora_status st = check_act8(a);
+  if (st != QLORA_OK) return st;
+  if (X == nullptr) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(X, 16)) return QLORA_ERR_ALIGNMENT;
+  st = check_device();
+  if (st != QLORA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(kFamAct8, s);
+  return from_cuda(launch_act8_dequantize(view_of(a), X, s));
+}
+
 
 extern "C" qlora_status qlora_timing_enable(int32_t enable) {
   TimingState& T = timing();

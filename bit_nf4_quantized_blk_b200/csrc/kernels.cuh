@@ -186,6 +186,9 @@ int skinny_splits(int64_t M, int64_t C);
 size_t skinny_partial_bytes(int64_t M, int64_t C);
 cudaError_t launch_skinny(const uint16_t* In, int64_t M, int64_t C, const uint16_t* Wt, bool wt_is_rc, int r,
                           int64_t ldw, float* part, const SkinnyOut& out, int* status, cudaStream_t stream);
+// The reduction of launch_skinny's split partials alone ([splits][M][64] in `part`).
+cudaError_t launch_skinny_finalize(const float* part, int64_t M, int r, int splits, const SkinnyOut& out,
+                                   cudaStream_t stream);
 // hi/lo bf16 split of a compact fp32 [M][r] matrix into [M][64] buffers.
 cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, cudaStream_t stream);
 
@@ -230,6 +233,30 @@ cudaError_t launch_vdb_finalize(const float* vpart, int ncb, const float* dbpart
 // the transposed source [r][rows].
 cudaError_t launch_pad_rank(const uint16_t* src, bool src_transposed, int64_t rows, int r, uint16_t* dst,
                             cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// 8-bit activation checkpoints (act8.cu; the rounding rules in act8.cuh)
+// ---------------------------------------------------------------------------
+
+struct Act8View {
+  const uint8_t* codes;  // [rows][cols]
+  const uint16_t* step;  // [rows][cols / 64] bf16
+  int64_t rows, cols;
+  int format;            // QLORA_ACT8_*
+};
+
+cudaError_t launch_act8_quantize(const uint16_t* X, int64_t n, int format, uint8_t* codes, uint16_t* step,
+                                 cudaStream_t stream);
+cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t stream);
+// dst [r][K] = scale sum_m (hi[m][j] + lo[m][j]) X^[m][k]; `part` is scratch of
+// act8_colsum_partial_bytes(M, K) (enough for every rank).
+size_t act8_colsum_partial_bytes(int64_t M, int64_t K);
+cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, int r, float scale,
+                               float* part, float* dst, cudaStream_t stream);
+// launch_skinny's product X^ A^T from a checkpoint (A [r][K] bf16, 8-byte
+// aligned rows); `part` as for launch_skinny.
+cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, const SkinnyOut& out,
+                               cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // tcgen05 GEMM (gemm_tc.cu):  D[M][N] (+)= A[M][K] B[N][K]^T + A2[M][64] B2[N][64]^T

@@ -286,6 +286,11 @@ cudaError_t launch_skinny(const uint16_t* In, int64_t M, int64_t C, const uint16
                   : launch_skinny_nt<false, 8>(tin, tw, M, C, splits, part, status, stream);
   }
   if (e != cudaSuccess) return e;
+  return launch_skinny_finalize(part, M, r, splits, out, stream);
+}
+
+cudaError_t launch_skinny_finalize(const float* part, int64_t M, int r, int splits, const SkinnyOut& out,
+                                   cudaStream_t stream) {
   const int64_t total = M * (kRankPad / 2) + (out.bs.out != nullptr ? out.bs.groups : 0);
   skinny_finalize_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(part, M, r, splits, out);
   return cudaGetLastError();

@@ -403,12 +403,60 @@ qlora_status qlora_linear_bwd(const qlora_nf4_weight *w, const uint16_t *X, cons
                               void *stream);
 
 /*
+ * 8-bit activation checkpoint: the input X of a linear layer as it is kept
+ * between forward and backward, at 1.03 bytes per value instead of 2.  (The
+ * pages keep activations in 16 bits; "QLoRA: NF4 storage, gradients and local
+ * integration", section "Memory accounting before optimization", counts them
+ * among what grows with the sequence.)
+ * Storage, per block of 64 consecutive values of a row with absolute maximum a:
+ *   INT8 : step = bf16(a / 127), code = round(x / step) in [-127, 127]
+ *   E4M3 : step = bf16(a / 256), code = E4M3(x / step), saturating
+ * and the block stands for bf16(code * step); every rounding is to nearest
+ * even; x = -0 has code 0.  A block of zeros has step 0.  A block that holds a NaN or an infinity
+ * gets a NaN step: all of it stands for NaN.  (INT8: the step is at most 2^121,
+ * so that 127 steps stay finite, and codes beyond 127 are cut to it.)
+ *   rows, cols : X is [rows, cols] row-major; cols a multiple of 64.
+ *   codes      : rows*cols bytes, int8 or E4M3 bit patterns; 16-byte aligned.
+ *   step       : rows*cols/64 bf16; 2-byte aligned.
+ *   format     : qlora_act8_format.
+ */
+typedef enum qlora_act8_format { QLORA_ACT8_INT8 = 0, QLORA_ACT8_E4M3 = 1 } qlora_act8_format;
+typedef struct qlora_act8 {
+  int64_t rows;
+  int64_t cols;
+  uint8_t *codes;
+  uint16_t *step;
+  int32_t format;
+} qlora_act8;
+
+/*
+ * Write a checkpoint of X, bf16 [out->rows, out->cols] (16-byte aligned), and
+ * read one back as bf16 values.  Exact to the definition above, bit for bit.
+ * No workspace.
+ */
+qlora_status qlora_act8_quantize(const uint16_t *X, const qlora_act8 *out, void *stream);
+qlora_status qlora_act8_dequantize(const qlora_act8 *a, uint16_t *X, void *stream);
+
+/*
+ * LoRA linear backward from an 8-bit checkpoint of X: qlora_linear_bwd with X
+ * the checkpoint's values (rows = M tokens, cols = K).  The codes feed dA (and
+ * U, when U is NULL) directly; no bf16 copy of X is made.  dX takes no part of
+ * the checkpoint's rounding; dB only through a recomputed U.  All other
+ * arguments, the workspace and the errors are those of qlora_linear_bwd;
+ * X->cols other than w->cols is INVALID_ARG.
+ */
+qlora_status qlora_linear_bwd_act8(const qlora_nf4_weight *w, const qlora_act8 *X, const uint16_t *dY,
+                                   const uint16_t *A, const uint16_t *B, int32_t r, float scale, const float *U,
+                                   uint16_t *dX, int32_t accumulate, float *dA, float *dB, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/*
  * Kernel timing (instrumentation for benchmarks; off by default).
  * While enabled, every kernel the library enqueues is bracketed by CUDA
  * events recorded on the launching stream, grouped by family:
  *   "quantize" (quantize + double quant), "dequant", "gemv", "side" (rank-r
  *   products, gradient column sums, padding), "gemm" (tensor-core GEMM),
- *   "merge" (qlora_merge).
+ *   "merge" (qlora_merge), "act8" (activation checkpoints written and read back).
  *   qlora_timing_enable : 1 starts recording (clearing earlier records), 0 stops.
  *   qlora_timing_read   : waits for the recorded events of `family` and returns
  *                         the summed device time in milliseconds and the number

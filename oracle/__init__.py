@@ -22,6 +22,7 @@ What it computes, and where each step comes from (page titles, sections):
   gradient paragraph closing "Exact CPU teaching quantizer and adapter
   gradient path"); "FT-02: QLoRA -- Fine-Tuning with Quantization"
   (section "4. The LoRA mechanics the API wraps").
+* ``oracle.act8`` -- 8-bit activation checkpoints (the library's own format).
 * ``oracle.accounting`` -- bits per weight and storage bytes of the packed
   state, adapter parameter counts.
 
