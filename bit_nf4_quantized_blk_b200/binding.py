@@ -56,6 +56,9 @@ EXPORTED = [
     "qlora_act8_quantize",
     "qlora_act8_dequantize",
     "qlora_linear_bwd_act8",
+    "qlora_residual_norm_fwd",
+    "qlora_residual_norm_ws_bytes",
+    "qlora_residual_norm_bwd",
     "qlora_timing_enable",
     "qlora_timing_read",
 ]
@@ -143,6 +146,9 @@ def lib() -> ctypes.CDLL:
         "qlora_act8_quantize": (i32, [P, C8, P]),
         "qlora_act8_dequantize": (i32, [C8, P, P]),
         "qlora_linear_bwd_act8": (i32, [W, C8, P, P, P, i32, f32, P, P, i32, P, P, P, sz, P]),
+        "qlora_residual_norm_fwd": (i32, [P, P, P, P, f32, P, f32, i64, i64, i32, P, P, C8, P, P, P]),
+        "qlora_residual_norm_ws_bytes": (sz, [i64, i64]),
+        "qlora_residual_norm_bwd": (i32, [P, P, P, P, P, P, f32, P, P, P, i64, i64, i32, P, P, P, P, P, P, sz, P]),
         "qlora_timing_enable": (i32, [i32]),
         "qlora_timing_read": (i32, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]),
     }
@@ -565,6 +571,68 @@ def qlora_linear_bwd_act8(w: NF4Weight, X: Act8, dY, A, B, r: int, scale: float,
     _check("qlora_linear_bwd_act8",
            lib().qlora_linear_bwd_act8(ctypes.byref(st), ctypes.byref(sx), gp, ap, bp, r, float(scale), up, dxp,
                                        int(accumulate), dap, dbp, wsp, wsb, _stream(stream)))
+
+
+def _stream_shape(t, name: str) -> tuple[int, int, int]:
+    """(M, D, res_dtype) of a residual-stream tensor [M, D]."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D [M, D] tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    return t.shape[0], t.shape[1], 0 if t.dtype == torch.bfloat16 else 1
+
+
+def qlora_residual_norm_fwd(h, y, w_post, gate, scale: float, w_pre, eps: float, h_out, x, ckpt, rstd_post, rstd_pre,
+                            stream=None) -> None:
+    """h [M, D] bf16 or fp32 (h_out of the same dtype); y, w_post, gate, w_pre and every output may be None as the
+    header says."""
+    M, D, res = _stream_shape(h, "h")
+    n, rd = M * D, (h.dtype,)
+    hp = _dev(h, "h")
+    yp = _dev_opt(y, "y", _BF16_BITS, n)
+    wpp = _dev_opt(w_post, "w_post", _F32, D)
+    gp = _dev_opt(gate, "gate", _F32, D)
+    wrp = _dev_opt(w_pre, "w_pre", _F32, D)
+    hop = _dev_opt(h_out, "h_out", rd, n)
+    xp = _dev_opt(x, "x", _BF16_BITS, n)
+    cp = None if ckpt is None else ctypes.byref(ckpt.c_struct())
+    rpp = _dev_opt(rstd_post, "rstd_post", _F32, M)
+    rrp = _dev_opt(rstd_pre, "rstd_pre", _F32, M)
+    _check("qlora_residual_norm_fwd",
+           lib().qlora_residual_norm_fwd(hp, yp, wpp, gp, float(scale), wrp, float(eps), M, D, res, hop, xp, cp, rpp,
+                                         rrp, _stream(stream)))
+
+
+def qlora_residual_norm_ws_bytes(M: int, D: int) -> int:
+    return int(lib().qlora_residual_norm_ws_bytes(M, D))
+
+
+def qlora_residual_norm_bwd(dh_out, dx, h_out, y, w_post, gate, scale: float, w_pre, rstd_post, rstd_pre, dh, dy,
+                            dw_post, dgate, dw_pre, ws, stream=None) -> None:
+    """dh_out, h_out and dh share one dtype (bf16 or fp32); arguments may be None as the header says."""
+    shaped = next(((t, k) for t, k in ((dh_out, "dh_out"), (h_out, "h_out"), (dh, "dh")) if t is not None), None)
+    if shaped is None:
+        raise ValueError("one of dh_out, h_out and dh gives the shape")
+    M, D, res = _stream_shape(*shaped)
+    n, rd = M * D, (shaped[0].dtype,)
+    dhop = _dev_opt(dh_out, "dh_out", rd, n)
+    dxp = _dev_opt(dx, "dx", _BF16_BITS, n)
+    hp = _dev_opt(h_out, "h_out", rd, n)
+    yp = _dev_opt(y, "y", _BF16_BITS, n)
+    wpp = _dev_opt(w_post, "w_post", _F32, D)
+    gp = _dev_opt(gate, "gate", _F32, D)
+    wrp = _dev_opt(w_pre, "w_pre", _F32, D)
+    rpp = _dev_opt(rstd_post, "rstd_post", _F32, M)
+    rrp = _dev_opt(rstd_pre, "rstd_pre", _F32, M)
+    dhp = _dev_opt(dh, "dh", rd, n)
+    dyp = _dev_opt(dy, "dy", _BF16_BITS, n)
+    dwp = _dev_opt(dw_post, "dw_post", _F32, D)
+    dgp = _dev_opt(dgate, "dgate", _F32, D)
+    dwr = _dev_opt(dw_pre, "dw_pre", _F32, D)
+    wsp, wsb = (None, 0) if ws is None else _ws(ws)
+    _check("qlora_residual_norm_bwd",
+           lib().qlora_residual_norm_bwd(dhop, dxp, hp, yp, wpp, gp, float(scale), wrp, rpp, rrp, M, D, res, dhp, dyp,
+                                         dwp, dgp, dwr, wsp, wsb, _stream(stream)))
 
 
 def qlora_timing_enable(enable: bool) -> None:

@@ -192,8 +192,8 @@ const Nf4DecisionTable* decision_table(int codebook) {
 // Kernel timing (instrumentation): CUDA events around each launch family.
 // ---------------------------------------------------------------------------
 
-enum Family { kFamQuant, kFamDequant, kFamGemv, kFamSide, kFamGemm, kFamMerge, kFamAct8, kFamCount };
-const char* const kFamNames[kFamCount] = {"quantize", "dequant", "gemv", "side", "gemm", "merge", "act8"};
+enum Family { kFamQuant, kFamDequant, kFamGemv, kFamSide, kFamGemm, kFamMerge, kFamAct8, kFamNorm, kFamCount };
+const char* const kFamNames[kFamCount] = {"quantize", "dequant", "gemv", "side", "gemm", "merge", "act8", "norm"};
 
 // Shared by every host thread: `mu` guards the event pool and the records.
 struct TimingState {
@@ -1048,6 +1048,114 @@ extern "C" qlora_status qlora_act8_dequantize(const qlora_act8* a, uint16_t* X, 
   return from_cuda(launch_act8_dequantize(view_of(a), X, s));
 }
 
+
+namespace {
+
+qlora_status check_norm_shape(int64_t M, int64_t D, int32_t res_dtype) {
+  if (M < 1 || D < kBlock || D % kBlock != 0 || (res_dtype != 0 && res_dtype != 1)) return QLORA_ERR_INVALID_ARG;
+  if (D > kNormMaxD || M > INT32_MAX) return QLORA_ERR_UNSUPPORTED;
+  return QLORA_OK;
+}
+
+}  // namespace
+
+extern "C" qlora_status qlora_residual_norm_fwd(const void* h, const uint16_t* y, const float* w_post,
+                                                const float* gate, float scale, const float* w_pre, float eps,
+                                                int64_t M, int64_t D, int32_t res_dtype, void* h_out, uint16_t* x,
+                                                const qlora_act8* ckpt, float* rstd_post, float* rstd_pre,
+                                                void* stream) {
+  qlora_status st = check_norm_shape(M, D, res_dtype);
+  if (st != QLORA_OK) return st;
+  if (!h || (!h_out && !x) || !std::isfinite(scale) || !std::isfinite(eps) || eps <= 0.0f) return QLORA_ERR_INVALID_ARG;
+  if (!y && (w_post || gate)) return QLORA_ERR_INVALID_ARG;
+  if ((x != nullptr) != (w_pre != nullptr) || (!x && (ckpt || rstd_pre)) || (rstd_post && !w_post))
+    return QLORA_ERR_INVALID_ARG;
+  if (ckpt != nullptr) {
+    st = check_act8(ckpt);
+    if (st != QLORA_OK) return st;
+    if (ckpt->rows != M || ckpt->cols != D) return QLORA_ERR_INVALID_ARG;
+  }
+  if (!aligned(h, 16) || !aligned(y, 16) || !aligned(w_post, 16) || !aligned(gate, 16) || !aligned(w_pre, 16) ||
+      !aligned(h_out, 16) || !aligned(x, 16) || !aligned(rstd_post, 4) || !aligned(rstd_pre, 4))
+    return QLORA_ERR_ALIGNMENT;
+  st = check_device();
+  if (st != QLORA_OK) return st;
+  ResidualNormFwd p{};
+  p.h = h;
+  p.y = y;
+  p.w_post = w_post;
+  p.gate = gate;
+  p.w_pre = w_pre;
+  p.scale = scale;
+  p.eps = eps;
+  p.M = M;
+  p.D = D;
+  p.h_out = h_out;
+  p.x = x;
+  if (ckpt != nullptr) {
+    p.codes = ckpt->codes;
+    p.step = ckpt->step;
+    p.format = ckpt->format;
+  }
+  p.rstd_post = rstd_post;
+  p.rstd_pre = rstd_pre;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(kFamNorm, s);
+  return from_cuda(launch_residual_norm_fwd(p, res_dtype, s));
+}
+
+extern "C" size_t qlora_residual_norm_ws_bytes(int64_t M, int64_t D) {
+  if (check_norm_shape(M, D, 0) != QLORA_OK) return 0;
+  return kWsHeader + 3 * static_cast<size_t>(residual_norm_bwd_ctas(M, D)) * static_cast<size_t>(D) * sizeof(float);
+}
+
+extern "C" qlora_status qlora_residual_norm_bwd(const void* dh_out, const uint16_t* dx, const void* h_out,
+                                                const uint16_t* y, const float* w_post, const float* gate,
+                                                float scale, const float* w_pre, const float* rstd_post,
+                                                const float* rstd_pre, int64_t M, int64_t D, int32_t res_dtype,
+                                                void* dh, uint16_t* dy, float* dw_post, float* dgate, float* dw_pre,
+                                                void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_norm_shape(M, D, res_dtype);
+  if (st != QLORA_OK) return st;
+  if ((!dh_out && !dx) || !std::isfinite(scale)) return QLORA_ERR_INVALID_ARG;
+  if (!dh && !dy && !dw_post && !dgate && !dw_pre) return QLORA_ERR_INVALID_ARG;
+  if (dx ? (!h_out || !w_pre || !rstd_pre) : dw_pre != nullptr) return QLORA_ERR_INVALID_ARG;
+  if (w_post ? !rstd_post : dw_post != nullptr) return QLORA_ERR_INVALID_ARG;
+  if (dgate && !gate) return QLORA_ERR_INVALID_ARG;
+  if (!y && (w_post || dgate)) return QLORA_ERR_INVALID_ARG;
+  const bool sums = dw_post || dgate || dw_pre;
+  if (sums && ws == nullptr) return QLORA_ERR_WORKSPACE;
+  if (!aligned(dh_out, 16) || !aligned(dx, 16) || !aligned(h_out, 16) || !aligned(y, 16) || !aligned(w_post, 16) ||
+      !aligned(gate, 16) || !aligned(w_pre, 16) || !aligned(dh, 16) || !aligned(dy, 16) || !aligned(rstd_post, 4) ||
+      !aligned(rstd_pre, 4) || !aligned(dw_post, 4) || !aligned(dgate, 4) || !aligned(dw_pre, 4) ||
+      (sums && !aligned(ws, 256)))
+    return QLORA_ERR_ALIGNMENT;
+  if (sums && ws_bytes < qlora_residual_norm_ws_bytes(M, D)) return QLORA_ERR_WORKSPACE;
+  st = check_device();
+  if (st != QLORA_OK) return st;
+  ResidualNormBwd p{};
+  p.dh_out = dh_out;
+  p.dx = dx;
+  p.h_out = h_out;
+  p.y = y;
+  p.w_post = w_post;
+  p.gate = gate;
+  p.w_pre = w_pre;
+  p.rstd_post = rstd_post;
+  p.rstd_pre = rstd_pre;
+  p.scale = scale;
+  p.M = M;
+  p.D = D;
+  p.dh = dh;
+  p.dy = dy;
+  p.dw_post = dw_post;
+  p.dgate = dgate;
+  p.dw_pre = dw_pre;
+  p.part = sums ? at<float>(ws, kWsHeader) : nullptr;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(kFamNorm, s, sums ? 2 : 1);
+  return from_cuda(launch_residual_norm_bwd(p, res_dtype, s));
+}
 
 extern "C" qlora_status qlora_timing_enable(int32_t enable) {
   TimingState& T = timing();

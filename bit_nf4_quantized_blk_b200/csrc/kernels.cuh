@@ -259,6 +259,53 @@ cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, floa
                                cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
+// Residual sum between two norms (residual_norm.cu)
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kNormMaxD = 16384;  // longest row the kernels hold in registers
+
+struct ResidualNormFwd {
+  const void* h;         // [M][D] bf16 or fp32
+  const uint16_t* y;     // [M][D] bf16, may be null
+  const float* w_post;   // [D], may be null
+  const float* gate;     // [D], may be null
+  const float* w_pre;    // [D], null exactly when x is
+  float scale, eps;
+  int64_t M, D;
+  void* h_out;           // as h (may be h), may be null
+  uint16_t* x;           // [M][D] bf16, may be null
+  uint8_t* codes;        // checkpoint of x, may be null
+  uint16_t* step;
+  int format;            // QLORA_ACT8_*
+  float* rstd_post;      // [M], may be null
+  float* rstd_pre;       // [M], may be null
+};
+
+struct ResidualNormBwd {
+  const void* dh_out;    // [M][D] bf16 or fp32, may be null
+  const uint16_t* dx;    // [M][D] bf16, may be null
+  const void* h_out;     // as dh_out; read with dx
+  const uint16_t* y;     // read with w_post or dgate
+  const float* w_post;   // may be null
+  const float* gate;     // may be null
+  const float* w_pre;    // read with dx
+  const float* rstd_post;
+  const float* rstd_pre;
+  float scale;
+  int64_t M, D;
+  void* dh;              // as dh_out (may be dh_out), may be null
+  uint16_t* dy;          // may be null
+  float* dw_post;        // [D] each, may be null
+  float* dgate;
+  float* dw_pre;
+  float* part;           // [3][residual_norm_bwd_ctas(M, D)][D]
+};
+
+int residual_norm_bwd_ctas(int64_t M, int64_t D);
+cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cudaStream_t stream);
+cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
 // tcgen05 GEMM (gemm_tc.cu):  D[M][N] (+)= A[M][K] B[N][K]^T + A2[M][64] B2[N][64]^T
 // ---------------------------------------------------------------------------
 struct GemmArgs {

@@ -451,12 +451,63 @@ qlora_status qlora_linear_bwd_act8(const qlora_nf4_weight *w, const qlora_act8 *
                                    size_t ws_bytes, void *stream);
 
 /*
+ * The pass between two blocks of a network: the norm after a block, its gate
+ * and residual scale, the residual sum and the norm before the next block,
+ * whose output x is the next linear call's X.  Per row of D values, with
+ * rstd(v) = 1 / sqrt(mean(v^2) + eps):
+ *     p = y rstd(y) w_post,   v = h + scale * gate * p,
+ *     h_out = round(v),       x = v rstd(v) w_pre
+ * (x takes v before it is rounded to h_out's type).  Parts are left out by NULL:
+ * w_post (p = y), gate (1), y with both (v = h), h_out or x (not both).
+ *   h, h_out  : the residual stream, [M, D] of res_dtype (0 = bf16, 1 = fp32);
+ *               h_out may be h.
+ *   y         : bf16 [M, D], the block's output.
+ *   w_post, gate, w_pre : fp32 [D], 16-byte aligned; w_pre exactly with x.
+ *   x         : bf16 [M, D].
+ *   ckpt      : an 8-bit checkpoint of x as stored ([M, D]), or NULL.
+ *   rstd_post, rstd_pre : fp32 [M] outputs rstd(y) and rstd(v) (keep them for
+ *               the backward), or NULL.
+ * D is a multiple of 64, at most 16384 (UNSUPPORTED beyond); eps > 0.  All
+ * arithmetic is fp32.  No workspace.
+ */
+qlora_status qlora_residual_norm_fwd(const void *h, const uint16_t *y, const float *w_post, const float *gate,
+                                     float scale, const float *w_pre, float eps, int64_t M, int64_t D,
+                                     int32_t res_dtype, void *h_out, uint16_t *x, const qlora_act8 *ckpt,
+                                     float *rstd_post, float *rstd_pre, void *stream);
+
+/*
+ * Its backward, for upstream gradients dh_out of h_out (res_dtype) and dx of x
+ * (bf16; what the linear backward accumulated), either of which may be NULL for
+ * zero.  With n = h_out rstd_pre, m = y rstd_post and p as above:
+ *     g = dh_out + rstd_pre (dx w_pre - n mean(dx w_pre n)),   dh = g,
+ *     dw_pre = sum dx n,   dgate = sum scale g p,
+ *     dp = scale g gate,   dw_post = sum dp m,
+ *     dy = rstd_post (dp w_post - m mean(dp w_post m))     (dy = dp without w_post)
+ * the sums over the M rows.
+ *   dx needs h_out, w_pre and rstd_pre; w_post needs y and rstd_post; dgate
+ *   needs y.  w_post, gate and scale are the forward's.
+ *   dh   : [M, D] of res_dtype, or NULL; may be dh_out.
+ *   dy   : bf16 [M, D], or NULL.
+ *   dw_post, dgate, dw_pre : fp32 [D] outputs (overwritten), each may be NULL.
+ *   ws   : 256-byte aligned, qlora_residual_norm_ws_bytes(M, D) (0 for shapes
+ *          the calls refuse); needed for the [D] outputs only.  Its first 256
+ *          bytes are left alone, so a linear workspace may serve.
+ */
+size_t qlora_residual_norm_ws_bytes(int64_t M, int64_t D);
+qlora_status qlora_residual_norm_bwd(const void *dh_out, const uint16_t *dx, const void *h_out, const uint16_t *y,
+                                     const float *w_post, const float *gate, float scale, const float *w_pre,
+                                     const float *rstd_post, const float *rstd_pre, int64_t M, int64_t D,
+                                     int32_t res_dtype, void *dh, uint16_t *dy, float *dw_post, float *dgate,
+                                     float *dw_pre, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Kernel timing (instrumentation for benchmarks; off by default).
  * While enabled, every kernel the library enqueues is bracketed by CUDA
  * events recorded on the launching stream, grouped by family:
  *   "quantize" (quantize + double quant), "dequant", "gemv", "side" (rank-r
  *   products, gradient column sums, padding), "gemm" (tensor-core GEMM),
- *   "merge" (qlora_merge), "act8" (activation checkpoints written and read back).
+ *   "merge" (qlora_merge), "act8" (activation checkpoints written and read back),
+ *   "norm" (the residual norms).
  *   qlora_timing_enable : 1 starts recording (clearing earlier records), 0 stops.
  *   qlora_timing_read   : waits for the recorded events of `family` and returns
  *                         the summed device time in milliseconds and the number

@@ -23,6 +23,8 @@ What it computes, and where each step comes from (page titles, sections):
   gradient path"); "FT-02: QLoRA -- Fine-Tuning with Quantization"
   (section "4. The LoRA mechanics the API wraps").
 * ``oracle.act8`` -- 8-bit activation checkpoints (the library's own format).
+* ``oracle.blocks`` -- the residual norms and token log probabilities around
+  the linear calls (the library's own operators).
 * ``oracle.accounting`` -- bits per weight and storage bytes of the packed
   state, adapter parameter counts.
 
