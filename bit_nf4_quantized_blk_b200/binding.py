@@ -59,6 +59,8 @@ EXPORTED = [
     "qlora_residual_norm_fwd",
     "qlora_residual_norm_ws_bytes",
     "qlora_residual_norm_bwd",
+    "qlora_token_logprobs_fwd",
+    "qlora_token_logprobs_bwd",
     "qlora_timing_enable",
     "qlora_timing_read",
 ]
@@ -149,6 +151,8 @@ def lib() -> ctypes.CDLL:
         "qlora_residual_norm_fwd": (i32, [P, P, P, P, f32, P, f32, i64, i64, i32, P, P, C8, P, P, P]),
         "qlora_residual_norm_ws_bytes": (sz, [i64, i64]),
         "qlora_residual_norm_bwd": (i32, [P, P, P, P, P, P, f32, P, P, P, i64, i64, i32, P, P, P, P, P, P, sz, P]),
+        "qlora_token_logprobs_fwd": (i32, [P, i32, i64, i64, i64, P, f32, P, P, P, P, i32, P, P, P]),
+        "qlora_token_logprobs_bwd": (i32, [P, i32, i64, i64, i64, P, f32, P, P, P, P, P, P, i64, P]),
         "qlora_timing_enable": (i32, [i32]),
         "qlora_timing_read": (i32, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]),
     }
@@ -633,6 +637,59 @@ def qlora_residual_norm_bwd(dh_out, dx, h_out, y, w_post, gate, scale: float, w_
     _check("qlora_residual_norm_bwd",
            lib().qlora_residual_norm_bwd(dhop, dxp, hp, yp, wpp, gp, float(scale), wrp, rpp, rrp, M, D, res, dhp, dyp,
                                          dwp, dgp, dwr, wsp, wsb, _stream(stream)))
+
+
+_LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _rows(t, name: str) -> tuple[int, int, int, int, int]:
+    """(pointer, dtype code, M, V, row pitch) of a [M, V] tensor whose rows are contiguous; the rows may be
+    further apart than V (a view of a padded tensor)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D [M, V] tensor")
+    if t.dtype not in _LOGITS:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    M, V = t.shape
+    ld = t.stride(0)
+    if M == 1:  # one row: torch leaves the pitch open; any aligned one will do
+        ld = (V + 7) // 8 * 8
+    if (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"{name}: rows must be contiguous and not overlap")
+    _check_placement(t, name)
+    return t.data_ptr(), _LOGITS[t.dtype], M, V, ld
+
+
+def qlora_token_logprobs_fwd(logits, targets, inv_temperature: float, logprob, entropy, row_max, log_sum, k: int,
+                             top_ids, top_logprob, stream=None) -> None:
+    """logits [M, V] bf16 or fp32 (rows may be padded), targets int64 [M]; outputs may be None as the header says."""
+    lp, dtype, M, V, ld = _rows(logits, "logits")
+    tp = _dev_opt(targets, "targets", (torch.int64,), M)
+    outs = [_dev_opt(t, name, _F32, M) for t, name in ((logprob, "logprob"), (entropy, "entropy"),
+                                                       (row_max, "row_max"), (log_sum, "log_sum"))]
+    n = M * k if k > 0 else None
+    ip = _dev_opt(top_ids, "top_ids", (torch.int32,), n)
+    tlp = _dev_opt(top_logprob, "top_logprob", _F32, n)
+    _check("qlora_token_logprobs_fwd",
+           lib().qlora_token_logprobs_fwd(lp, dtype, M, V, ld, tp, float(inv_temperature), *outs, int(k), ip, tlp,
+                                          _stream(stream)))
+
+
+def qlora_token_logprobs_bwd(logits, targets, inv_temperature: float, row_max, log_sum, entropy, g_logprob, g_entropy,
+                             dlogits, stream=None) -> None:
+    """dlogits [M, V] of logits' dtype (rows may be padded; may be logits itself)."""
+    lp, dtype, M, V, ld = _rows(logits, "logits")
+    dp, ddtype, dM, dV, ldd = _rows(dlogits, "dlogits")
+    if (ddtype, dM, dV) != (dtype, M, V):
+        raise ValueError(f"dlogits: {dlogits.dtype} {list(dlogits.shape)}, logits are {logits.dtype} {[M, V]}")
+    tp = _dev_opt(targets, "targets", (torch.int64,), M)
+    ins = [_dev_opt(t, name, _F32, M) for t, name in ((row_max, "row_max"), (log_sum, "log_sum"),
+                                                      (entropy, "entropy"), (g_logprob, "g_logprob"),
+                                                      (g_entropy, "g_entropy"))]
+    _check("qlora_token_logprobs_bwd",
+           lib().qlora_token_logprobs_bwd(lp, dtype, M, V, ld, tp, float(inv_temperature), *ins, dp, ldd,
+                                          _stream(stream)))
 
 
 def qlora_timing_enable(enable: bool) -> None:

@@ -23,7 +23,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqlora_nf4.so")
 
 SOURCES = ["api.cu", "quantize.cu", "dequant.cu", "gemv.cu", "lora_side.cu", "gemm_tc.cu", "gemm_nf4.cu", "merge.cu", "vdb_tc.cu", "selftest.cu",
-           "act8.cu", "residual_norm.cu"]
+           "act8.cu", "residual_norm.cu", "token_logprobs.cu"]
 
 NVCC_FLAGS = [
     "-O3",

@@ -192,8 +192,8 @@ const Nf4DecisionTable* decision_table(int codebook) {
 // Kernel timing (instrumentation): CUDA events around each launch family.
 // ---------------------------------------------------------------------------
 
-enum Family { kFamQuant, kFamDequant, kFamGemv, kFamSide, kFamGemm, kFamMerge, kFamAct8, kFamNorm, kFamCount };
-const char* const kFamNames[kFamCount] = {"quantize", "dequant", "gemv", "side", "gemm", "merge", "act8", "norm"};
+enum Family { kFamQuant, kFamDequant, kFamGemv, kFamSide, kFamGemm, kFamMerge, kFamAct8, kFamNorm, kFamLogprobs, kFamCount };
+const char* const kFamNames[kFamCount] = {"quantize", "dequant", "gemv", "side", "gemm", "merge", "act8", "norm", "logprobs"};
 
 // Shared by every host thread: `mu` guards the event pool and the records.
 struct TimingState {
@@ -1155,6 +1155,67 @@ extern "C" qlora_status qlora_residual_norm_bwd(const void* dh_out, const uint16
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Timed tm(kFamNorm, s, sums ? 2 : 1);
   return from_cuda(launch_residual_norm_bwd(p, res_dtype, s));
+}
+
+namespace {
+
+qlora_status check_logits(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld) {
+  if (!logits || (dtype != 0 && dtype != 1) || M < 1 || V < 1 || ld < V) return QLORA_ERR_INVALID_ARG;
+  if (V > INT32_MAX || ld > (int64_t{1} << 40) / M) return QLORA_ERR_UNSUPPORTED;
+  const int64_t size = dtype == 0 ? 2 : 4;
+  return aligned(logits, 16) && ld * size % 16 == 0 ? QLORA_OK : QLORA_ERR_ALIGNMENT;
+}
+
+}  // namespace
+
+extern "C" qlora_status qlora_token_logprobs_fwd(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                                 const int64_t* targets, float inv_temperature, float* logprob,
+                                                 float* entropy, float* row_max, float* log_sum, int32_t k,
+                                                 int32_t* top_ids, float* top_logprob, void* stream) {
+  qlora_status st = check_logits(logits, dtype, M, V, ld);
+  if (st != QLORA_OK) return st;
+  if (M > INT32_MAX) return QLORA_ERR_UNSUPPORTED;
+  if (!std::isfinite(inv_temperature) || inv_temperature <= 0.0f) return QLORA_ERR_INVALID_ARG;
+  if ((targets != nullptr) != (logprob != nullptr)) return QLORA_ERR_INVALID_ARG;
+  if (k < 0 || k > kLogprobsMaxTop || k > V || (k > 0) != (top_ids != nullptr) || (k > 0) != (top_logprob != nullptr))
+    return QLORA_ERR_INVALID_ARG;
+  if (!logprob && !entropy && !row_max && !log_sum && k == 0) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(targets, 8) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(row_max, 4) ||
+      !aligned(log_sum, 4) || !aligned(top_ids, 4) || !aligned(top_logprob, 4))
+    return QLORA_ERR_ALIGNMENT;
+  st = check_device();
+  if (st != QLORA_OK) return st;
+  const TokenLogprobsFwd p{logits, M, V, ld, targets, inv_temperature, logprob, entropy, row_max, log_sum, k, top_ids,
+                           top_logprob};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(kFamLogprobs, s);
+  return from_cuda(launch_token_logprobs_fwd(p, dtype, s));
+}
+
+extern "C" qlora_status qlora_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                                 const int64_t* targets, float inv_temperature, const float* row_max,
+                                                 const float* log_sum, const float* entropy, const float* g_logprob,
+                                                 const float* g_entropy, void* dlogits, int64_t ldd, void* stream) {
+  qlora_status st = check_logits(logits, dtype, M, V, ld);
+  if (st != QLORA_OK) return st;
+  st = check_logits(dlogits, dtype, M, V, ldd);
+  if (st != QLORA_OK) return st;
+  if (dlogits == logits && ldd != ld) return QLORA_ERR_INVALID_ARG;
+  if (!std::isfinite(inv_temperature) || inv_temperature <= 0.0f) return QLORA_ERR_INVALID_ARG;
+  if (!row_max || !log_sum || (!g_logprob && !g_entropy)) return QLORA_ERR_INVALID_ARG;
+  if ((g_logprob != nullptr) != (targets != nullptr) || (g_entropy != nullptr) != (entropy != nullptr))
+    return QLORA_ERR_INVALID_ARG;
+  if (M > INT32_MAX / ((V + 4095) / 4096)) return QLORA_ERR_UNSUPPORTED;  // the grid
+  if (!aligned(targets, 8) || !aligned(row_max, 4) || !aligned(log_sum, 4) || !aligned(entropy, 4) ||
+      !aligned(g_logprob, 4) || !aligned(g_entropy, 4))
+    return QLORA_ERR_ALIGNMENT;
+  st = check_device();
+  if (st != QLORA_OK) return st;
+  const TokenLogprobsBwd p{logits,  M,       V,         ld,        targets, inv_temperature, row_max,
+                           log_sum, entropy, g_logprob, g_entropy, dlogits, ldd,             0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(kFamLogprobs, s);
+  return from_cuda(launch_token_logprobs_bwd(p, dtype, s));
 }
 
 extern "C" qlora_status qlora_timing_enable(int32_t enable) {

@@ -306,6 +306,44 @@ cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cud
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
+// Token log probabilities (token_logprobs.cu)
+// ---------------------------------------------------------------------------
+
+constexpr int kLogprobsMaxTop = 32;
+
+struct TokenLogprobsFwd {
+  const void* logits;      // [M][ld] bf16 or fp32, V valid columns
+  int64_t M, V, ld;
+  const int64_t* targets;  // [M], null exactly when logprob is
+  float inv_temperature;
+  float* logprob;          // [M] each, may be null
+  float* entropy;
+  float* row_max;
+  float* log_sum;
+  int k;                   // 0 .. kLogprobsMaxTop, at most V
+  int32_t* top_ids;        // [M][k]
+  float* top_logprob;
+};
+
+struct TokenLogprobsBwd {
+  const void* logits;      // [M][ld]
+  int64_t M, V, ld;
+  const int64_t* targets;  // read with g_logprob
+  float inv_temperature;
+  const float* row_max;    // [M], of the forward
+  const float* log_sum;
+  const float* entropy;    // read with g_entropy
+  const float* g_logprob;  // may be null
+  const float* g_entropy;  // may be null
+  void* dlogits;           // [M][ldd], as logits (may be logits)
+  int64_t ldd;
+  int64_t chunks;          // CTAs per row (set by the launcher)
+};
+
+cudaError_t launch_token_logprobs_fwd(const TokenLogprobsFwd& p, int fp32, cudaStream_t stream);
+cudaError_t launch_token_logprobs_bwd(TokenLogprobsBwd p, int fp32, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
 // tcgen05 GEMM (gemm_tc.cu):  D[M][N] (+)= A[M][K] B[N][K]^T + A2[M][64] B2[N][64]^T
 // ---------------------------------------------------------------------------
 struct GemmArgs {

@@ -501,13 +501,60 @@ qlora_status qlora_residual_norm_bwd(const void *dh_out, const uint16_t *dx, con
                                      float *dw_pre, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * Log probabilities of given tokens, the entropy of each row and the most
+ * likely alternatives.  Per row of V logits x, c = inv_temperature,
+ * m = max x:
+ *     log_sum = log sum exp((x - m) c),   log p_j = (x_j - m) c - log_sum,
+ *     logprob = log p_target,             entropy = -sum p log p
+ *   logits  : [M, V] bf16 (dtype 0) or fp32 (1), rows ld elements apart; 16-byte
+ *             aligned, ld * element size a multiple of 16 (ALIGNMENT otherwise).
+ *             Nothing past column V - 1 is read.
+ *   targets : int64 [M], NULL exactly when logprob is.  A negative target is not
+ *             scored (logprob 0); one of V or more gives NaN.
+ *   inv_temperature : finite, > 0.
+ *   logprob, entropy, row_max (m), log_sum : fp32 [M] outputs, each may be NULL.
+ *             Keep row_max, log_sum (and entropy) for the backward.
+ *   k       : 0 .. 32, at most V.  top_ids (int32 [M, k]) receives the ids of the
+ *             k largest logits, largest first, the lowest id first among equals;
+ *             top_logprob (fp32 [M, k]) their log probabilities.  Both NULL
+ *             exactly when k is 0.
+ * A row whose logits are all -inf has row_max -inf, log_sum 0, entropy 0 and log
+ * probabilities -inf; a row masked to a finite value is an ordinary one.  A row
+ * with a NaN or +inf has NaN outputs (row_max: NaN or +inf); NaN ranks above
+ * every number among the alternatives.  Sums are fp32.  No workspace.
+ */
+qlora_status qlora_token_logprobs_fwd(const void *logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                      const int64_t *targets, float inv_temperature, float *logprob, float *entropy,
+                                      float *row_max, float *log_sum, int32_t k, int32_t *top_ids,
+                                      float *top_logprob, void *stream);
+
+/*
+ * Its gradient for upstream gradients g of logprob and gH of entropy (fp32
+ * [M], either may be NULL):
+ *     dlogits_j = c (g (1[j = target] - p_j) - gH p_j (log p_j + entropy))
+ *   targets : NULL exactly when g_logprob is; a negative target takes no part of
+ *             g (a mask of unscored positions), one of V or more gives a NaN row.
+ *   row_max, log_sum, entropy : the forward's (entropy NULL exactly when
+ *             g_entropy is).
+ *   dlogits : [M, V] of the logits' dtype, rows ldd elements apart, aligned as
+ *             logits; may be logits itself (with ldd = ld).  Columns from V on are
+ *             left alone: for the dY of a linear call whose rows are padded past
+ *             V, clear them once.
+ * Rows whose logits are all -inf get zeros, rows with NaN or +inf NaN.
+ */
+qlora_status qlora_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
+                                      const int64_t *targets, float inv_temperature, const float *row_max,
+                                      const float *log_sum, const float *entropy, const float *g_logprob,
+                                      const float *g_entropy, void *dlogits, int64_t ldd, void *stream);
+
+/*
  * Kernel timing (instrumentation for benchmarks; off by default).
  * While enabled, every kernel the library enqueues is bracketed by CUDA
  * events recorded on the launching stream, grouped by family:
  *   "quantize" (quantize + double quant), "dequant", "gemv", "side" (rank-r
  *   products, gradient column sums, padding), "gemm" (tensor-core GEMM),
  *   "merge" (qlora_merge), "act8" (activation checkpoints written and read back),
- *   "norm" (the residual norms).
+ *   "norm" (the residual norms), "logprobs" (token log probabilities).
  *   qlora_timing_enable : 1 starts recording (clearing earlier records), 0 stops.
  *   qlora_timing_read   : waits for the recorded events of `family` and returns
  *                         the summed device time in milliseconds and the number
