@@ -188,12 +188,19 @@ def _dev(t, name: str, dtypes=None, need: int | None = None) -> int:
     return t.data_ptr()
 
 
+# The current device and its current stream, once a CUDA tensor exists (so CUDA is initialised): the calls behind
+# torch.cuda.current_device / current_stream without their initialisation check and Stream object, which took half of
+# a short call's host time (one call per tensor argument).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _check_placement(t: torch.Tensor, name: str) -> None:
     """The tensor lives on the current CUDA device (the one the library launches on)."""
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor, got one on {t.device}")
-    cur = torch.cuda.current_device()
-    if t.device.index != cur:
+    cur = _current_device()
+    if t.get_device() != cur:
         raise ValueError(f"{name}: on {t.device}, but the library runs on the current device cuda:{cur}")
 
 
@@ -212,7 +219,9 @@ def _rank_ok(r: int) -> bool:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -17,8 +17,10 @@
 // registers of its threads between the two reductions, and nothing is read
 // twice.  A thread holds NC groups of 8 consecutive values, TPR groups apart
 // (16-byte accesses, lanes side by side; 8 lanes hold one 64-value checkpoint
-// block).  Rows of up to 1024 values take one warp (reductions by shuffles
-// alone), longer ones a CTA.  All arithmetic is fp32.
+// block).  Rows of up to 512 values take one warp (reductions by shuffles
+// alone), longer ones a CTA.  All arithmetic is fp32.  CTAs stay for many
+// rows: while a row is computed, the next one's operands travel to shared
+// memory (cp.async), so the two reductions' waits do not stop the loads.
 //
 // The backward's column sums stay in registers over all rows of a CTA; each
 // CTA writes one partial row and residual_norm_finish_kernel adds those in a
@@ -36,6 +38,12 @@ constexpr int kWarpRowCtas = 8;  // rows (warps) of a CTA when a warp takes a ro
 
 template <int TPR>
 constexpr int kNormThreads = TPR == 32 ? 32 * kWarpRowCtas : TPR;
+
+// Threads that share an SM: what the registers allow (64 and 128 per thread).
+constexpr int kFwdResident = 1024, kBwdResident = 512;
+
+template <int TPR, int kResident>
+constexpr int kMinCtas = kNormThreads<TPR> >= kResident ? 1 : kResident / kNormThreads<TPR>;
 
 // Sum over the TPR threads of a row, the same in each of them.  `slots`: one
 // float per warp, a different array for consecutive calls of a row.
@@ -67,11 +75,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// Eight values at element offset `at`; plain loads, as some inputs may be
-// written by the same call (in place).
-__device__ __forceinline__ void load8(const uint16_t* p, int64_t at, float (&v)[8]) {
-  unpack8(*reinterpret_cast<const uint4*>(p + at), v);
-}
+// Eight values at element offset `at`.
 __device__ __forceinline__ void load8(const float* p, int64_t at, float (&v)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p + at), b = *reinterpret_cast<const float4*>(p + at + 4);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -84,126 +88,198 @@ __device__ __forceinline__ void store8(float* p, int64_t at, const float (&v)[8]
   *reinterpret_cast<float4*>(p + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// A thread's share of one tensor's next row: copied to shared memory
+// asynchronously, read back by the same thread (so it needs no barrier), into
+// 16-byte slots kThreads apart (no bank conflicts).  Slots past the row's end
+// are zero-filled.
+template <typename T, int TPR, int NC>
+struct RowSlot {
+  static constexpr int kVecs = NC * static_cast<int>(sizeof(T)) / 2;  // 16-byte vectors
+  static constexpr int kThreads = kNormThreads<TPR>;
+  static constexpr int kBytes = kVecs * kThreads * 16;
+
+  __device__ static __forceinline__ void fetch(uint8_t* slot, const T* row, int tid, int64_t D, bool live) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = (c * TPR + tid) * 8;
+      const bool ok = live && at < D;
+#pragma unroll
+      for (int q = 0; q < kVecs / NC; ++q)
+        cp_async_16(slot + ((c * (kVecs / NC) + q) * kThreads + threadIdx.x) * 16,
+                    ok ? row + at + q * (16 / static_cast<int>(sizeof(T))) : row, ok);
+    }
+  }
+  __device__ static __forceinline__ void read(const uint8_t* slot, int c, float (&v)[8]) {
+    const uint4* s = reinterpret_cast<const uint4*>(slot) + c * (kVecs / NC) * kThreads + threadIdx.x;
+    if constexpr (sizeof(T) == 2) {
+      unpack8(*s, v);
+    } else {
+      const uint4 a = s[0], b = s[kThreads];
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    }
+  }
+};
+
 }  // namespace
 
 template <typename TRes, int TPR, int NC>
-__global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_fwd_kernel(ResidualNormFwd p) {
-  __shared__ float slots[2][32];
+__global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>)
+    residual_norm_fwd_kernel(ResidualNormFwd p) {
+  using H = RowSlot<TRes, TPR, NC>;
+  using Y = RowSlot<uint16_t, TPR, NC>;
+  constexpr int kRows = kNormThreads<TPR> / TPR;
+  extern __shared__ __align__(16) uint8_t slots_h[];
+  uint8_t* slots_y = slots_h + H::kBytes;
+  __shared__ float sums[4][32];
   const int tid = threadIdx.x % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kNormThreads<TPR> / TPR) + threadIdx.x / TPR;
-  if (row >= p.M) return;  // a whole warp (TPR = 32) or nothing
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
   const TRes* h = static_cast<const TRes*>(p.h);
   TRes* h_out = static_cast<TRes*>(p.h_out);
-  const int64_t base = row * p.D;
   const float inv_d = 1.0f / static_cast<float>(p.D);
 
-  float v[NC][8];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int at = (c * TPR + tid) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
-    if (at < p.D) load8(h, base + at, v[c]);
-  }
-  if (p.y != nullptr) {
-    float y[NC][8];
+  auto fetch = [&](int64_t next) {
+    const bool live = next < p.M;
+    const int64_t at = live ? next * p.D : 0;
+    H::fetch(slots_h, h + at, tid, p.D, live);
+    if (p.y != nullptr) Y::fetch(slots_y, p.y + at, tid, p.D, live);
+    cp_async_commit();
+  };
+  fetch(row);
+  int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
+  for (; row < p.M; row += stride, turn ^= 1) {
+    const int64_t base = row * p.D;
+    cp_async_wait<0>();
+    float v[NC][8], y[NC][8];
     float ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int at = (c * TPR + tid) * 8;
+      H::read(slots_h, c, v[c]);
+      if (p.y != nullptr) {
+        Y::read(slots_y, c, y[c]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[c][i] = 0.0f;
-      if (at < p.D) load8(p.y, base + at, y[c]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(y[c][i], y[c][i], ss);
+        for (int i = 0; i < 8; ++i) ss = fmaf(y[c][i], y[c][i], ss);
+      }
     }
-    float rstd = 1.0f;
-    if (p.w_post != nullptr) {
-      ss = row_sum<TPR>(ss, slots[0]);
-      rstd = 1.0f / sqrtf(ss * inv_d + p.eps);
-      if (p.rstd_post != nullptr && tid == 0) p.rstd_post[row] = rstd;
-    }
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int at = (c * TPR + tid) * 8;
-      if (at >= p.D) continue;
-      float w[8], g[8];
+    fetch(row + stride);  // into the slots just read
+    if (p.y != nullptr) {
+      float rstd = 1.0f;
       if (p.w_post != nullptr) {
-        load8(p.w_post, at, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[c][i] = y[c][i] * rstd * w[i];
-      }
-      if (p.gate != nullptr) {
-        load8(p.gate, at, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[c][i] *= g[i];
+        ss = row_sum<TPR>(ss, sums[2 * turn]);
+        rstd = 1.0f / sqrtf(ss * inv_d + p.eps);
+        if (p.rstd_post != nullptr && tid == 0) p.rstd_post[row] = rstd;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = fmaf(p.scale, y[c][i], v[c][i]);
+      for (int c = 0; c < NC; ++c) {
+        const int at = (c * TPR + tid) * 8;
+        if (at >= p.D) continue;
+        float w[8];
+        if (p.w_post != nullptr) {
+          load8(p.w_post, at, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[c][i] = y[c][i] * rstd * w[i];
+        }
+        if (p.gate != nullptr) {
+          load8(p.gate, at, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[c][i] *= w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(p.scale, y[c][i], v[c][i]);
+      }
     }
-  }
-  if (h_out != nullptr) {
+    if (h_out != nullptr) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int at = (c * TPR + tid) * 8;
+        if (at < p.D) store8(h_out, base + at, v[c]);
+      }
+    }
+    if (p.x == nullptr) continue;
+    ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+    ss = row_sum<TPR>(ss, sums[2 * turn + 1]);
+    const float rstd = 1.0f / sqrtf(ss * inv_d + p.eps);
+    if (p.rstd_pre != nullptr && tid == 0) p.rstd_pre[row] = rstd;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * TPR + tid) * 8;
-      if (at < p.D) store8(h_out, base + at, v[c]);
-    }
-  }
-  if (p.x == nullptr) return;
-  float ss = 0.0f;
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
-  ss = row_sum<TPR>(ss, slots[1]);
-  const float rstd = 1.0f / sqrtf(ss * inv_d + p.eps);
-  if (p.rstd_pre != nullptr && tid == 0) p.rstd_pre[row] = rstd;
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int at = (c * TPR + tid) * 8;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (at < p.D) {
-      float w[8];
-      load8(p.w_pre, at, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = v[c][i] * rstd * w[i];
-      x = pack8(w);
-      *reinterpret_cast<uint4*>(p.x + base + at) = x;
-    }
-    if (p.codes != nullptr) {  // the checkpoint is of x as stored; 8 lanes hold a block
-      uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(x.x & 0x7FFF7FFFu, x.y), x.z), x.w);
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 4));
-      m = max(m & 0xFFFFu, m >> 16);
-      uint2 q;
-      uint32_t step;
-      if (p.format == kAct8Int8) {
-        const Act8Encoder<kAct8Int8> enc(m);
-        q = enc.encode8(x), step = enc.step;
-      } else {
-        const Act8Encoder<kAct8E4m3> enc(m);
-        q = enc.encode8(x), step = enc.step;
-      }
+      uint4 x = make_uint4(0, 0, 0, 0);
       if (at < p.D) {
-        *reinterpret_cast<uint2*>(p.codes + base + at) = q;
-        if ((tid & 7) == 0) p.step[(base + at) / kBlock] = static_cast<uint16_t>(step);
+        float w[8];
+        load8(p.w_pre, at, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = v[c][i] * rstd * w[i];
+        x = pack8(w);
+        *reinterpret_cast<uint4*>(p.x + base + at) = x;
+      }
+      if (p.codes != nullptr) {  // the checkpoint is of x as stored; 8 lanes hold a block
+        uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(x.x & 0x7FFF7FFFu, x.y), x.z), x.w);
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = max(m & 0xFFFFu, m >> 16);
+        uint2 q;
+        uint32_t step;
+        if (p.format == kAct8Int8) {
+          const Act8Encoder<kAct8Int8> enc(m);
+          q = enc.encode8(x), step = enc.step;
+        } else {
+          const Act8Encoder<kAct8E4m3> enc(m);
+          q = enc.encode8(x), step = enc.step;
+        }
+        if (at < p.D) {
+          *reinterpret_cast<uint2*>(p.codes + base + at) = q;
+          if ((tid & 7) == 0) p.step[(base + at) / kBlock] = static_cast<uint16_t>(step);
+        }
       }
     }
   }
+  cp_async_wait<0>();
 }
 
 template <typename TRes, int TPR, int NC>
-__global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_bwd_kernel(ResidualNormBwd p) {
+__global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>)
+    residual_norm_bwd_kernel(ResidualNormBwd p) {
+  using H = RowSlot<TRes, TPR, NC>;
+  using Y = RowSlot<uint16_t, TPR, NC>;
   constexpr int kRows = kNormThreads<TPR> / TPR;
-  __shared__ float slots[4][32];
+  extern __shared__ __align__(16) uint8_t slots_dh[];
+  uint8_t* slots_h = slots_dh + H::kBytes;
+  uint8_t* slots_dx = slots_h + H::kBytes;
+  uint8_t* slots_y = slots_dx + Y::kBytes;
+  __shared__ float sums[4][32];
   const int tid = threadIdx.x % TPR;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
   const TRes* dh_out = static_cast<const TRes*>(p.dh_out);
   const TRes* h_out = static_cast<const TRes*>(p.h_out);
   TRes* dh = static_cast<TRes*>(p.dh);
   const float inv_d = 1.0f / static_cast<float>(p.D);
   const bool need_y = p.w_post != nullptr || p.dgate;
+  const bool branch = p.dy != nullptr || p.dgate || p.dw_post;
+
+  // Two groups of copies per row, each refilled as soon as it is read.
+  auto fetch = [&](int64_t next) {
+    const bool live = next < p.M;
+    const int64_t at = live ? next * p.D : 0;
+    if (dh_out != nullptr) H::fetch(slots_dh, dh_out + at, tid, p.D, live);
+    if (p.dx != nullptr) {
+      H::fetch(slots_h, h_out + at, tid, p.D, live);
+      Y::fetch(slots_dx, p.dx + at, tid, p.D, live);
+    }
+    cp_async_commit();
+  };
+  auto fetch_y = [&](int64_t next) {
+    const bool live = next < p.M;
+    if (need_y) Y::fetch(slots_y, p.y + (live ? next * p.D : 0), tid, p.D, live);
+    cp_async_commit();
+  };
 
   float s_pre[NC][8], s_gate[NC][8], s_post[NC][8];
 #pragma unroll
@@ -211,31 +287,32 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_bwd_kernel(Re
 #pragma unroll
     for (int i = 0; i < 8; ++i) s_pre[c][i] = s_gate[c][i] = s_post[c][i] = 0.0f;
 
+  fetch(row);
+  fetch_y(row);
   int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR; row < p.M;
-       row += stride, turn ^= 1) {
+  for (; row < p.M; row += stride, turn ^= 1) {
     const int64_t base = row * p.D;
-    float g[NC][8];
+    cp_async_wait<1>();
+    float g[NC][8], dn[NC][8], n[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int at = (c * TPR + tid) * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[c][i] = 0.0f;
-      if (dh_out != nullptr && at < p.D) load8(dh_out, base + at, g[c]);
+      if (dh_out != nullptr) H::read(slots_dh, c, g[c]);
+      if (p.dx != nullptr) {
+        H::read(slots_h, c, n[c]);
+        Y::read(slots_dx, c, dn[c]);
+      }
     }
+    fetch(row + stride);
     if (p.dx != nullptr) {
       const float rstd = p.rstd_pre[row];
-      float dn[NC][8], n[NC][8];
       float dot = 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int at = (c * TPR + tid) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dn[c][i] = n[c][i] = 0.0f;
         if (at >= p.D) continue;
         float w[8];
-        load8(p.dx, base + at, dn[c]);
-        load8(h_out, base + at, n[c]);
         load8(p.w_pre, at, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -245,7 +322,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_bwd_kernel(Re
           dot = fmaf(dn[c][i], n[c][i], dot);
         }
       }
-      dot = row_sum<TPR>(dot, slots[2 * turn]) * inv_d;
+      dot = row_sum<TPR>(dot, sums[2 * turn]) * inv_d;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -258,20 +335,28 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_bwd_kernel(Re
         if (at < p.D) store8(dh, base + at, g[c]);
       }
     }
-    if (p.dy == nullptr && !p.dgate && !p.dw_post) continue;
+    if (!branch) {
+      cp_async_commit();  // keeps the two groups per row
+      continue;
+    }
+    cp_async_wait<1>();
     float m[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[c][i] = 0.0f;
+      if (need_y) Y::read(slots_y, c, m[c]);
+    }
+    fetch_y(row + stride);
     const float rstd = p.w_post != nullptr ? p.rstd_post[row] : 1.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * TPR + tid) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[c][i] = 0.0f;
       if (at >= p.D) continue;
       float w[8], gt[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = gt[i] = 1.0f;
-      if (need_y) load8(p.y, base + at, m[c]);
       if (p.w_post != nullptr) load8(p.w_post, at, w);
       if (p.gate != nullptr) load8(p.gate, at, gt);
 #pragma unroll
@@ -286,7 +371,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_bwd_kernel(Re
       }
     }
     if (p.w_post != nullptr) {
-      dot = row_sum<TPR>(dot, slots[2 * turn + 1]) * inv_d;
+      dot = row_sum<TPR>(dot, sums[2 * turn + 1]) * inv_d;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -300,6 +385,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_bwd_kernel(Re
       }
     }
   }
+  cp_async_wait<0>();
 
   // One partial row per CTA.  With a warp per row, the warps add theirs in turn.
   auto put = [&](const float (&s)[NC][8], int which) {
@@ -328,79 +414,118 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) residual_norm_bwd_kernel(Re
 }
 
 // dst_q[d] = sum of the `count` partial rows of gradient q = blockIdx.y.  A CTA
-// takes 32 columns; its 8 warps take every eighth row, then add in order.
-__global__ void __launch_bounds__(256) residual_norm_finish_kernel(const float* __restrict__ part, int count, int64_t D,
-                                                                   float* dw_pre, float* dgate, float* dw_post) {
-  __shared__ float sums[8][32];
+// takes 32 columns; its 32 warps take every 32nd row, then add in order.
+__global__ void __launch_bounds__(1024) residual_norm_finish_kernel(const float* __restrict__ part, int count,
+                                                                    int64_t D, float* dw_pre, float* dgate,
+                                                                    float* dw_post) {
+  __shared__ float sums[32][33];
   float* dst = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dgate : dw_post;
   if (dst == nullptr) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  const float* src = part + static_cast<int64_t>(blockIdx.y) * count * D + d;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32;
+  const float* src = part + static_cast<int64_t>(blockIdx.y) * count * D + d + lane;
   float s = 0.0f;
-  for (int i = warp; i < count; i += 8) s += src[i * D];
+#pragma unroll 8
+  for (int i = warp; i < count; i += 32) s += src[i * D];
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0) {
-    s = 0.0f;
+  // Warp w adds column w's 32 sums by a fixed tree.
+  s = sums[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += sums[w][lane];
-    dst[d] = s;
-  }
+  for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+  if (lane == 0) dst[d + warp] = s;
 }
 
 namespace {
 
-// Threads per row and 8-value groups per thread, by the row's length.
-template <typename F>
-cudaError_t with_shape(int64_t D, F&& f) {
-  if (D <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-  if (D <= 512) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
-  if (D <= 1024) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
-  if (D <= 2048) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{});
-  if (D <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (D <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+// Threads per row (TPR) and 8-value groups per thread (NC), by the row's length.
+struct NormShape {
+  int tpr, nc;
+};
+
+constexpr NormShape norm_shape(int64_t D) {
+  return D <= 256    ? NormShape{32, 1}
+         : D <= 512  ? NormShape{32, 2}
+         : D <= 1024 ? NormShape{64, 2}
+         : D <= 2048 ? NormShape{128, 2}
+         : D <= 4096 ? NormShape{256, 2}
+         : D <= 8192 ? NormShape{512, 2}
+                     : NormShape{1024, 2};
 }
 
-int64_t rows_per_cta(int64_t D) { return D <= 1024 ? kWarpRowCtas : 1; }
+template <typename F>
+cudaError_t with_shape(int64_t D, F&& f) {
+  using std::integral_constant;
+  switch (norm_shape(D).tpr) {
+    case 32:
+      switch (norm_shape(D).nc) {
+        case 1: return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+        default: return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+      }
+    case 64: return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    case 128: return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+    case 256: return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    case 512: return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    default: return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  }
+}
+
+// CTAs of one wave on a 148-SM B200 with `threads` resident threads per SM,
+// or as many as the rows need.
+int64_t norm_ctas(int64_t M, int64_t D, int64_t resident) {
+  const int64_t tpr = norm_shape(D).tpr, rows = tpr == 32 ? kWarpRowCtas : 1;
+  const int64_t threads = tpr * rows, want = (M + rows - 1) / rows;
+  const int64_t most = 148 * (threads >= resident ? 1 : resident / threads);
+  return want < most ? want : most;
+}
+
+template <typename Kernel, typename Params>
+cudaError_t launch_norm(Kernel kernel, DeviceOnce& configured, int ctas, int threads, int smem, const Params& p,
+                        cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = configured.run(dev, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, threads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename TRes>
+cudaError_t launch_fwd(const ResidualNormFwd& p, cudaStream_t stream) {
+  return with_shape(p.D, [&](auto tpr, auto nc) {
+    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
+    constexpr int smem = RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes;
+    static DeviceOnce configured;
+    const int ctas = static_cast<int>(norm_ctas(p.M, p.D, kFwdResident));
+    return launch_norm(residual_norm_fwd_kernel<TRes, TPR, NC>, configured, ctas, kNormThreads<TPR>, smem, p, stream);
+  });
+}
+
+template <typename TRes>
+cudaError_t launch_bwd(const ResidualNormBwd& p, cudaStream_t stream) {
+  return with_shape(p.D, [&](auto tpr, auto nc) {
+    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
+    constexpr int smem = 2 * (RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes);
+    static DeviceOnce configured;
+    const int ctas = residual_norm_bwd_ctas(p.M, p.D);
+    return launch_norm(residual_norm_bwd_kernel<TRes, TPR, NC>, configured, ctas, kNormThreads<TPR>, smem, p, stream);
+  });
+}
 
 }  // namespace
 
-int residual_norm_bwd_ctas(int64_t M, int64_t D) {
-  const int64_t want = (M + rows_per_cta(D) - 1) / rows_per_cta(D);
-  // Resident CTAs of a 148-SM B200: 512 threads or one CTA per SM.
-  const int64_t threads = D <= 1024 ? 256 : D <= 2048 ? 128 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024;
-  const int64_t most = 148 * (threads >= 512 ? 1 : 512 / threads);
-  return static_cast<int>(want < most ? want : most);
-}
+int residual_norm_bwd_ctas(int64_t M, int64_t D) { return static_cast<int>(norm_ctas(M, D, kBwdResident)); }
 
 cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cudaStream_t stream) {
-  const int64_t rows = rows_per_cta(p.D);
-  const unsigned grid = static_cast<unsigned>((p.M + rows - 1) / rows);
-  return with_shape(p.D, [&](auto tpr, auto nc) {
-    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
-    if (res_fp32)
-      residual_norm_fwd_kernel<float, TPR, NC><<<grid, kNormThreads<TPR>, 0, stream>>>(p);
-    else
-      residual_norm_fwd_kernel<uint16_t, TPR, NC><<<grid, kNormThreads<TPR>, 0, stream>>>(p);
-    return cudaGetLastError();
-  });
+  return res_fp32 ? launch_fwd<float>(p, stream) : launch_fwd<uint16_t>(p, stream);
 }
 
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cudaStream_t stream) {
-  const int ctas = residual_norm_bwd_ctas(p.M, p.D);
-  const cudaError_t e = with_shape(p.D, [&](auto tpr, auto nc) {
-    constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
-    if (res_fp32)
-      residual_norm_bwd_kernel<float, TPR, NC><<<ctas, kNormThreads<TPR>, 0, stream>>>(p);
-    else
-      residual_norm_bwd_kernel<uint16_t, TPR, NC><<<ctas, kNormThreads<TPR>, 0, stream>>>(p);
-    return cudaGetLastError();
-  });
+  const cudaError_t e = res_fp32 ? launch_bwd<float>(p, stream) : launch_bwd<uint16_t>(p, stream);
   if (e != cudaSuccess || (!p.dw_pre && !p.dgate && !p.dw_post)) return e;
-  residual_norm_finish_kernel<<<dim3(static_cast<unsigned>(p.D / 32), 3), 256, 0, stream>>>(p.part, ctas, p.D, p.dw_pre,
-                                                                                           p.dgate, p.dw_post);
+  residual_norm_finish_kernel<<<dim3(static_cast<unsigned>(p.D / 32), 3), 1024, 0, stream>>>(
+      p.part, residual_norm_bwd_ctas(p.M, p.D), p.D, p.dw_pre, p.dgate, p.dw_post);
   return cudaGetLastError();
 }
 
