@@ -298,7 +298,7 @@ struct ResidualNormBwd {
   float* dw_post;        // [D] each, may be null
   float* dgate;
   float* dw_pre;
-  float* part;           // [3][residual_norm_bwd_ctas(M, D)][D]
+  float* part;           // [2][residual_norm_bwd_ctas(M, D)][D]
 };
 
 int residual_norm_bwd_ctas(int64_t M, int64_t D);

@@ -39,8 +39,8 @@ constexpr int kWarpRowCtas = 8;  // rows (warps) of a CTA when a warp takes a ro
 template <int TPR>
 constexpr int kNormThreads = TPR == 32 ? 32 * kWarpRowCtas : TPR;
 
-// Threads that share an SM: what the registers allow (64 and 128 per thread).
-constexpr int kFwdResident = 1024, kBwdResident = 512;
+// Threads that share an SM: what the registers allow (about 80 and 128 per thread).
+constexpr int kFwdResident = 768, kBwdResident = 512;
 
 template <int TPR, int kResident>
 constexpr int kMinCtas = kNormThreads<TPR> >= kResident ? 1 : kResident / kNormThreads<TPR>;
@@ -56,8 +56,18 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
     if ((threadIdx.x & 31) == 0) slots[warp] = v;
     __syncthreads();
     v = 0.0f;
+    if constexpr (TPR == 64) {
+      const float2 s = *reinterpret_cast<const float2*>(slots);
+      v = s.x + s.y;
+    } else {
+      float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < TPR / 32; ++w) v += slots[w];
+      for (int w = 0; w < TPR / 32; w += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(slots + w);
+        u[0] += s.x, u[1] += s.y, u[2] += s.z, u[3] += s.w;
+      }
+      v = (u[0] + u[1]) + (u[2] + u[3]);
+    }
   }
   return v;
 }
@@ -132,7 +142,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
   constexpr int kRows = kNormThreads<TPR> / TPR;
   extern __shared__ __align__(16) uint8_t slots_h[];
   uint8_t* slots_y = slots_h + H::kBytes;
-  __shared__ float sums[4][32];
+  __shared__ __align__(16) float sums[4][32];
   const int tid = threadIdx.x % TPR;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
@@ -148,6 +158,28 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
     cp_async_commit();
   };
   fetch(row);
+  // The branch's factor scale gate w_post and w_pre stay in registers: read
+  // from L1 for every row they were half of the kernel's L1 traffic.
+  float coef[NC][8], w_pre[NC][8];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int at = (c * TPR + tid) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) coef[c][i] = p.scale, w_pre[c][i] = 0.0f;
+    if (at >= p.D) continue;
+    float w[8];
+    if (p.w_post != nullptr) {
+      load8(p.w_post, at, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) coef[c][i] *= w[i];
+    }
+    if (p.gate != nullptr) {
+      load8(p.gate, at, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) coef[c][i] *= w[i];
+    }
+    if (p.w_pre != nullptr) load8(p.w_pre, at, w_pre[c]);
+  }
   int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
   for (; row < p.M; row += stride, turn ^= 1) {
     const int64_t base = row * p.D;
@@ -168,27 +200,13 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
       float rstd = 1.0f;
       if (p.w_post != nullptr) {
         ss = row_sum<TPR>(ss, sums[2 * turn]);
-        rstd = 1.0f / sqrtf(ss * inv_d + p.eps);
+        rstd = rsqrtf(ss * inv_d + p.eps);
         if (p.rstd_post != nullptr && tid == 0) p.rstd_post[row] = rstd;
       }
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int at = (c * TPR + tid) * 8;
-        if (at >= p.D) continue;
-        float w[8];
-        if (p.w_post != nullptr) {
-          load8(p.w_post, at, w);
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[c][i] = y[c][i] * rstd * w[i];
-        }
-        if (p.gate != nullptr) {
-          load8(p.gate, at, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[c][i] *= w[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(p.scale, y[c][i], v[c][i]);
-      }
+        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(y[c][i] * rstd, coef[c][i], v[c][i]);
     }
     if (h_out != nullptr) {
 #pragma unroll
@@ -204,18 +222,16 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
     ss = row_sum<TPR>(ss, sums[2 * turn + 1]);
-    const float rstd = 1.0f / sqrtf(ss * inv_d + p.eps);
+    const float rstd = rsqrtf(ss * inv_d + p.eps);
     if (p.rstd_pre != nullptr && tid == 0) p.rstd_pre[row] = rstd;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * TPR + tid) * 8;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (at < p.D) {
-        float w[8];
-        load8(p.w_pre, at, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = v[c][i] * rstd * w[i];
-        x = pack8(w);
+        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * rstd * w_pre[c][i];
+        x = pack8(v[c]);
         *reinterpret_cast<uint4*>(p.x + base + at) = x;
       }
       if (p.codes != nullptr) {  // the checkpoint is of x as stored; 8 lanes hold a block
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
   uint8_t* slots_h = slots_dh + H::kBytes;
   uint8_t* slots_dx = slots_h + H::kBytes;
   uint8_t* slots_y = slots_dx + Y::kBytes;
-  __shared__ float sums[4][32];
+  __shared__ __align__(16) float sums[4][32];
   const int tid = threadIdx.x % TPR;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
   const TRes* h_out = static_cast<const TRes*>(p.h_out);
   TRes* dh = static_cast<TRes*>(p.dh);
   const float inv_d = 1.0f / static_cast<float>(p.D);
-  const bool need_y = p.w_post != nullptr || p.dgate;
+  const bool need_y = p.w_post != nullptr || p.dgate;  // else dy = scale gate g alone
   const bool branch = p.dy != nullptr || p.dgate || p.dw_post;
 
   // Two groups of copies per row, each refilled as soon as it is read.
@@ -281,14 +297,22 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
     cp_async_commit();
   };
 
-  float s_pre[NC][8], s_gate[NC][8], s_post[NC][8];
+  float s_pre[NC][8], s_branch[NC][8];  // column sums of dx n and of g m
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_gate[c][i] = s_post[c][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_branch[c][i] = 0.0f;
 
+  // Row scalars travel a row ahead as well, in registers.
+  float next_pre = 0.0f, next_post = 1.0f;
+  auto fetch_rstd = [&](int64_t next) {
+    if (next >= p.M) return;
+    if (p.dx != nullptr) next_pre = p.rstd_pre[next];
+    if (p.w_post != nullptr) next_post = p.rstd_post[next];
+  };
   fetch(row);
   fetch_y(row);
+  fetch_rstd(row);
   int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
   for (; row < p.M; row += stride, turn ^= 1) {
     const int64_t base = row * p.D;
@@ -305,8 +329,9 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
       }
     }
     fetch(row + stride);
+    const float rstd_pre = next_pre, rstd_post = next_post;
+    fetch_rstd(row + stride);
     if (p.dx != nullptr) {
-      const float rstd = p.rstd_pre[row];
       float dot = 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -316,7 +341,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
         load8(p.w_pre, at, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          n[c][i] *= rstd;
+          n[c][i] *= rstd_pre;
           s_pre[c][i] = fmaf(dn[c][i], n[c][i], s_pre[c][i]);
           dn[c][i] *= w[i];
           dot = fmaf(dn[c][i], n[c][i], dot);
@@ -326,7 +351,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[c][i] = fmaf(rstd, dn[c][i] - n[c][i] * dot, g[c][i]);
+        for (int i = 0; i < 8; ++i) g[c][i] = fmaf(rstd_pre, fmaf(-n[c][i], dot, dn[c][i]), g[c][i]);
     }
     if (dh != nullptr) {
 #pragma unroll
@@ -348,25 +373,29 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
       if (need_y) Y::read(slots_y, c, m[c]);
     }
     fetch_y(row + stride);
-    const float rstd = p.w_post != nullptr ? p.rstd_post[row] : 1.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * TPR + tid) * 8;
       if (at >= p.D) continue;
-      float w[8], gt[8];
+      float coef[8], w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = gt[i] = 1.0f;
-      if (p.w_post != nullptr) load8(p.w_post, at, w);
-      if (p.gate != nullptr) load8(p.gate, at, gt);
+      for (int i = 0; i < 8; ++i) coef[i] = p.scale;
+      if (p.w_post != nullptr) {
+        load8(p.w_post, at, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) coef[i] *= w[i];
+      }
+      if (p.gate != nullptr) {
+        load8(p.gate, at, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) coef[i] *= w[i];
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        m[c][i] *= rstd;
-        float dp = p.scale * g[c][i];
-        s_gate[c][i] = fmaf(dp, m[c][i] * w[i], s_gate[c][i]);
-        dp *= gt[i];
-        s_post[c][i] = fmaf(dp, m[c][i], s_post[c][i]);
-        g[c][i] = dp * w[i];
+        m[c][i] *= rstd_post;
+        s_branch[c][i] = fmaf(g[c][i], m[c][i], s_branch[c][i]);
+        g[c][i] *= coef[i];
         dot = fmaf(g[c][i], m[c][i], dot);
       }
     }
@@ -375,7 +404,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[c][i] = rstd * (g[c][i] - m[c][i] * dot);
+        for (int i = 0; i < 8; ++i) g[c][i] = rstd_post * fmaf(-m[c][i], dot, g[c][i]);
     }
     if (p.dy != nullptr) {
 #pragma unroll
@@ -409,31 +438,35 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
     }
   };
   if (p.dw_pre) put(s_pre, 0);
-  if (p.dgate) put(s_gate, 1);
-  if (p.dw_post) put(s_post, 2);
+  if (p.dgate || p.dw_post) put(s_branch, 1);
 }
 
-// dst_q[d] = sum of the `count` partial rows of gradient q = blockIdx.y.  A CTA
-// takes 32 columns; its 32 warps take every 32nd row, then add in order.
-__global__ void __launch_bounds__(1024) residual_norm_finish_kernel(const float* __restrict__ part, int count,
-                                                                    int64_t D, float* dw_pre, float* dgate,
-                                                                    float* dw_post) {
+// Column sums from the `count` partial rows of quantity q = blockIdx.y: dw_pre
+// is the first, and dgate and dw_post are both the second, T = sum g m, times
+// what does not depend on the row (scale w_post and scale gate).  A CTA takes
+// 32 columns; its 32 warps take every 32nd row, then add in a fixed tree.
+__global__ void __launch_bounds__(1024) residual_norm_finish_kernel(ResidualNormBwd p, int count) {
   __shared__ float sums[32][33];
-  float* dst = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dgate : dw_post;
-  if (dst == nullptr) return;
+  if (blockIdx.y == 0 ? p.dw_pre == nullptr : p.dgate == nullptr && p.dw_post == nullptr) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32;
-  const float* src = part + static_cast<int64_t>(blockIdx.y) * count * D + d + lane;
+  const int64_t d0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const float* src = p.part + static_cast<int64_t>(blockIdx.y) * count * p.D + d0 + lane;
   float s = 0.0f;
 #pragma unroll 8
-  for (int i = warp; i < count; i += 32) s += src[i * D];
+  for (int i = warp; i < count; i += 32) s += src[i * p.D];
   sums[warp][lane] = s;
   __syncthreads();
-  // Warp w adds column w's 32 sums by a fixed tree.
-  s = sums[lane][warp];
+  s = sums[lane][warp];  // warp w: column w
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-  if (lane == 0) dst[d + warp] = s;
+  if (lane != 0) return;
+  const int64_t d = d0 + warp;
+  if (blockIdx.y == 0) {
+    p.dw_pre[d] = s;
+    return;
+  }
+  if (p.dgate != nullptr) p.dgate[d] = s * p.scale * (p.w_post != nullptr ? p.w_post[d] : 1.0f);
+  if (p.dw_post != nullptr) p.dw_post[d] = s * p.scale * (p.gate != nullptr ? p.gate[d] : 1.0f);
 }
 
 namespace {
@@ -524,8 +557,8 @@ cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cud
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cudaStream_t stream) {
   const cudaError_t e = res_fp32 ? launch_bwd<float>(p, stream) : launch_bwd<uint16_t>(p, stream);
   if (e != cudaSuccess || (!p.dw_pre && !p.dgate && !p.dw_post)) return e;
-  residual_norm_finish_kernel<<<dim3(static_cast<unsigned>(p.D / 32), 3), 1024, 0, stream>>>(
-      p.part, residual_norm_bwd_ctas(p.M, p.D), p.D, p.dw_pre, p.dgate, p.dw_post);
+  residual_norm_finish_kernel<<<dim3(static_cast<unsigned>(p.D / 32), 2), 1024, 0, stream>>>(
+      p, residual_norm_bwd_ctas(p.M, p.D));
   return cudaGetLastError();
 }
 
