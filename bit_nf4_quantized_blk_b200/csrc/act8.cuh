@@ -11,6 +11,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace qnf4 {
 
@@ -39,66 +40,65 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t m, uint32_t v) { retu
 template <int kFormat>
 struct Act8Encoder {
   uint32_t step;  // bf16 bits
-  float pre, d, inv, limit;
+  float d, inv;   // divisor and its approximate reciprocal
+  float pre;      // factor of the values before the division
+  bool plain;     // pre = 1, and no quotient leaves the int8 range
 
   __device__ __forceinline__ explicit Act8Encoder(uint32_t amax_bits) {
-    if (amax_bits >= 0x7F80u) {
-      step = kAct8NanStep;
-      pre = d = inv = limit = 0.0f;
-      return;
-    }
     const float a = bf16_bits_to_float(amax_bits);
-    step = pack_bf16x2(kFormat == kAct8Int8 ? __fdiv_rn(a, 127.0f) : a * 0x1p-8f, 0.0f) & 0xFFFFu;
+    // a times fp32(1 / 127) rounds to the same bf16 as a / 127 for every bf16 a.
+    step = pack_bf16x2(a * (kFormat == kAct8Int8 ? 1.0f / 127.0f : 0x1p-8f), 0.0f) & 0xFFFFu;
     // 127 steps of more than 2^121 would pass the largest bf16 value.
     if (kFormat == kAct8Int8 && step > 0x7C00u) step = 0x7C00u;
-    // Steps below 2^-60 are divided by with both sides scaled up, so that
+    if (amax_bits >= 0x7F80u) step = kAct8NanStep;
+    // Steps below 2^-90 are divided by with both sides scaled up, so that
     // neither the reciprocal nor the residual leaves the normal range.
-    pre = step < 0x2180u ? 0x1p64f : 1.0f;
+    plain = step >= 0x1280u && step < 0x7C00u;
+    pre = plain ? 1.0f : step < 0x1280u ? 0x1p64f : 1.0f;
     d = bf16_bits_to_float(step) * pre;
-    inv = step != 0 ? __frcp_rn(d) : 0.0f;
-    // |x / step| passes 127.5 only where the step itself was cut or is subnormal.
-    limit = (step >= 0x0080u && step < 0x7C00u) ? 0.0f : 127.0f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
   }
 
-  // x / step, rounded once.  t = n inv is within two units in the last place;
-  // the residual n - t d is exact in fp32 (x and step have 8 significant
-  // bits), and one correction by it gives the nearest fp32 to the quotient
-  // (Markstein's refinement), exactly the quotient where that is
-  // representable, so ties are seen as ties.  Other quotients of two 8-bit
+  // x / step for two values, each rounded once.  t = n inv is within a few
+  // units in the last place; the residual n - t d is exact in fp32 (x and step
+  // have 8 significant bits), and one correction by it gives the nearest fp32
+  // to the quotient (Markstein's refinement), exactly the quotient where that
+  // is representable, so ties are seen as ties.  Other quotients of two 8-bit
   // significands are at least 2^-17 (relative) away from a rounding border.
-  __device__ __forceinline__ float quotient(float x) const {
-    const float n = x * pre;
-    const float t = n * inv;
-    return fmaf(fmaf(-t, d, n), inv, t);
+  __device__ __forceinline__ F2 quotient(F2 n) const {
+    const F2 t = mul2(n, splat2(inv));
+    return fma2(fma2(F2{-t.x, -t.y}, splat2(d), n), splat2(inv), t);
   }
 
-  // Codes of four values, value 0 in the lowest byte.
-  __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3) const {
-    float q[4] = {quotient(x0), quotient(x1), quotient(x2), quotient(x3)};
+  // Codes of four values (two packed bf16 words), value 0 in the lowest byte.
+  template <bool kPlain>
+  __device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1) const {
+    F2 a{__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xFFFF0000u)};
+    F2 b{__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xFFFF0000u)};
+    if constexpr (!kPlain) a = mul2(a, splat2(pre)), b = mul2(b, splat2(pre));
+    a = quotient(a), b = quotient(b);
     if constexpr (kFormat == kAct8Int8) {
-      if (limit != 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = fminf(fmaxf(q[i], -limit), limit);
+      if constexpr (!kPlain) {
+        a = F2{fminf(fmaxf(a.x, -127.0f), 127.0f), fminf(fmaxf(a.y, -127.0f), 127.0f)};
+        b = F2{fminf(fmaxf(b.x, -127.0f), 127.0f), fminf(fmaxf(b.y, -127.0f), 127.0f)};
       }
-      uint32_t b[4];
       // 1.5 2^23 + q rounds q to an integer (ties to even) in the low mantissa bits.
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[i] + 12582912.0f);
-      return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+      a = add2(a, splat2(12582912.0f)), b = add2(b, splat2(12582912.0f));
+      return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                         __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
     } else {
       uint16_t lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[1]), "f"(q[0]));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[3]), "f"(q[2]));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
       return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
     }
   }
 
   // Codes of eight packed bf16 values.
   __device__ __forceinline__ uint2 encode8(const uint4& v) const {
-    if (inv == 0.0f) return make_uint2(0u, 0u);
-    auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
-    auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
-    return make_uint2(encode4(lo(v.x), hi(v.x), lo(v.y), hi(v.y)), encode4(lo(v.z), hi(v.z), lo(v.w), hi(v.w)));
+    if (plain) return make_uint2(encode4<true>(v.x, v.y), encode4<true>(v.z, v.w));
+    if (step == 0 || step == kAct8NanStep) return make_uint2(0u, 0u);
+    return make_uint2(encode4<false>(v.x, v.y), encode4<false>(v.z, v.w));
   }
 };
 

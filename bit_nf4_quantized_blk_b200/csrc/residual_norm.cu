@@ -72,30 +72,29 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
   return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+// Eight consecutive values are four pairs throughout.
+__device__ __forceinline__ void unpack8(const uint4& u, F2 (&v)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = F2{__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)};
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const F2 (&v)[4]) {
+  return make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                    pack_bf16x2(v[3].x, v[3].y));
 }
 
 // Eight values at element offset `at`.
-__device__ __forceinline__ void load8(const float* p, int64_t at, float (&v)[8]) {
+__device__ __forceinline__ void load8(const float* p, int64_t at, F2 (&v)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p + at), b = *reinterpret_cast<const float4*>(p + at + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  v[0] = F2{a.x, a.y}, v[1] = F2{a.z, a.w}, v[2] = F2{b.x, b.y}, v[3] = F2{b.z, b.w};
 }
-__device__ __forceinline__ void store8(uint16_t* p, int64_t at, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t* p, int64_t at, const F2 (&v)[4]) {
   *reinterpret_cast<uint4*>(p + at) = pack8(v);
 }
-__device__ __forceinline__ void store8(float* p, int64_t at, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p + at) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float* p, int64_t at, const F2 (&v)[4]) {
+  *reinterpret_cast<float4*>(p + at) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  *reinterpret_cast<float4*>(p + at + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
 
 // A thread's share of one tensor's next row: copied to shared memory
@@ -119,15 +118,14 @@ struct RowSlot {
                     ok ? row + at + q * (16 / static_cast<int>(sizeof(T))) : row, ok);
     }
   }
-  __device__ static __forceinline__ void read(const uint8_t* slot, int c, float (&v)[8]) {
+  __device__ static __forceinline__ void read(const uint8_t* slot, int c, F2 (&v)[4]) {
     const uint4* s = reinterpret_cast<const uint4*>(slot) + c * (kVecs / NC) * kThreads + threadIdx.x;
     if constexpr (sizeof(T) == 2) {
       unpack8(*s, v);
     } else {
       const uint4 a = s[0], b = s[kThreads];
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+      v[0] = F2{__uint_as_float(a.x), __uint_as_float(a.y)}, v[1] = F2{__uint_as_float(a.z), __uint_as_float(a.w)};
+      v[2] = F2{__uint_as_float(b.x), __uint_as_float(b.y)}, v[3] = F2{__uint_as_float(b.z), __uint_as_float(b.w)};
     }
   }
 };
@@ -160,23 +158,23 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
   fetch(row);
   // The branch's factor scale gate w_post and w_pre stay in registers: read
   // from L1 for every row they were half of the kernel's L1 traffic.
-  float coef[NC][8], w_pre[NC][8];
+  F2 coef[NC][4], w_pre[NC][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int at = (c * TPR + tid) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) coef[c][i] = p.scale, w_pre[c][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) coef[c][i] = splat2(p.scale), w_pre[c][i] = splat2(0.0f);
     if (at >= p.D) continue;
-    float w[8];
+    F2 w[4];
     if (p.w_post != nullptr) {
       load8(p.w_post, at, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) coef[c][i] *= w[i];
+      for (int i = 0; i < 4; ++i) coef[c][i] = mul2(coef[c][i], w[i]);
     }
     if (p.gate != nullptr) {
       load8(p.gate, at, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) coef[c][i] *= w[i];
+      for (int i = 0; i < 4; ++i) coef[c][i] = mul2(coef[c][i], w[i]);
     }
     if (p.w_pre != nullptr) load8(p.w_pre, at, w_pre[c]);
   }
@@ -184,29 +182,28 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
   for (; row < p.M; row += stride, turn ^= 1) {
     const int64_t base = row * p.D;
     cp_async_wait<0>();
-    float v[NC][8], y[NC][8];
-    float ss = 0.0f;
+    F2 v[NC][4], y[NC][4];
+    F2 ss = splat2(0.0f);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       H::read(slots_h, c, v[c]);
       if (p.y != nullptr) {
         Y::read(slots_y, c, y[c]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[c][i], y[c][i], ss);
+        for (int i = 0; i < 4; ++i) ss = fma2(y[c][i], y[c][i], ss);
       }
     }
     fetch(row + stride);  // into the slots just read
     if (p.y != nullptr) {
       float rstd = 1.0f;
       if (p.w_post != nullptr) {
-        ss = row_sum<TPR>(ss, sums[2 * turn]);
-        rstd = rsqrtf(ss * inv_d + p.eps);
+        rstd = rsqrtf(row_sum<TPR>(ss.x + ss.y, sums[2 * turn]) * inv_d + p.eps);
         if (p.rstd_post != nullptr && tid == 0) p.rstd_post[row] = rstd;
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(y[c][i] * rstd, coef[c][i], v[c][i]);
+        for (int i = 0; i < 4; ++i) v[c][i] = fma2(mul2(y[c][i], splat2(rstd)), coef[c][i], v[c][i]);
     }
     if (h_out != nullptr) {
 #pragma unroll
@@ -216,13 +213,12 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
       }
     }
     if (p.x == nullptr) continue;
-    ss = 0.0f;
+    ss = splat2(0.0f);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
-    ss = row_sum<TPR>(ss, sums[2 * turn + 1]);
-    const float rstd = rsqrtf(ss * inv_d + p.eps);
+      for (int i = 0; i < 4; ++i) ss = fma2(v[c][i], v[c][i], ss);
+    const float rstd = rsqrtf(row_sum<TPR>(ss.x + ss.y, sums[2 * turn + 1]) * inv_d + p.eps);
     if (p.rstd_pre != nullptr && tid == 0) p.rstd_pre[row] = rstd;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -230,7 +226,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
       uint4 x = make_uint4(0, 0, 0, 0);
       if (at < p.D) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * rstd * w_pre[c][i];
+        for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], splat2(rstd)), w_pre[c][i]);
         x = pack8(v[c]);
         *reinterpret_cast<uint4*>(p.x + base + at) = x;
       }
@@ -297,11 +293,11 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
     cp_async_commit();
   };
 
-  float s_pre[NC][8], s_branch[NC][8];  // column sums of dx n and of g m
+  F2 s_pre[NC][4], s_branch[NC][4];  // column sums of dx n and of g m
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_branch[c][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) s_pre[c][i] = s_branch[c][i] = splat2(0.0f);
 
   // Row scalars travel a row ahead as well, in registers.
   float next_pre = 0.0f, next_post = 1.0f;
@@ -316,12 +312,19 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
   int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
   for (; row < p.M; row += stride, turn ^= 1) {
     const int64_t base = row * p.D;
+    F2 g[NC][4], dn[NC][4], n[NC][4], w[NC][4];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {  // L1 reads, under way before the wait
+      const int at = (c * TPR + tid) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[c][i] = splat2(0.0f);
+      if (p.dx != nullptr && at < p.D) load8(p.w_pre, at, w[c]);
+    }
     cp_async_wait<1>();
-    float g[NC][8], dn[NC][8], n[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[c][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) g[c][i] = splat2(0.0f);
       if (dh_out != nullptr) H::read(slots_dh, c, g[c]);
       if (p.dx != nullptr) {
         H::read(slots_h, c, n[c]);
@@ -332,26 +335,42 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
     const float rstd_pre = next_pre, rstd_post = next_post;
     fetch_rstd(row + stride);
     if (p.dx != nullptr) {
-      float dot = 0.0f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int at = (c * TPR + tid) * 8;
-        if (at >= p.D) continue;
-        float w[8];
-        load8(p.w_pre, at, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          n[c][i] *= rstd_pre;
-          s_pre[c][i] = fmaf(dn[c][i], n[c][i], s_pre[c][i]);
-          dn[c][i] *= w[i];
-          dot = fmaf(dn[c][i], n[c][i], dot);
-        }
-      }
-      dot = row_sum<TPR>(dot, sums[2 * turn]) * inv_d;
+      F2 dots = splat2(0.0f);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[c][i] = fmaf(rstd_pre, fmaf(-n[c][i], dot, dn[c][i]), g[c][i]);
+        for (int i = 0; i < 4; ++i) {
+          n[c][i] = mul2(n[c][i], splat2(rstd_pre));
+          s_pre[c][i] = fma2(dn[c][i], n[c][i], s_pre[c][i]);
+          dn[c][i] = mul2(dn[c][i], w[c][i]);
+          dots = fma2(dn[c][i], n[c][i], dots);
+        }
+      const float dot = row_sum<TPR>(dots.x + dots.y, sums[2 * turn]) * inv_d;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          g[c][i] = fma2(splat2(rstd_pre), fma2(n[c][i], splat2(-dot), dn[c][i]), g[c][i]);
+    }
+    if (branch) {  // the branch's factor scale gate w_post, likewise ahead of its wait
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int at = (c * TPR + tid) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[c][i] = splat2(p.scale);
+        if (at >= p.D) continue;
+        F2 f[4];
+        if (p.w_post != nullptr) {
+          load8(p.w_post, at, f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[c][i] = mul2(w[c][i], f[i]);
+        }
+        if (p.gate != nullptr) {
+          load8(p.gate, at, f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[c][i] = mul2(w[c][i], f[i]);
+        }
+      }
     }
     if (dh != nullptr) {
 #pragma unroll
@@ -365,46 +384,30 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
       continue;
     }
     cp_async_wait<1>();
-    float m[NC][8];
+    F2 m[NC][4];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m[c][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) m[c][i] = splat2(0.0f);
       if (need_y) Y::read(slots_y, c, m[c]);
     }
     fetch_y(row + stride);
-    float dot = 0.0f;
+    F2 dots = splat2(0.0f);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int at = (c * TPR + tid) * 8;
-      if (at >= p.D) continue;
-      float coef[8], w[8];
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) coef[i] = p.scale;
-      if (p.w_post != nullptr) {
-        load8(p.w_post, at, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) coef[i] *= w[i];
+      for (int i = 0; i < 4; ++i) {
+        m[c][i] = mul2(m[c][i], splat2(rstd_post));
+        s_branch[c][i] = fma2(g[c][i], m[c][i], s_branch[c][i]);
+        g[c][i] = mul2(g[c][i], w[c][i]);
+        dots = fma2(g[c][i], m[c][i], dots);
       }
-      if (p.gate != nullptr) {
-        load8(p.gate, at, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) coef[i] *= w[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m[c][i] *= rstd_post;
-        s_branch[c][i] = fmaf(g[c][i], m[c][i], s_branch[c][i]);
-        g[c][i] *= coef[i];
-        dot = fmaf(g[c][i], m[c][i], dot);
-      }
-    }
     if (p.w_post != nullptr) {
-      dot = row_sum<TPR>(dot, sums[2 * turn + 1]) * inv_d;
+      const float dot = row_sum<TPR>(dots.x + dots.y, sums[2 * turn + 1]) * inv_d;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[c][i] = rstd_post * fmaf(-m[c][i], dot, g[c][i]);
+        for (int i = 0; i < 4; ++i) g[c][i] = mul2(splat2(rstd_post), fma2(m[c][i], splat2(-dot), g[c][i]));
     }
     if (p.dy != nullptr) {
 #pragma unroll
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
   cp_async_wait<0>();
 
   // One partial row per CTA.  With a warp per row, the warps add theirs in turn.
-  auto put = [&](const float (&s)[NC][8], int which) {
+  auto put = [&](const F2 (&s)[NC][4], int which) {
     float* dst = p.part + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * p.D;
     for (int w = 0; w < kRows; ++w) {
       if (static_cast<int>(threadIdx.x) / TPR == w) {
@@ -425,12 +428,12 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
         for (int c = 0; c < NC; ++c) {
           const int at = (c * TPR + tid) * 8;
           if (at >= p.D) continue;
-          float o[8];
+          F2 o[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+          for (int i = 0; i < 4; ++i) o[i] = splat2(0.0f);
           if (w > 0) load8(dst, at, o);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] += s[c][i];
+          for (int i = 0; i < 4; ++i) o[i] = add2(o[i], s[c][i]);
           store8(dst, at, o);
         }
       }
