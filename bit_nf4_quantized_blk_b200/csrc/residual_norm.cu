@@ -42,6 +42,12 @@ constexpr int kNormThreads = TPR == 32 ? 32 * kWarpRowCtas : TPR;
 // Threads that share an SM: what the registers allow (about 80 and 128 per thread).
 constexpr int kFwdResident = 768, kBwdResident = 512;
 
+// Whether the backward keeps its channel factors in shared memory: read from
+// L1 for every row their latency was a third of its stalls.  The longest rows
+// leave no room.
+template <int TPR>
+constexpr bool kStash = TPR <= 512;
+
 template <int TPR, int kResident>
 constexpr int kMinCtas = kNormThreads<TPR> >= kResident ? 1 : kResident / kNormThreads<TPR>;
 
@@ -117,6 +123,12 @@ struct RowSlot {
         cp_async_16(slot + ((c * (kVecs / NC) + q) * kThreads + threadIdx.x) * 16,
                     ok ? row + at + q * (16 / static_cast<int>(sizeof(T))) : row, ok);
     }
+  }
+  __device__ static __forceinline__ void write(uint8_t* slot, int c, const F2 (&v)[4]) {
+    static_assert(sizeof(T) == 4, "fp32 slots");
+    float4* s = reinterpret_cast<float4*>(slot) + c * (kVecs / NC) * kThreads + threadIdx.x;
+    s[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    s[kThreads] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   }
   __device__ static __forceinline__ void read(const uint8_t* slot, int c, F2 (&v)[4]) {
     const uint4* s = reinterpret_cast<const uint4*>(slot) + c * (kVecs / NC) * kThreads + threadIdx.x;
@@ -255,6 +267,29 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
   cp_async_wait<0>();
 }
 
+namespace {
+
+// w_pre (0 without one) and scale gate w_post of the eight channels at `at`.
+__device__ __forceinline__ void read_factors(const ResidualNormBwd& p, int at, F2 (&pre)[4], F2 (&branch)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pre[i] = splat2(0.0f), branch[i] = splat2(p.scale);
+  if (at >= p.D) return;
+  if (p.dx != nullptr) load8(p.w_pre, at, pre);
+  F2 f[4];
+  if (p.w_post != nullptr) {
+    load8(p.w_post, at, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) branch[i] = mul2(branch[i], f[i]);
+  }
+  if (p.gate != nullptr) {
+    load8(p.gate, at, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) branch[i] = mul2(branch[i], f[i]);
+  }
+}
+
+}  // namespace
+
 template <typename TRes, int TPR, int NC>
 __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>)
     residual_norm_bwd_kernel(ResidualNormBwd p) {
@@ -265,6 +300,9 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
   uint8_t* slots_h = slots_dh + H::kBytes;
   uint8_t* slots_dx = slots_h + H::kBytes;
   uint8_t* slots_y = slots_dx + Y::kBytes;
+  using W = RowSlot<float, TPR, NC>;
+  uint8_t* factor_pre = slots_y + Y::kBytes;
+  uint8_t* factor_branch = factor_pre + W::kBytes;
   __shared__ __align__(16) float sums[4][32];
   const int tid = threadIdx.x % TPR;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
@@ -309,16 +347,27 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
   fetch(row);
   fetch_y(row);
   fetch_rstd(row);
+  // w_pre and the branch's factor scale gate w_post, each thread's own share.
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    F2 f[4], b[4];
+    read_factors(p, (c * TPR + tid) * 8, f, b);
+    if constexpr (kStash<TPR>) {
+      W::write(factor_pre, c, f);
+      W::write(factor_branch, c, b);
+    }
+  }
   int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
   for (; row < p.M; row += stride, turn ^= 1) {
     const int64_t base = row * p.D;
     F2 g[NC][4], dn[NC][4], n[NC][4], w[NC][4];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {  // L1 reads, under way before the wait
-      const int at = (c * TPR + tid) * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[c][i] = splat2(0.0f);
-      if (p.dx != nullptr && at < p.D) load8(p.w_pre, at, w[c]);
+    for (int c = 0; c < NC; ++c) {
+      F2 other[4];
+      if constexpr (kStash<TPR>)
+        W::read(factor_pre, c, w[c]);
+      else
+        read_factors(p, (c * TPR + tid) * 8, w[c], other);
     }
     cp_async_wait<1>();
 #pragma unroll
@@ -352,25 +401,13 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
         for (int i = 0; i < 4; ++i)
           g[c][i] = fma2(splat2(rstd_pre), fma2(n[c][i], splat2(-dot), dn[c][i]), g[c][i]);
     }
-    if (branch) {  // the branch's factor scale gate w_post, likewise ahead of its wait
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int at = (c * TPR + tid) * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[c][i] = splat2(p.scale);
-        if (at >= p.D) continue;
-        F2 f[4];
-        if (p.w_post != nullptr) {
-          load8(p.w_post, at, f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[c][i] = mul2(w[c][i], f[i]);
-        }
-        if (p.gate != nullptr) {
-          load8(p.gate, at, f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[c][i] = mul2(w[c][i], f[i]);
-        }
-      }
+    for (int c = 0; c < NC; ++c) {
+      F2 other[4];
+      if constexpr (kStash<TPR>)
+        W::read(factor_branch, c, w[c]);
+      else
+        read_factors(p, (c * TPR + tid) * 8, other, w[c]);
     }
     if (dh != nullptr) {
 #pragma unroll
@@ -542,7 +579,8 @@ template <typename TRes>
 cudaError_t launch_bwd(const ResidualNormBwd& p, cudaStream_t stream) {
   return with_shape(p.D, [&](auto tpr, auto nc) {
     constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
-    constexpr int smem = 2 * (RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes);
+    constexpr int smem = 2 * (RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes) +
+                         (kStash<TPR> ? 2 * RowSlot<float, TPR, NC>::kBytes : 0);
     static DeviceOnce configured;
     const int ctas = residual_norm_bwd_ctas(p.M, p.D);
     return launch_norm(residual_norm_bwd_kernel<TRes, TPR, NC>, configured, ctas, kNormThreads<TPR>, smem, p, stream);
