@@ -337,16 +337,19 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
 #pragma unroll
     for (int i = 0; i < 4; ++i) s_pre[c][i] = s_branch[c][i] = splat2(0.0f);
 
-  // Row scalars travel a row ahead as well, in registers.
-  float next_pre = 0.0f, next_post = 1.0f;
-  auto fetch_rstd = [&](int64_t next) {
-    if (next >= p.M) return;
-    if (p.dx != nullptr) next_pre = p.rstd_pre[next];
-    if (p.w_post != nullptr) next_post = p.rstd_post[next];
+  // The row scalars of 32 rows at a time, one per lane.  Loaded row by row,
+  // even a row ahead, their waits also held up the copies in flight (a fifth
+  // of the kernel's time).
+  const int lane = threadIdx.x & 31;
+  float lane_pre = 0.0f, lane_post = 1.0f;
+  auto fetch_rstd = [&](int64_t first) {
+    const int64_t r = first + lane * stride;
+    if (r >= p.M) return;
+    if (p.dx != nullptr) lane_pre = p.rstd_pre[r];
+    if (p.w_post != nullptr) lane_post = p.rstd_post[r];
   };
   fetch(row);
   fetch_y(row);
-  fetch_rstd(row);
   // w_pre and the branch's factor scale gate w_post, each thread's own share.
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -358,8 +361,10 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
     }
   }
   int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
-  for (; row < p.M; row += stride, turn ^= 1) {
+  int nth = 0;   // of 32 rows
+  for (; row < p.M; row += stride, turn ^= 1, nth = (nth + 1) & 31) {
     const int64_t base = row * p.D;
+    if (nth == 0) fetch_rstd(row);
     F2 g[NC][4], dn[NC][4], n[NC][4], w[NC][4];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -381,8 +386,8 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
       }
     }
     fetch(row + stride);
-    const float rstd_pre = next_pre, rstd_post = next_post;
-    fetch_rstd(row + stride);
+    const float rstd_pre = __shfl_sync(0xffffffffu, lane_pre, nth);
+    const float rstd_post = __shfl_sync(0xffffffffu, lane_post, nth);
     if (p.dx != nullptr) {
       F2 dots = splat2(0.0f);
 #pragma unroll
