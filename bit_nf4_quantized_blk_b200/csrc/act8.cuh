@@ -67,7 +67,7 @@ struct Act8Encoder {
   // significands are at least 2^-17 (relative) away from a rounding border.
   __device__ __forceinline__ F2 quotient(F2 n) const {
     const F2 t = mul2(n, splat2(inv));
-    return fma2(fma2(F2{-t.x, -t.y}, splat2(d), n), splat2(inv), t);
+    return fma2(fma2(t, splat2(-d), n), splat2(inv), t);
   }
 
   // Codes of four values (two packed bf16 words), value 0 in the lowest byte.

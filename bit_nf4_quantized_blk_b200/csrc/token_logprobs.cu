@@ -12,15 +12,28 @@
 // a large |m| (a row masked to the type's lowest value), their difference
 // with x is exact.
 //
-// HBM-bound: 2 or 4 bytes per logit against about 8 instructions.  The k
-// largest come from the same pass: a thread's running maximum is one
-// candidate key (value, lowest id first); the k-th largest of the keys is a
-// bound that at least k logits reach, and only the threads whose key reaches
-// it are looked through once more (their logits are in L2).
+// HBM-bound: 2 or 4 bytes per logit against about 6 instructions (packed fp32
+// pairs) and one exponential, which is the tightest unit behind HBM.  CTAs
+// stay for many rows and every thread runs its own ring of asynchronous
+// copies (cp.async into slots that it alone reads, so without barriers) across
+// the rows' ends: the next row arrives while this one is reduced.  With few
+// rows a cluster of up to 8 CTAs shares each row and joins over distributed
+// shared memory, still one launch without a workspace.
+//
+// The k largest come from the same pass.  A thread's maximum is one
+// candidate; the k-th largest of the (groups of) threads' maxima is a bound
+// that at least k logits reach, and only the threads whose maximum reaches it
+// are looked through once more (their logits are in L2).  Should ties put more
+// logits at the bound than the list holds, the bound is chosen again among
+// exact keys (value, then lowest id); should the largest logits all sit in a
+// few threads, they are taken one by one.
 //
 // The gradient  dx_j = c (g (1[j = t] - p_j) - g_H p_j (log p_j + H)) is
 // elementwise from the saved m, log s and H: one read, one write.
+#include <algorithm>
+
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.cuh"
 
 namespace qnf4 {
@@ -30,8 +43,13 @@ namespace {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpVecs = 4;       // 16-byte vectors per thread and step
+constexpr int kLpStages = 3;     // steps in flight
+constexpr int kLpPerSm = 4;      // CTAs per SM (registers and shared memory)
+constexpr int kLpMaxCluster = 8;
 constexpr int kLpGroup = 4;      // threads whose keys are joined before the bound is chosen
+constexpr int kLpGroups = kLpThreads / kLpGroup;
 constexpr int kLpList = 256;     // logits at or above the bound that are ranked directly
+constexpr int kLpRing = kLpStages * kLpVecs * kLpThreads * 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -103,6 +121,8 @@ __device__ __forceinline__ uint64_t lp_key(float v, int64_t id) {
   return (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
 }
 
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
 __device__ __forceinline__ float lp_key_value(uint64_t key) {
   const uint32_t order = static_cast<uint32_t>(key >> 32);
   if (order == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
@@ -136,11 +156,34 @@ struct LpSums {
   }
 };
 
+// Largest of one thread's packed or plain values.
+template <typename T>
+__device__ __forceinline__ float lp_max(const uint4 (&u)[kLpVecs]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t m = 0xFF80FF80u;
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[j]));
+    }
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  } else {
+    float m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i)
+      m = max_nan(max_nan(max_nan(m, __uint_as_float(u[i].x)), __uint_as_float(u[i].y)),
+                  max_nan(__uint_as_float(u[i].z), __uint_as_float(u[i].w)));
+    return m;
+  }
+}
+
 struct LpShared {
-  LpSums warp[kLpWarps];
-  LpSums row;
-  uint64_t thread_key[kLpThreads];
-  uint64_t group_key[kLpThreads / kLpGroup];
+  LpSums warp[2][kLpWarps];  // alternate from row to row
+  LpSums cta;                // this CTA's part of the row, for the cluster
+  LpSums row;                // (maximum, log sum) of the whole row
+  uint64_t top[kLogprobsMaxTop];  // this CTA's largest keys, largest first
+  uint64_t group_key[kLpGroups];
   uint64_t list[kLpList];
   uint64_t bound;
   uint64_t best[kLpWarps];
@@ -148,180 +191,285 @@ struct LpShared {
   int cands, listed;
 };
 
-}  // namespace
+// The same shared object in CTA `rank` of the cluster.
+__device__ __forceinline__ uint64_t ld_cluster_u64(const void* p, uint32_t rank) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to_cta(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(const void* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_cta(p, rank)) : "memory");
+  return v;
+}
 
+// This CTA's vectors of a row: [first, end), of which those below `whole` lie
+// within the row entirely (at most one, the row's last, does not).
+struct LpSegment {
+  int64_t first, end, whole;
+};
+
+// The k largest keys of the CTA's part of the row into sh.top, 0 past its size.
+// `m`: the thread's maximum; best_step: the first vector of the step that had it first (-1: none).
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_fwd_kernel(TokenLogprobsFwd p) {
+__device__ void lp_select(LpShared& sh, const T* row, int64_t V, const LpSegment& seg, int k, float m,
+                          int64_t best_step) {
   constexpr int P = kLpPer<T>;
-  __shared__ LpShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t r = blockIdx.x;
-  const T* row = static_cast<const T*>(p.logits) + r * p.ld;
-  const int64_t vecs = (p.V + P - 1) / P;
-  const float c2 = p.inv_temperature * kLog2e;
-
-  LpSums a{kNegInf, 0.0f, 0.0f};
-  float base = 0.0f;       // the maximum that t is relative to (0 while it is -inf)
-  int64_t best_step = -1;  // first vector of the step that holds the thread's maximum first
-  for (int64_t v0 = tid; v0 < vecs; v0 += kLpThreads * kLpVecs) {
-    uint4 u[kLpVecs];
-#pragma unroll
-    for (int i = 0; i < kLpVecs; ++i) u[i] = lp_load(row, p.V, v0 + i * kLpThreads);
-    float x[kLpVecs][P];
-    float mx = kNegInf;
-#pragma unroll
-    for (int i = 0; i < kLpVecs; ++i) {
-      lp_values<T>(u[i], x[i]);
-#pragma unroll
-      for (int j = 0; j < P; ++j) mx = max_nan(mx, x[i][j]);
-    }
-    if (best_step < 0 || (!(mx <= a.m) && a.m == a.m)) {
-      best_step = v0;
-      a.move(mx, c2);
-      base = mx == kNegInf ? 0.0f : mx;
-    }
-#pragma unroll
-    for (int i = 0; i < kLpVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        // Masked logits give t = -inf: a finite bound keeps e t = 0 there.
-        const float t = max_nan((x[i][j] - base) * c2, -1000.0f);
-        const float e = ex2(t);
-        a.s += e;
-        a.q = fmaf(e, t, a.q);
-      }
-  }
-
-  LpSums w = a;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    LpSums o{__shfl_xor_sync(0xffffffffu, w.m, d), __shfl_xor_sync(0xffffffffu, w.s, d),
-             __shfl_xor_sync(0xffffffffu, w.q, d)};
-    w.join(o, c2);
-  }
-  if (lane == 0) sh.warp[warp] = w;
-  if (tid == 0) sh.cands = sh.listed = 0;
-  __syncthreads();
-  if (tid == 0) {
-    LpSums all = sh.warp[0];
-    for (int i = 1; i < kLpWarps; ++i) all.join(sh.warp[i], c2);
-    const bool empty = all.m == kNegInf;  // every logit is -inf
-    const float log_sum = empty ? 0.0f : logf(all.s);
-    if (p.entropy != nullptr) p.entropy[r] = empty ? 0.0f : log_sum - all.q / all.s * kLn2;
-    if (p.row_max != nullptr) p.row_max[r] = all.m;
-    if (p.log_sum != nullptr) p.log_sum[r] = log_sum;
-    if (p.logprob != nullptr) {
-      const int64_t t = p.targets[r];
-      float v = 0.0f;
-      if (t >= p.V) {
-        v = __uint_as_float(0x7FC00000u);
-      } else if (t >= 0) {
-        float x;
-        if constexpr (sizeof(T) == 2)
-          x = bf16_bits_to_float(row[t]);
-        else
-          x = row[t];
-        v = (x - (empty ? 0.0f : all.m)) * p.inv_temperature - log_sum;
-      }
-      p.logprob[r] = v;
-    }
-    sh.row = LpSums{empty ? 0.0f : all.m, log_sum, 0.0f};
-  }
-  if (p.k == 0) return;
-
-  // The thread's key: its maximum and the first id that has it.
-  uint64_t key = 0;
-  if (best_step >= 0) {
-    for (int i = kLpVecs - 1; i >= 0; --i) {
-      float x[P];
-      const int64_t vec = best_step + i * kLpThreads;
-      lp_values<T>(lp_load(row, p.V, vec), x);
-#pragma unroll
-      for (int j = P - 1; j >= 0; --j)
-        if (vec * P + j < p.V && (x[j] == a.m || x[j] != x[j])) key = lp_key(x[j], vec * P + j);
-    }
-  }
-  sh.thread_key[tid] = key;
-  uint64_t gk = key;
-#pragma unroll
-  for (int d = 1; d < kLpGroup; d *= 2) {
-    const uint64_t o = __shfl_xor_sync(0xffffffffu, gk, d);
-    gk = o > gk ? o : gk;
-  }
-  if (tid % kLpGroup == 0) sh.group_key[tid / kLpGroup] = gk;
-  __syncthreads();
-  // The k-th largest group key (keys differ: each holds its own id; empty groups' zeros rank last).
-  if (tid < kLpThreads / kLpGroup) {
-    const uint64_t mine = sh.group_key[tid];
-    int above = 0;
-#pragma unroll 8
-    for (int i = 0; i < kLpThreads / kLpGroup; ++i) above += sh.group_key[i] > mine || (sh.group_key[i] == mine && i < tid);
-    if (above == p.k - 1) sh.bound = mine;
-  }
-  __syncthreads();
-  const uint64_t bound = sh.bound > 0 ? sh.bound : 1;
-  if (key >= bound) sh.cand[atomicAdd(&sh.cands, 1)] = tid;
-  __syncthreads();
-  // Every logit of the candidate threads that reaches the bound.
-  const int64_t per = (vecs + kLpThreads - 1) / kLpThreads;
-  const int64_t items = static_cast<int64_t>(sh.cands) * per;
-  for (int64_t i = tid; i < items; i += kLpThreads) {
-    const int64_t vec = sh.cand[i / per] + (i % per) * kLpThreads;
+  const uint32_t per = static_cast<uint32_t>((seg.end - seg.first + kLpThreads - 1) / kLpThreads);
+  // Item i of the candidate threads' vectors.
+  auto vector_of = [&](uint32_t i) { return seg.first + sh.cand[i / per] + static_cast<int64_t>(i % per) * kLpThreads; };
+  auto for_each_key = [&](int64_t vec, auto&& f) {
+    if (vec >= seg.end) return;
     float x[P];
-    lp_values<T>(lp_load(row, p.V, vec), x);
+    lp_values<T>(lp_load(row, V, vec), x);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const uint64_t k = lp_key(x[j], vec * P + j);
-      if (vec * P + j < p.V && k >= bound) {
-        const int at = atomicAdd(&sh.listed, 1);
-        if (at < kLpList) sh.list[at] = k;
-      }
-    }
-  }
-  __syncthreads();
-  int32_t* ids = p.top_ids + r * p.k;
-  float* lps = p.top_logprob + r * p.k;
-  auto put = [&](int rank, uint64_t k) {
-    ids[rank] = lp_key_id(k);
-    lps[rank] = (lp_key_value(k) - sh.row.m) * p.inv_temperature - sh.row.s;
+    for (int j = 0; j < P; ++j)
+      if (vec * P + j < V) f(lp_key(x[j], vec * P + j));
   };
-  const int n = sh.listed;
-  if (n <= kLpList) {
-    if (tid < n) {
-      const uint64_t mine = sh.list[tid];
-      int above = 0;
-      for (int i = 0; i < n; ++i) above += sh.list[i] > mine;
-      if (above < p.k) put(above, mine);
-    }
-    return;
-  }
-  // Too many to rank (the largest logits sit in few threads): take the
-  // largest key below the last one, k times.
-  uint64_t last = ~uint64_t{0};
-  for (int rank = 0; rank < p.k; ++rank) {
-    uint64_t best = 0;
-    for (int64_t i = tid; i < items; i += kLpThreads) {
-      const int64_t vec = sh.cand[i / per] + (i % per) * kLpThreads;
-      float x[P];
-      lp_values<T>(lp_load(row, p.V, vec), x);
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const uint64_t k = lp_key(x[j], vec * P + j);
-        if (vec * P + j < p.V && k < last && k > best) best = k;
+  if (tid < kLogprobsMaxTop) sh.top[tid] = 0;
+  uint32_t items = 0;
+  for (int exact = 0; exact < 2; ++exact) {
+    // The thread's key: by value alone (its number only tells keys apart), or the first id with its maximum.
+    uint64_t key = 0;
+    if (best_step >= 0) {
+      if (exact == 0) {
+        key = (lp_key(m, 0) & 0xFFFFFFFF00000000ull) | (0xFFFFFFFFu - tid);
+      } else {
+        for (int i = kLpVecs - 1; i >= 0; --i)
+          for_each_key(best_step + i * kLpThreads, [&](uint64_t o) { key = max_u64(key, o); });
       }
     }
+    uint64_t gk = key;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const uint64_t o = __shfl_xor_sync(0xffffffffu, best, d);
-      best = o > best ? o : best;
+    for (int d = 1; d < kLpGroup; d *= 2) gk = max_u64(gk, __shfl_xor_sync(0xffffffffu, gk, d));
+    if (tid % kLpGroup == 0) sh.group_key[tid / kLpGroup] = gk;
+    if (tid == 0) sh.cands = sh.listed = 0;
+    __syncthreads();
+    // The k-th largest group key (they differ; empty groups' zeros rank last).
+    if (tid < kLpGroups) {
+      const uint64_t mine = sh.group_key[tid];
+      int above = 0;
+#pragma unroll 8
+      for (int i = 0; i < kLpGroups; ++i) above += sh.group_key[i] > mine || (sh.group_key[i] == mine && i < tid);
+      if (above == k - 1) sh.bound = exact ? mine : mine & 0xFFFFFFFF00000000ull;
     }
+    __syncthreads();
+    const uint64_t bound = max_u64(sh.bound, 1);
+    if (key >= bound) sh.cand[atomicAdd(&sh.cands, 1)] = tid;
+    __syncthreads();
+    // Every logit of the candidate threads that reaches the bound; the order
+    // of the list does not matter, as its keys are ranked.
+    items = static_cast<uint32_t>(sh.cands) * per;
+    for (uint32_t i = tid; i < items; i += kLpThreads)
+      for_each_key(vector_of(i), [&](uint64_t o) {
+        if (o < bound) return;
+        const int at = atomicAdd(&sh.listed, 1);
+        if (at < kLpList) sh.list[at] = o;
+      });
+    __syncthreads();
+    const int n = sh.listed;
+    if (n <= kLpList) {
+      if (tid < n) {
+        const uint64_t mine = sh.list[tid];
+        int above = 0;
+        for (int i = 0; i < n; ++i) above += sh.list[i] > mine;
+        if (above < k) sh.top[above] = mine;
+      }
+      __syncthreads();
+      return;
+    }
+    __syncthreads();
+  }
+  uint64_t last = ~uint64_t{0};
+  for (int rank = 0; rank < k; ++rank) {
+    uint64_t best = 0;
+    for (uint32_t i = tid; i < items; i += kLpThreads)
+      for_each_key(vector_of(i), [&](uint64_t o) {
+        if (o < last) best = max_u64(best, o);
+      });
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) best = max_u64(best, __shfl_xor_sync(0xffffffffu, best, d));
     if (lane == 0) sh.best[warp] = best;
     __syncthreads();
     last = sh.best[0];
-    for (int i = 1; i < kLpWarps; ++i) last = sh.best[i] > last ? sh.best[i] : last;
-    if (tid == 0) put(rank, last);
+    for (int i = 1; i < kLpWarps; ++i) last = max_u64(last, sh.best[i]);
+    if (tid == 0) sh.top[rank] = last;
     __syncthreads();
   }
+}
+
+}  // namespace
+
+template <typename T, bool kTop, bool kCluster>
+__global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kernel(TokenLogprobsFwd p, int cluster) {
+  constexpr int P = kLpPer<T>;
+  extern __shared__ __align__(16) uint8_t ring[];
+  LpShared& sh = *reinterpret_cast<LpShared*>(ring + kLpRing);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = kCluster ? cluster_ctarank() : 0;
+  const int64_t stride = kCluster ? gridDim.x / cluster : gridDim.x;
+  int64_t r = kCluster ? blockIdx.x / cluster : blockIdx.x;
+  const float c2 = p.inv_temperature * kLog2e;
+  LpSegment seg;
+  {
+    const int64_t vecs = (p.V + P - 1) / P, share = kCluster ? (vecs + cluster - 1) / cluster : vecs;
+    seg.first = min(share * rank, vecs);
+    seg.end = min(seg.first + share, vecs);
+    seg.whole = min(seg.end, p.V / P);
+  }
+  const int steps = static_cast<int>((seg.end - seg.first + kLpThreads * kLpVecs - 1) / (kLpThreads * kLpVecs));
+
+  // The ring: step `next_step` of row `next_row` into the slots of stage `st`.
+  int64_t next_row = r;
+  int next_step = 0;
+  auto fetch = [&](int st) {
+    if (next_row < p.M && next_step < steps) {
+      const T* row = static_cast<const T*>(p.logits) + next_row * p.ld;
+      const int64_t v0 = seg.first + static_cast<int64_t>(next_step) * (kLpThreads * kLpVecs) + tid;
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i) {
+        const bool ok = v0 + i * kLpThreads < seg.whole;
+        cp_async_16(ring + ((st * kLpVecs + i) * kLpThreads + tid) * 16, ok ? row + (v0 + i * kLpThreads) * P : row, ok);
+      }
+      if (++next_step == steps) next_step = 0, next_row += stride;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kLpStages; ++i) fetch(i);
+  int st = 0, turn = 0;
+  // Targets and their logits of 32 rows at a time, one per lane of warp 0.
+  int64_t lane_t = -1;
+  float lane_x = 0.0f;
+  int nth = 0;
+
+  for (; r < p.M; r += stride, turn ^= 1, nth = (nth + 1) & 31) {
+    const T* row = static_cast<const T*>(p.logits) + r * p.ld;
+    if (warp == 0 && rank == 0 && p.logprob != nullptr && nth == 0) {
+      const int64_t mine = r + lane * stride;
+      if (mine < p.M) {
+        lane_t = p.targets[mine];
+        if (lane_t >= 0 && lane_t < p.V) {
+          const T x = static_cast<const T*>(p.logits)[mine * p.ld + lane_t];
+          if constexpr (sizeof(T) == 2)
+            lane_x = bf16_bits_to_float(x);
+          else
+            lane_x = x;
+        }
+      }
+    }
+    LpSums a{kNegInf, 0.0f, 0.0f};
+    F2 s2 = splat2(0.0f), q2 = splat2(0.0f);
+    float base = 0.0f;       // the maximum that t is relative to (0 while it is -inf)
+    int64_t best_step = -1;  // first vector of the step that holds the thread's maximum first
+    for (int step = 0; step < steps; ++step) {
+      const int64_t v0 = seg.first + static_cast<int64_t>(step) * (kLpThreads * kLpVecs) + tid;
+      cp_async_wait<kLpStages - 1>();
+      uint4 u[kLpVecs];
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i)
+        u[i] = *reinterpret_cast<const uint4*>(ring + ((st * kLpVecs + i) * kLpThreads + tid) * 16);
+      fetch(st);
+      st = st + 1 == kLpStages ? 0 : st + 1;
+      if (v0 + (kLpVecs - 1) * kLpThreads >= seg.whole) {  // the row's end
+#pragma unroll
+        for (int i = 0; i < kLpVecs; ++i)
+          if (v0 + i * kLpThreads >= seg.whole)
+            u[i] = v0 + i * kLpThreads < seg.end ? lp_load(row, p.V, v0 + i * kLpThreads) : lp_neg_inf<T>();
+      }
+      const float mx = lp_max<T>(u);
+      if ((best_step < 0 && v0 < seg.end) || (!(mx <= a.m) && a.m == a.m)) {
+        best_step = v0;
+        a.s = s2.x + s2.y, a.q = q2.x + q2.y;
+        a.move(mx, c2);
+        s2 = F2{a.s, 0.0f}, q2 = F2{a.q, 0.0f};
+        base = mx == kNegInf ? 0.0f : mx;
+      }
+      const F2 minus = splat2(-base), c = splat2(c2);
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i) {
+        float x[P];
+        lp_values<T>(u[i], x);
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+          // Masked logits give t = -inf: a finite bound keeps e t = 0 there.
+          F2 tt = mul2(add2(F2{x[j], x[j + 1]}, minus), c);
+          tt = F2{max_nan(tt.x, -1000.0f), max_nan(tt.y, -1000.0f)};
+          const F2 e{ex2(tt.x), ex2(tt.y)};
+          s2 = add2(s2, e);
+          q2 = fma2(e, tt, q2);
+        }
+      }
+    }
+    a.s = s2.x + s2.y, a.q = q2.x + q2.y;
+
+    LpSums w = a;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      LpSums o{__shfl_xor_sync(0xffffffffu, w.m, d), __shfl_xor_sync(0xffffffffu, w.s, d),
+               __shfl_xor_sync(0xffffffffu, w.q, d)};
+      w.join(o, c2);
+    }
+    if (lane == 0) sh.warp[turn][warp] = w;
+    __syncthreads();
+    LpSums all;  // of the CTA, in thread 0
+    const int64_t t = __shfl_sync(0xffffffffu, lane_t, nth);
+    const float target = __shfl_sync(0xffffffffu, lane_x, nth);
+    if (tid == 0) {
+      all = sh.warp[turn][0];
+      for (int i = 1; i < kLpWarps; ++i) all.join(sh.warp[turn][i], c2);
+      if (kCluster) sh.cta = all;
+    }
+    if constexpr (kTop) lp_select<T>(sh, row, p.V, seg, p.k, a.m, best_step);
+    if constexpr (kCluster) {
+      __syncwarp();
+      cluster_sync();  // every CTA's sums and keys are written
+      if (rank == 0 && tid == 0)
+        for (int i = 1; i < cluster; ++i)
+          all.join(LpSums{ld_cluster_f32(&sh.cta.m, i), ld_cluster_f32(&sh.cta.s, i), ld_cluster_f32(&sh.cta.q, i)}, c2);
+    }
+    if (rank == 0 && tid == 0) {
+      const bool empty = all.m == kNegInf;  // every logit is -inf
+      const float log_sum = empty ? 0.0f : logf(all.s);
+      const float m = empty ? 0.0f : all.m;
+      if (p.entropy != nullptr) p.entropy[r] = empty ? 0.0f : log_sum - all.q / all.s * kLn2;
+      if (p.row_max != nullptr) p.row_max[r] = all.m;
+      if (p.log_sum != nullptr) p.log_sum[r] = log_sum;
+      if (p.logprob != nullptr)
+        p.logprob[r] = t < 0 ? 0.0f
+                       : t >= p.V ? __uint_as_float(0x7FC00000u)
+                                  : (target - m) * p.inv_temperature - log_sum;
+      if (kTop) sh.row = LpSums{m, log_sum, 0.0f};
+    }
+    if constexpr (kTop) {
+      // The keys of every CTA; rank 0 ranks them.
+      const int n = kCluster ? cluster * p.k : p.k;
+      uint64_t mine = 0;
+      if (rank == 0 && tid < n) mine = kCluster ? ld_cluster_u64(&sh.top[tid % p.k], tid / p.k) : sh.top[tid];
+      if (rank == 0) {
+        __syncthreads();  // sh.row; the list is free
+        if (kCluster && tid < n) sh.list[tid] = mine;
+        if (kCluster) __syncthreads();
+        int above = tid;
+        if (kCluster) {
+          above = 0;
+          if (mine != 0)
+            for (int i = 0; i < n; ++i) above += sh.list[i] > mine;
+        }
+        if (tid < n && mine != 0 && above < p.k) {
+          p.top_ids[r * p.k + above] = lp_key_id(mine);
+          p.top_logprob[r * p.k + above] = (lp_key_value(mine) - sh.row.m) * p.inv_temperature - sh.row.s;
+        }
+        if (!kCluster) __syncthreads();  // before the next row's keys
+      }
+    }
+    if constexpr (kCluster) {
+      __syncwarp();
+      cluster_sync();  // the other CTAs' shared memory is read no more
+    }
+  }
+  cp_async_wait<0>();
 }
 
 template <typename T>
@@ -372,13 +520,48 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(TokenLog
   }
 }
 
+namespace {
+
+template <typename T, bool kTop, bool kCluster>
+cudaError_t launch_fwd(const TokenLogprobsFwd& p, int cluster, cudaStream_t stream) {
+  constexpr int smem = kLpRing + static_cast<int>(sizeof(LpShared));
+  const auto kernel = token_logprobs_fwd_kernel<T, kTop, kCluster>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static DeviceOnce configured;
+  e = configured.run(dev, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t config{};
+  const int64_t rows = kCluster ? p.M : std::min<int64_t>(p.M, 148 * kLpPerSm);
+  config.gridDim = dim3(static_cast<unsigned>(rows * cluster));
+  config.blockDim = dim3(kLpThreads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  config.attrs = attr;
+  config.numAttrs = kCluster ? 1 : 0;
+  return cudaLaunchKernelEx(&config, kernel, p, cluster);
+}
+
+template <typename T>
+cudaError_t launch_fwd_type(const TokenLogprobsFwd& p, cudaStream_t stream) {
+  // CTAs per row: a power of two that keeps the machine's CTA slots filled
+  // without a second wave, and gives each CTA a full step at least.
+  const int64_t step = kLpThreads * kLpVecs * kLpPer<T>;
+  int cluster = 1;
+  while (cluster < kLpMaxCluster && p.M * cluster * 2 <= 148 * kLpPerSm && p.V >= step * cluster * 2) cluster *= 2;
+  if (p.k > 0)
+    return cluster > 1 ? launch_fwd<T, true, true>(p, cluster, stream) : launch_fwd<T, true, false>(p, 1, stream);
+  return cluster > 1 ? launch_fwd<T, false, true>(p, cluster, stream) : launch_fwd<T, false, false>(p, 1, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_token_logprobs_fwd(const TokenLogprobsFwd& p, int fp32, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(p.M);
-  if (fp32)
-    token_logprobs_fwd_kernel<float><<<grid, kLpThreads, 0, stream>>>(p);
-  else
-    token_logprobs_fwd_kernel<uint16_t><<<grid, kLpThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return fp32 ? launch_fwd_type<float>(p, stream) : launch_fwd_type<uint16_t>(p, stream);
 }
 
 cudaError_t launch_token_logprobs_bwd(TokenLogprobsBwd p, int fp32, cudaStream_t stream) {
