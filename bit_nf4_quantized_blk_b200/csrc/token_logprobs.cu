@@ -31,6 +31,7 @@
 // The gradient  dx_j = c (g (1[j = t] - p_j) - g_H p_j (log p_j + H)) is
 // elementwise from the saved m, log s and H: one read, one write.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -178,6 +179,22 @@ __device__ __forceinline__ float lp_max(const uint4 (&u)[kLpVecs]) {
   }
 }
 
+// The sums of the 2^n lanes around this one, in each of them: the maximum
+// first, so that every lane moves its sums once.
+template <int kLanes>
+__device__ __forceinline__ LpSums lp_join_lanes(LpSums a, float c2) {
+  float m = a.m;
+#pragma unroll
+  for (int d = kLanes / 2; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+  a.move(m, c2);
+#pragma unroll
+  for (int d = kLanes / 2; d > 0; d >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, d);
+    a.q += __shfl_xor_sync(0xffffffffu, a.q, d);
+  }
+  return a;
+}
+
 struct LpShared {
   LpSums warp[2][kLpWarps];  // alternate from row to row
   LpSums cta;                // this CTA's part of the row, for the cluster
@@ -219,13 +236,14 @@ __device__ void lp_select(LpShared& sh, const T* row, int64_t V, const LpSegment
   const uint32_t per = static_cast<uint32_t>((seg.end - seg.first + kLpThreads - 1) / kLpThreads);
   // Item i of the candidate threads' vectors.
   auto vector_of = [&](uint32_t i) { return seg.first + sh.cand[i / per] + static_cast<int64_t>(i % per) * kLpThreads; };
-  auto for_each_key = [&](int64_t vec, auto&& f) {
+  // f(key) of the vector's logits that are not below `least`.
+  auto for_each_key = [&](int64_t vec, float least, auto&& f) {
     if (vec >= seg.end) return;
     float x[P];
     lp_values<T>(lp_load(row, V, vec), x);
 #pragma unroll
     for (int j = 0; j < P; ++j)
-      if (vec * P + j < V) f(lp_key(x[j], vec * P + j));
+      if (!(x[j] < least) && vec * P + j < V) f(lp_key(x[j], vec * P + j));
   };
   if (tid < kLogprobsMaxTop) sh.top[tid] = 0;
   uint32_t items = 0;
@@ -237,7 +255,7 @@ __device__ void lp_select(LpShared& sh, const T* row, int64_t V, const LpSegment
         key = (lp_key(m, 0) & 0xFFFFFFFF00000000ull) | (0xFFFFFFFFu - tid);
       } else {
         for (int i = kLpVecs - 1; i >= 0; --i)
-          for_each_key(best_step + i * kLpThreads, [&](uint64_t o) { key = max_u64(key, o); });
+          for_each_key(best_step + i * kLpThreads, kNegInf, [&](uint64_t o) { key = max_u64(key, o); });
       }
     }
     uint64_t gk = key;
@@ -256,13 +274,14 @@ __device__ void lp_select(LpShared& sh, const T* row, int64_t V, const LpSegment
     }
     __syncthreads();
     const uint64_t bound = max_u64(sh.bound, 1);
+    const float least = sh.bound > 1 ? lp_key_value(bound) : kNegInf;  // NaN: every value passes, and is ranked by key
     if (key >= bound) sh.cand[atomicAdd(&sh.cands, 1)] = tid;
     __syncthreads();
     // Every logit of the candidate threads that reaches the bound; the order
     // of the list does not matter, as its keys are ranked.
     items = static_cast<uint32_t>(sh.cands) * per;
     for (uint32_t i = tid; i < items; i += kLpThreads)
-      for_each_key(vector_of(i), [&](uint64_t o) {
+      for_each_key(vector_of(i), least, [&](uint64_t o) {
         if (o < bound) return;
         const int at = atomicAdd(&sh.listed, 1);
         if (at < kLpList) sh.list[at] = o;
@@ -285,7 +304,7 @@ __device__ void lp_select(LpShared& sh, const T* row, int64_t V, const LpSegment
   for (int rank = 0; rank < k; ++rank) {
     uint64_t best = 0;
     for (uint32_t i = tid; i < items; i += kLpThreads)
-      for_each_key(vector_of(i), [&](uint64_t o) {
+      for_each_key(vector_of(i), kNegInf, [&](uint64_t o) {
         if (o < last) best = max_u64(best, o);
       });
 #pragma unroll
@@ -319,20 +338,37 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
     seg.whole = min(seg.end, p.V / P);
   }
   const int steps = static_cast<int>((seg.end - seg.first + kLpThreads * kLpVecs - 1) / (kLpThreads * kLpVecs));
+  const int full = static_cast<int>((seg.whole - seg.first) / (kLpThreads * kLpVecs));  // steps without a ragged end
+  const uint32_t slots = smem_u32(ring) + tid * 16;  // this thread's; kLpThreads * 16 apart
 
-  // The ring: step `next_step` of row `next_row` into the slots of stage `st`.
+  // The ring: step `next_step` of row `next_row` into stage `st`.
   int64_t next_row = r;
   int next_step = 0;
+  const uint8_t* const start = static_cast<const uint8_t*>(p.logits) + (seg.first + tid) * 16;
+  const uint8_t* src = start + r * p.ld * static_cast<int64_t>(sizeof(T));
   auto fetch = [&](int st) {
-    if (next_row < p.M && next_step < steps) {
-      const T* row = static_cast<const T*>(p.logits) + next_row * p.ld;
-      const int64_t v0 = seg.first + static_cast<int64_t>(next_step) * (kLpThreads * kLpVecs) + tid;
+    if (next_row < p.M) {
+      const uint32_t dst = slots + st * (kLpVecs * kLpThreads * 16);
+      if (next_step < full) {
 #pragma unroll
-      for (int i = 0; i < kLpVecs; ++i) {
-        const bool ok = v0 + i * kLpThreads < seg.whole;
-        cp_async_16(ring + ((st * kLpVecs + i) * kLpThreads + tid) * 16, ok ? row + (v0 + i * kLpThreads) * P : row, ok);
+        for (int i = 0; i < kLpVecs; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * (kLpThreads * 16)),
+                       "l"(src + i * (kLpThreads * 16))
+                       : "memory");
+      } else {
+        const int64_t v0 = seg.first + static_cast<int64_t>(next_step) * (kLpThreads * kLpVecs) + tid;
+#pragma unroll
+        for (int i = 0; i < kLpVecs; ++i)
+          if (v0 + i * kLpThreads < seg.whole)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * (kLpThreads * 16)),
+                         "l"(src + i * (kLpThreads * 16))
+                         : "memory");
       }
-      if (++next_step == steps) next_step = 0, next_row += stride;
+      src += kLpVecs * kLpThreads * 16;
+      if (++next_step == steps) {
+        next_step = 0, next_row += stride;
+        src = start + next_row * p.ld * static_cast<int64_t>(sizeof(T));
+      }
     }
     cp_async_commit();
   };
@@ -363,8 +399,28 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
     F2 s2 = splat2(0.0f), q2 = splat2(0.0f);
     float base = 0.0f;       // the maximum that t is relative to (0 while it is -inf)
     int64_t best_step = -1;  // first vector of the step that holds the thread's maximum first
-    for (int step = 0; step < steps; ++step) {
-      const int64_t v0 = seg.first + static_cast<int64_t>(step) * (kLpThreads * kLpVecs) + tid;
+    // Adds one vector; kMasked: with a lower bound on t that keeps e t = 0
+    // for masked logits (t = -inf), which one more instruction per value buys.
+    auto add = [&](auto masked, const uint4& u) {
+      float x[P];
+      lp_values<T>(u, x);
+#pragma unroll
+      for (int j = 0; j < P; j += 2) {
+        F2 tt = mul2(add2(F2{x[j], x[j + 1]}, splat2(-base)), splat2(c2));
+        if constexpr (decltype(masked)::value) tt = F2{max_nan(tt.x, -1000.0f), max_nan(tt.y, -1000.0f)};
+        const F2 e{ex2(tt.x), ex2(tt.y)};
+        s2 = add2(s2, e);
+        q2 = fma2(e, tt, q2);
+      }
+    };
+    auto raise = [&](float mx, int64_t v0) {  // take in a step's maximum
+      best_step = v0;
+      a.s = s2.x + s2.y, a.q = q2.x + q2.y;
+      a.move(mx, c2);
+      s2 = F2{a.s, 0.0f}, q2 = F2{a.q, 0.0f};
+      base = mx == kNegInf ? 0.0f : mx;
+    };
+    for (int step = 0; step < full; ++step) {
       cp_async_wait<kLpStages - 1>();
       uint4 u[kLpVecs];
 #pragma unroll
@@ -372,54 +428,52 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
         u[i] = *reinterpret_cast<const uint4*>(ring + ((st * kLpVecs + i) * kLpThreads + tid) * 16);
       fetch(st);
       st = st + 1 == kLpStages ? 0 : st + 1;
-      if (v0 + (kLpVecs - 1) * kLpThreads >= seg.whole) {  // the row's end
-#pragma unroll
-        for (int i = 0; i < kLpVecs; ++i)
-          if (v0 + i * kLpThreads >= seg.whole)
-            u[i] = v0 + i * kLpThreads < seg.end ? lp_load(row, p.V, v0 + i * kLpThreads) : lp_neg_inf<T>();
-      }
       const float mx = lp_max<T>(u);
-      if ((best_step < 0 && v0 < seg.end) || (!(mx <= a.m) && a.m == a.m)) {
-        best_step = v0;
-        a.s = s2.x + s2.y, a.q = q2.x + q2.y;
-        a.move(mx, c2);
-        s2 = F2{a.s, 0.0f}, q2 = F2{a.q, 0.0f};
-        base = mx == kNegInf ? 0.0f : mx;
-      }
-      const F2 minus = splat2(-base), c = splat2(c2);
+      if (best_step < 0 || (!(mx <= a.m) && a.m == a.m))
+        raise(mx, seg.first + static_cast<int64_t>(step) * (kLpThreads * kLpVecs) + tid);
+      const F2 s0 = s2, q0 = q2;
 #pragma unroll
+      for (int i = 0; i < kLpVecs; ++i) add(std::false_type{}, u[i]);
+      if (q2.x + q2.y != q2.x + q2.y) {  // a masked logit (or a NaN, which stays one)
+        s2 = s0, q2 = q0;
+#pragma unroll
+        for (int i = 0; i < kLpVecs; ++i) add(std::true_type{}, u[i]);
+      }
+    }
+    if (full < steps) {  // the row's end
+      const int64_t v0 = seg.first + static_cast<int64_t>(full) * (kLpThreads * kLpVecs) + tid;
+      cp_async_wait<kLpStages - 1>();
+#pragma unroll 1
       for (int i = 0; i < kLpVecs; ++i) {
+        const int64_t vec = v0 + i * kLpThreads;
+        if (vec >= seg.end) break;
+        const uint4 u = vec < seg.whole
+                            ? *reinterpret_cast<const uint4*>(ring + ((st * kLpVecs + i) * kLpThreads + tid) * 16)
+                            : lp_load(row, p.V, vec);
         float x[P];
-        lp_values<T>(u[i], x);
+        lp_values<T>(u, x);
+        float mx = x[0];
 #pragma unroll
-        for (int j = 0; j < P; j += 2) {
-          // Masked logits give t = -inf: a finite bound keeps e t = 0 there.
-          F2 tt = mul2(add2(F2{x[j], x[j + 1]}, minus), c);
-          tt = F2{max_nan(tt.x, -1000.0f), max_nan(tt.y, -1000.0f)};
-          const F2 e{ex2(tt.x), ex2(tt.y)};
-          s2 = add2(s2, e);
-          q2 = fma2(e, tt, q2);
-        }
+        for (int j = 1; j < P; ++j) mx = max_nan(mx, x[j]);
+        if (best_step < 0 || (!(mx <= a.m) && a.m == a.m)) raise(mx, v0);
+        add(std::true_type{}, u);
       }
+      fetch(st);
+      st = st + 1 == kLpStages ? 0 : st + 1;
     }
     a.s = s2.x + s2.y, a.q = q2.x + q2.y;
 
-    LpSums w = a;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      LpSums o{__shfl_xor_sync(0xffffffffu, w.m, d), __shfl_xor_sync(0xffffffffu, w.s, d),
-               __shfl_xor_sync(0xffffffffu, w.q, d)};
-      w.join(o, c2);
-    }
+    const LpSums w = lp_join_lanes<32>(a, c2);
     if (lane == 0) sh.warp[turn][warp] = w;
     __syncthreads();
-    LpSums all;  // of the CTA, in thread 0
-    const int64_t t = __shfl_sync(0xffffffffu, lane_t, nth);
-    const float target = __shfl_sync(0xffffffffu, lane_x, nth);
-    if (tid == 0) {
-      all = sh.warp[turn][0];
-      for (int i = 1; i < kLpWarps; ++i) all.join(sh.warp[turn][i], c2);
-      if (kCluster) sh.cta = all;
+    LpSums all{kNegInf, 0.0f, 0.0f};  // of the CTA, in warp 0
+    int64_t t = -1;
+    float target = 0.0f;
+    if (warp == 0) {
+      all = lp_join_lanes<kLpWarps>(sh.warp[turn][lane % kLpWarps], c2);
+      t = __shfl_sync(0xffffffffu, lane_t, nth);
+      target = __shfl_sync(0xffffffffu, lane_x, nth);
+      if (kCluster && lane == 0) sh.cta = all;
     }
     if constexpr (kTop) lp_select<T>(sh, row, p.V, seg, p.k, a.m, best_step);
     if constexpr (kCluster) {
