@@ -20,13 +20,13 @@
 // rows a cluster of up to 8 CTAs shares each row and joins over distributed
 // shared memory, still one launch without a workspace.
 //
-// The k largest come from the same pass.  A thread's maximum is one
-// candidate; the k-th largest of the (groups of) threads' maxima is a bound
-// that at least k logits reach, and only the threads whose maximum reaches it
-// are looked through once more (their logits are in L2).  Should ties put more
-// logits at the bound than the list holds, the bound is chosen again among
-// exact keys (value, then lowest id); should the largest logits all sit in a
-// few threads, they are taken one by one.
+// The k largest come from the same pass.  The k-th largest (or a little less)
+// of the threads' maxima is a bound that at least k logits reach, and only the
+// vectors of the threads whose maximum reaches it are looked through once more
+// (they are in L2).  Should ties put more logits at the bound than the list
+// holds, those above the bound are ranked and the rest taken from the row's
+// start, where the lowest ids are; should that many be above it (the largest
+// logits sitting in a few threads), they are taken one by one.
 //
 // The gradient  dx_j = c (g (1[j = t] - p_j) - g_H p_j (log p_j + H)) is
 // elementwise from the saved m, log s and H: one read, one write.
@@ -47,8 +47,6 @@ constexpr int kLpVecs = 4;       // 16-byte vectors per thread and step
 constexpr int kLpStages = 3;     // steps in flight
 constexpr int kLpPerSm = 4;      // CTAs per SM (registers and shared memory)
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpGroup = 4;      // threads whose keys are joined before the bound is chosen
-constexpr int kLpGroups = kLpThreads / kLpGroup;
 constexpr int kLpList = 256;     // logits at or above the bound that are ranked directly
 constexpr int kLpRing = kLpStages * kLpVecs * kLpThreads * 16;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -114,12 +112,15 @@ __device__ __forceinline__ uint4 lp_load(const T* row, int64_t V, int64_t vec) {
   return u;
 }
 
-// (value, id) as one key: larger values first, the lower id first among
-// equals (-0 = 0), NaN above everything.  0 is below every key.
-__device__ __forceinline__ uint64_t lp_key(float v, int64_t id) {
+// Unsigned integers in the order of the values (-0 = 0, NaN above everything; never 0).
+__device__ __forceinline__ uint32_t lp_order(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  const uint32_t order = v != v ? 0xFFFFFFFFu : (u >> 31) ? ~u : (u | 0x80000000u);
-  return (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+  return v != v ? 0xFFFFFFFFu : (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+// (value, id) as one key: larger values first, the lower id first among equals.  0 is below every key.
+__device__ __forceinline__ uint64_t lp_key(float v, int64_t id) {
+  return (static_cast<uint64_t>(lp_order(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
 }
 
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
@@ -128,6 +129,12 @@ __device__ __forceinline__ float lp_key_value(uint64_t key) {
   const uint32_t order = static_cast<uint32_t>(key >> 32);
   if (order == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
   return __uint_as_float((order >> 31) ? (order & 0x7FFFFFFFu) : ~order);
+}
+
+// A value such that everything of order `bound` or more is not below it (NaN, not below which is everything, at the top).
+__device__ __forceinline__ float lp_least(uint32_t bound) {
+  if (bound <= 0x007FFFFFu) return kNegInf;
+  return lp_key_value(static_cast<uint64_t>(bound) << 32);
 }
 
 __device__ __forceinline__ int lp_key_id(uint64_t key) {
@@ -147,13 +154,6 @@ struct LpSums {
       s *= a;
     }
     m = to;
-  }
-  __device__ __forceinline__ void join(LpSums o, float c2) {
-    const float to = max_nan(m, o.m);
-    move(to, c2);
-    o.move(to, c2);
-    s += o.s;
-    q += o.q;
   }
 };
 
@@ -196,16 +196,16 @@ __device__ __forceinline__ LpSums lp_join_lanes(LpSums a, float c2) {
 }
 
 struct LpShared {
-  LpSums warp[2][kLpWarps];  // alternate from row to row
+  LpSums warp[2][kLpWarps];  // alternate from row to row, as the counts do
   LpSums cta;                // this CTA's part of the row, for the cluster
   LpSums row;                // (maximum, log sum) of the whole row
-  uint64_t top[kLogprobsMaxTop];  // this CTA's largest keys, largest first
-  uint64_t group_key[kLpGroups];
+  uint64_t top[kLogprobsMaxTop];  // this CTA's largest keys, largest first, for the cluster
   uint64_t list[kLpList];
-  uint64_t bound;
   uint64_t best[kLpWarps];
-  int cand[kLpThreads];
-  int cands, listed;
+  uint32_t order[kLpThreads];  // the threads' maxima, as lp_order
+  uint32_t bound;
+  int listed[2], cands[2];
+  uint8_t cand[kLpThreads];
 };
 
 // The same shared object in CTA `rank` of the cluster.
@@ -226,94 +226,147 @@ struct LpSegment {
   int64_t first, end, whole;
 };
 
-// The k largest keys of the CTA's part of the row into sh.top, 0 past its size.
-// `m`: the thread's maximum; best_step: the first vector of the step that had it first (-1: none).
-template <typename T>
-__device__ void lp_select(LpShared& sh, const T* row, int64_t V, const LpSegment& seg, int k, float m,
-                          int64_t best_step) {
+// A value that at least k of the warp's 32 N values reach, found bit by bit
+// from the top: the k-th largest itself, or, with `slack`, the first one on
+// the way that no more than k + slack reach.
+template <int N>
+__device__ __forceinline__ uint32_t lp_bound(const uint32_t (&v)[N], int k, int slack) {
+  uint32_t bound = 0;
+  for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+    const uint32_t at = bound | bit;
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine += v[i] >= at;
+    const int n = __reduce_add_sync(0xffffffffu, mine);
+    if (n < k) continue;
+    bound = at;
+    if (n <= k + slack) break;
+  }
+  return bound;
+}
+
+// The bound of the threads' maxima, by one warp.
+__device__ __forceinline__ uint32_t lp_threads_bound(const LpShared& sh, int k, int slack) {
+  uint32_t v[kLpThreads / 32];
+#pragma unroll
+  for (int i = 0; i < kLpThreads / 32; ++i) v[i] = sh.order[i * 32 + (threadIdx.x & 31)];
+  return lp_bound(v, k, slack);
+}
+
+// Lists the threads whose maximum reaches the bound (their number is *cands, zero before).
+__device__ __forceinline__ void lp_candidates(LpShared& sh, uint32_t order, uint32_t bound, int* cands) {
+  const uint32_t in = __ballot_sync(0xffffffffu, order >= bound);
+  if (in == 0) return;
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+  if (lane == 0) at = atomicAdd(cands, __popc(in));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(in & ((1u << lane) - 1u));
+  if ((in >> lane) & 1) sh.cand[at] = static_cast<uint8_t>(threadIdx.x);
+}
+
+// f(value, id) of the logits that are not below `least` in the vectors of the
+// `cands` listed threads, by the whole CTA; thread c has the vectors
+// seg.first + c, + kLpThreads, ...
+template <typename T, typename F>
+__device__ __forceinline__ void lp_scan(const LpShared& sh, const T* row, int64_t V, const LpSegment& seg, int cands,
+                                        float least, F&& f) {
   constexpr int P = kLpPer<T>;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t per = static_cast<uint32_t>((seg.end - seg.first + kLpThreads - 1) / kLpThreads);
-  // Item i of the candidate threads' vectors.
-  auto vector_of = [&](uint32_t i) { return seg.first + sh.cand[i / per] + static_cast<int64_t>(i % per) * kLpThreads; };
-  // f(key) of the vector's logits that are not below `least`.
-  auto for_each_key = [&](int64_t vec, float least, auto&& f) {
-    if (vec >= seg.end) return;
+  const uint32_t per = static_cast<uint32_t>((seg.end - seg.first + kLpThreads - 1) / kLpThreads), items = cands * per;
+#pragma unroll 1
+  for (uint32_t i = threadIdx.x; i < items; i += kLpThreads) {
+    const uint32_t c = i / per;
+    const int64_t vec = seg.first + sh.cand[c] + static_cast<int64_t>(i - c * per) * kLpThreads;
+    if (vec >= seg.end) continue;
     float x[P];
     lp_values<T>(lp_load(row, V, vec), x);
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < P; ++j) any = any || !(x[j] < least);
+    if (!any) continue;
 #pragma unroll
     for (int j = 0; j < P; ++j)
-      if (!(x[j] < least) && vec * P + j < V) f(lp_key(x[j], vec * P + j));
-  };
-  if (tid < kLogprobsMaxTop) sh.top[tid] = 0;
-  uint32_t items = 0;
-  for (int exact = 0; exact < 2; ++exact) {
-    // The thread's key: by value alone (its number only tells keys apart), or the first id with its maximum.
-    uint64_t key = 0;
-    if (best_step >= 0) {
-      if (exact == 0) {
-        key = (lp_key(m, 0) & 0xFFFFFFFF00000000ull) | (0xFFFFFFFFu - tid);
-      } else {
-        for (int i = kLpVecs - 1; i >= 0; --i)
-          for_each_key(best_step + i * kLpThreads, kNegInf, [&](uint64_t o) { key = max_u64(key, o); });
-      }
-    }
-    uint64_t gk = key;
+      if (!(x[j] < least) && vec * P + j < V) f(x[j], vec * P + j);
+  }
+}
+
+// put(rank, key) of the keys in the list that fewer than k exceed.
+template <typename F>
+__device__ __forceinline__ void lp_rank_list(const LpShared& sh, int n, int k, int first, int stride, F&& put) {
+  for (int i = first; i < n; i += stride) {
+    const uint64_t mine = sh.list[i];
+    int larger = 0;
+#pragma unroll 4
+    for (int o = 0; o < n; ++o) larger += sh.list[o] > mine;
+    if (larger < k) put(larger, mine);
+  }
+}
+
+// The k largest when more logits than the list holds reach the bound.
+template <typename T, typename F>
+__device__ void lp_select_many(LpShared& sh, const T* row, int64_t V, const LpSegment& seg, int k, uint32_t order,
+                               int turn, F&& put) {
+  constexpr int P = kLpPer<T>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __syncthreads();  // everyone has read the count
+  if (warp == 0) {
+    const uint32_t exact = lp_threads_bound(sh, k, 0);
+    if (lane == 0) sh.bound = exact, sh.listed[turn] = sh.cands[turn] = 0;
+  }
+  __syncthreads();
+  const uint32_t bound = sh.bound;
+  const float least = lp_least(bound);
+  lp_candidates(sh, order, bound, &sh.cands[turn]);
+  __syncthreads();
+  const int cands = sh.cands[turn];
+  lp_scan(sh, row, V, seg, cands, least, [&](float x, int64_t id) {
+    if (lp_order(x) <= bound) return;
+    const int at = atomicAdd(&sh.listed[turn], 1);
+    if (at < kLpList) sh.list[at] = lp_key(x, id);
+  });
+  __syncthreads();
+  int n = sh.listed[turn];
+  if (n <= kLpList) {
+    lp_rank_list(sh, n, k, tid, kLpThreads, put);
+    if (warp == 0) {  // then the lowest ids at the bound
+      for (int64_t v = seg.first + lane; n < k && v - lane < seg.end; v += 32) {
+        float x[P];
+        lp_values<T>(v < seg.end ? lp_load(row, V, v) : lp_neg_inf<T>(), x);
+        int mine = 0;
 #pragma unroll
-    for (int d = 1; d < kLpGroup; d *= 2) gk = max_u64(gk, __shfl_xor_sync(0xffffffffu, gk, d));
-    if (tid % kLpGroup == 0) sh.group_key[tid / kLpGroup] = gk;
-    if (tid == 0) sh.cands = sh.listed = 0;
-    __syncthreads();
-    // The k-th largest group key (they differ; empty groups' zeros rank last).
-    if (tid < kLpGroups) {
-      const uint64_t mine = sh.group_key[tid];
-      int above = 0;
-#pragma unroll 8
-      for (int i = 0; i < kLpGroups; ++i) above += sh.group_key[i] > mine || (sh.group_key[i] == mine && i < tid);
-      if (above == k - 1) sh.bound = exact ? mine : mine & 0xFFFFFFFF00000000ull;
-    }
-    __syncthreads();
-    const uint64_t bound = max_u64(sh.bound, 1);
-    const float least = sh.bound > 1 ? lp_key_value(bound) : kNegInf;  // NaN: every value passes, and is ranked by key
-    if (key >= bound) sh.cand[atomicAdd(&sh.cands, 1)] = tid;
-    __syncthreads();
-    // Every logit of the candidate threads that reaches the bound; the order
-    // of the list does not matter, as its keys are ranked.
-    items = static_cast<uint32_t>(sh.cands) * per;
-    for (uint32_t i = tid; i < items; i += kLpThreads)
-      for_each_key(vector_of(i), least, [&](uint64_t o) {
-        if (o < bound) return;
-        const int at = atomicAdd(&sh.listed, 1);
-        if (at < kLpList) sh.list[at] = o;
-      });
-    __syncthreads();
-    const int n = sh.listed;
-    if (n <= kLpList) {
-      if (tid < n) {
-        const uint64_t mine = sh.list[tid];
-        int above = 0;
-        for (int i = 0; i < n; ++i) above += sh.list[i] > mine;
-        if (above < k) sh.top[above] = mine;
+        for (int j = 0; j < P; ++j) mine += v < seg.end && v * P + j < V && lp_order(x[j]) == bound;
+        int upto = mine;  // of the lanes up to this one
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int o = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += o;
+        }
+        int at = n + upto - mine;
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          if (v < seg.end && v * P + j < V && lp_order(x[j]) == bound) {
+            if (at < k) put(at, lp_key(x[j], v * P + j));
+            ++at;
+          }
+        n += __shfl_sync(0xffffffffu, upto, 31);
       }
-      __syncthreads();
-      return;
     }
-    __syncthreads();
+    return;
   }
   uint64_t last = ~uint64_t{0};
   for (int rank = 0; rank < k; ++rank) {
     uint64_t best = 0;
-    for (uint32_t i = tid; i < items; i += kLpThreads)
-      for_each_key(vector_of(i), kNegInf, [&](uint64_t o) {
-        if (o < last) best = max_u64(best, o);
-      });
+    lp_scan(sh, row, V, seg, cands, least, [&](float x, int64_t id) {
+      const uint64_t key = lp_key(x, id);
+      if (key < last) best = max_u64(best, key);
+    });
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) best = max_u64(best, __shfl_xor_sync(0xffffffffu, best, d));
     if (lane == 0) sh.best[warp] = best;
     __syncthreads();
     last = sh.best[0];
+#pragma unroll
     for (int i = 1; i < kLpWarps; ++i) last = max_u64(last, sh.best[i]);
-    if (tid == 0) sh.top[rank] = last;
+    if (tid == 0) put(rank, last);
     __syncthreads();
   }
 }
@@ -398,7 +451,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
     LpSums a{kNegInf, 0.0f, 0.0f};
     F2 s2 = splat2(0.0f), q2 = splat2(0.0f);
     float base = 0.0f;       // the maximum that t is relative to (0 while it is -inf)
-    int64_t best_step = -1;  // first vector of the step that holds the thread's maximum first
     // Adds one vector; kMasked: with a lower bound on t that keeps e t = 0
     // for masked logits (t = -inf), which one more instruction per value buys.
     auto add = [&](auto masked, const uint4& u) {
@@ -413,12 +465,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
         q2 = fma2(e, tt, q2);
       }
     };
-    auto raise = [&](float mx, int64_t v0) {  // take in a step's maximum
-      best_step = v0;
+    auto raise = [&](float mx) {  // take in a step's maximum
+      if (mx <= a.m || a.m != a.m) return;
       a.s = s2.x + s2.y, a.q = q2.x + q2.y;
       a.move(mx, c2);
       s2 = F2{a.s, 0.0f}, q2 = F2{a.q, 0.0f};
-      base = mx == kNegInf ? 0.0f : mx;
+      base = mx;
     };
     for (int step = 0; step < full; ++step) {
       cp_async_wait<kLpStages - 1>();
@@ -428,9 +480,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
         u[i] = *reinterpret_cast<const uint4*>(ring + ((st * kLpVecs + i) * kLpThreads + tid) * 16);
       fetch(st);
       st = st + 1 == kLpStages ? 0 : st + 1;
-      const float mx = lp_max<T>(u);
-      if (best_step < 0 || (!(mx <= a.m) && a.m == a.m))
-        raise(mx, seg.first + static_cast<int64_t>(step) * (kLpThreads * kLpVecs) + tid);
+      raise(lp_max<T>(u));
       const F2 s0 = s2, q0 = q2;
 #pragma unroll
       for (int i = 0; i < kLpVecs; ++i) add(std::false_type{}, u[i]);
@@ -455,7 +505,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
         float mx = x[0];
 #pragma unroll
         for (int j = 1; j < P; ++j) mx = max_nan(mx, x[j]);
-        if (best_step < 0 || (!(mx <= a.m) && a.m == a.m)) raise(mx, v0);
+        raise(mx);
         add(std::true_type{}, u);
       }
       fetch(st);
@@ -464,58 +514,97 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
     a.s = s2.x + s2.y, a.q = q2.x + q2.y;
 
     const LpSums w = lp_join_lanes<32>(a, c2);
+    const uint32_t order = lp_order(a.m);
     if (lane == 0) sh.warp[turn][warp] = w;
+    if (kTop) sh.order[tid] = order;
     __syncthreads();
-    LpSums all{kNegInf, 0.0f, 0.0f};  // of the CTA, in warp 0
-    int64_t t = -1;
-    float target = 0.0f;
     if (warp == 0) {
-      all = lp_join_lanes<kLpWarps>(sh.warp[turn][lane % kLpWarps], c2);
-      t = __shfl_sync(0xffffffffu, lane_t, nth);
-      target = __shfl_sync(0xffffffffu, lane_x, nth);
-      if (kCluster && lane == 0) sh.cta = all;
-    }
-    if constexpr (kTop) lp_select<T>(sh, row, p.V, seg, p.k, a.m, best_step);
-    if constexpr (kCluster) {
-      __syncwarp();
-      cluster_sync();  // every CTA's sums and keys are written
-      if (rank == 0 && tid == 0)
-        for (int i = 1; i < cluster; ++i)
-          all.join(LpSums{ld_cluster_f32(&sh.cta.m, i), ld_cluster_f32(&sh.cta.s, i), ld_cluster_f32(&sh.cta.q, i)}, c2);
-    }
-    if (rank == 0 && tid == 0) {
-      const bool empty = all.m == kNegInf;  // every logit is -inf
-      const float log_sum = empty ? 0.0f : logf(all.s);
-      const float m = empty ? 0.0f : all.m;
-      if (p.entropy != nullptr) p.entropy[r] = empty ? 0.0f : log_sum - all.q / all.s * kLn2;
-      if (p.row_max != nullptr) p.row_max[r] = all.m;
-      if (p.log_sum != nullptr) p.log_sum[r] = log_sum;
-      if (p.logprob != nullptr)
-        p.logprob[r] = t < 0 ? 0.0f
-                       : t >= p.V ? __uint_as_float(0x7FC00000u)
-                                  : (target - m) * p.inv_temperature - log_sum;
-      if (kTop) sh.row = LpSums{m, log_sum, 0.0f};
+      LpSums all = lp_join_lanes<kLpWarps>(sh.warp[turn][lane % kLpWarps], c2);
+      if constexpr (kCluster) {
+        if (lane == 0) sh.cta = all;
+        __syncwarp();
+        cluster_sync();  // every CTA's sums are written
+        if (rank == 0) {
+          all = LpSums{kNegInf, 0.0f, 0.0f};
+          if (lane < cluster)
+            all = LpSums{ld_cluster_f32(&sh.cta.m, lane), ld_cluster_f32(&sh.cta.s, lane), ld_cluster_f32(&sh.cta.q, lane)};
+          all = lp_join_lanes<32>(all, c2);
+        }
+      }
+      if (rank == 0) {
+        const int64_t t = __shfl_sync(0xffffffffu, lane_t, nth);
+        const float target = __shfl_sync(0xffffffffu, lane_x, nth);
+        const bool empty = all.m == kNegInf;  // every logit is -inf
+        const float log_sum = empty ? 0.0f : logf(all.s);
+        const float m = empty ? 0.0f : all.m;
+        if (lane == 0) {
+          if (p.entropy != nullptr) p.entropy[r] = empty ? 0.0f : log_sum - all.q / all.s * kLn2;
+          if (p.row_max != nullptr) p.row_max[r] = all.m;
+          if (p.log_sum != nullptr) p.log_sum[r] = log_sum;
+          if (p.logprob != nullptr)
+            p.logprob[r] = t < 0 ? 0.0f
+                           : t >= p.V ? __uint_as_float(0x7FC00000u)
+                                      : (target - m) * p.inv_temperature - log_sum;
+          sh.row = LpSums{m, log_sum, 0.0f};
+        }
+      }
+    } else {
+      if (kTop && warp == 1) {  // beside warp 0's joins
+        const uint32_t bound = lp_threads_bound(sh, p.k, 2);
+        if (lane == 0) sh.bound = bound, sh.listed[turn] = sh.cands[turn] = 0;
+        __syncwarp();
+      }
+      if constexpr (kCluster) cluster_sync();
     }
     if constexpr (kTop) {
-      // The keys of every CTA; rank 0 ranks them.
-      const int n = kCluster ? cluster * p.k : p.k;
-      uint64_t mine = 0;
-      if (rank == 0 && tid < n) mine = kCluster ? ld_cluster_u64(&sh.top[tid % p.k], tid / p.k) : sh.top[tid];
-      if (rank == 0) {
-        __syncthreads();  // sh.row; the list is free
-        if (kCluster && tid < n) sh.list[tid] = mine;
-        if (kCluster) __syncthreads();
-        int above = tid;
-        if (kCluster) {
-          above = 0;
-          if (mine != 0)
-            for (int i = 0; i < n; ++i) above += sh.list[i] > mine;
+      auto put = [&](int at, uint64_t key) {  // an alternative of the whole row
+        p.top_ids[r * p.k + at] = lp_key_id(key);
+        p.top_logprob[r * p.k + at] = (lp_key_value(key) - sh.row.m) * p.inv_temperature - sh.row.s;
+      };
+      auto keep = [&](int at, uint64_t key) {  // of this CTA's part
+        if constexpr (kCluster)
+          sh.top[at] = key;
+        else
+          put(at, key);
+      };
+      __syncthreads();  // sh.bound, sh.row
+      const uint32_t bound = sh.bound;
+      lp_candidates(sh, order, bound, &sh.cands[turn]);
+      __syncthreads();
+      lp_scan(sh, row, p.V, seg, sh.cands[turn], lp_least(bound), [&](float x, int64_t id) {
+        if (lp_order(x) < bound) return;
+        const int at = atomicAdd(&sh.listed[turn], 1);
+        if (at < kLpList) sh.list[at] = lp_key(x, id);  // in any order: the keys are ranked
+      });
+      __syncthreads();
+      const int n = sh.listed[turn];
+      if (n <= kLpList)
+        lp_rank_list(sh, n, p.k, tid, kLpThreads, keep);
+      else
+        lp_select_many<T>(sh, row, p.V, seg, p.k, order, turn, keep);
+      if constexpr (kCluster) {
+        __syncwarp();
+        cluster_sync();  // every CTA's keys are written
+        if (rank == 0 && warp == 0) {
+          uint64_t key[kLpMaxCluster];
+          uint32_t first[kLpMaxCluster];
+#pragma unroll
+          for (int i = 0; i < kLpMaxCluster; ++i) {
+            key[i] = i < cluster && lane < p.k ? ld_cluster_u64(&sh.top[lane], i) : 0;
+            first[i] = static_cast<uint32_t>(key[i] >> 32);
+          }
+          const uint32_t least = lp_bound(first, p.k, 8);
+          int count = 0;
+#pragma unroll
+          for (int i = 0; i < kLpMaxCluster; ++i) {
+            const bool in = first[i] >= least && key[i] != 0;
+            const uint32_t any = __ballot_sync(0xffffffffu, in);
+            if (in) sh.list[count + __popc(any & ((1u << lane) - 1u))] = key[i];
+            count += __popc(any);
+          }
+          __syncwarp();
+          lp_rank_list(sh, count, p.k, lane, 32, put);
         }
-        if (tid < n && mine != 0 && above < p.k) {
-          p.top_ids[r * p.k + above] = lp_key_id(mine);
-          p.top_logprob[r * p.k + above] = (lp_key_value(mine) - sh.row.m) * p.inv_temperature - sh.row.s;
-        }
-        if (!kCluster) __syncthreads();  // before the next row's keys
       }
     }
     if constexpr (kCluster) {
