@@ -615,6 +615,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
   cp_async_wait<0>();
 }
 
+// dx = p (A - B log p), and c g more at the target, with t = log2 p:
+// t = (x - m) c log2 e - log s log2 e.
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(TokenLogprobsBwd p) {
   constexpr int P = kLpPer<T>;
@@ -622,27 +624,39 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(TokenLog
   const int64_t v0 = (blockIdx.x % p.chunks) * (kLpThreads * kLpVecs) + threadIdx.x;
   const T* row = static_cast<const T*>(p.logits) + r * p.ld;
   T* out = static_cast<T*>(p.dlogits) + r * p.ldd;
+  uint4 u[kLpVecs];
+#pragma unroll
+  for (int i = 0; i < kLpVecs; ++i) u[i] = lp_load(row, p.V, v0 + i * kLpThreads);
   const float c = p.inv_temperature;
   const float m = p.row_max[r], log_sum = p.log_sum[r];
-  const int64_t t = p.targets != nullptr ? p.targets[r] : -1;
-  const bool empty = m == kNegInf;
-  float g = p.g_logprob != nullptr && t >= 0 ? p.g_logprob[r] : 0.0f;
-  if (t >= p.V) g = __uint_as_float(0x7FC00000u);
+  const int64_t target = p.targets != nullptr ? p.targets[r] : -1;
+  float g = p.g_logprob != nullptr && target >= 0 ? p.g_logprob[r] : 0.0f;
+  if (target >= p.V) g = __uint_as_float(0x7FC00000u);
   const float gh = p.g_entropy != nullptr ? p.g_entropy[r] : 0.0f;
-  // dx = p (A - B log p), and c g more at the target.
-  const float A = -c * (g + (p.g_entropy != nullptr ? gh * p.entropy[r] : 0.0f)), B = c * gh;
+  const F2 A = splat2(-c * (g + (p.g_entropy != nullptr ? gh * p.entropy[r] : 0.0f))), B = splat2(-c * gh * kLn2);
+  const F2 minus = splat2(-m), c2 = splat2(c * kLog2e), shift = splat2(-log_sum * kLog2e);
+  const bool empty = m == kNegInf;
 #pragma unroll
   for (int i = 0; i < kLpVecs; ++i) {
     const int64_t vec = v0 + i * kLpThreads, first = vec * P;
     if (first >= p.V) return;
     float x[P];
-    lp_values<T>(lp_load(row, p.V, vec), x);
+    lp_values<T>(u[i], x);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const float lp = max_nan((x[j] - m) * c - log_sum, -1000.0f);  // p = 0 there, and 0 log 0 = 0
-      float d = ex2(lp * kLog2e) * (A - B * lp);
-      if (first + j == t) d += c * g;
-      x[j] = empty ? 0.0f : d;
+    for (int j = 0; j < P; j += 2) {
+      F2 t = fma2(add2(F2{x[j], x[j + 1]}, minus), c2, shift);
+      t = F2{max_nan(t.x, -1000.0f), max_nan(t.y, -1000.0f)};  // p = 0 there, and 0 log 0 = 0
+      const F2 d = mul2(F2{ex2(t.x), ex2(t.y)}, fma2(B, t, A));
+      x[j] = d.x, x[j + 1] = d.y;
+    }
+    if (target >= first && target < first + P) {
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+        if (first + j == target) x[j] += c * g;
+    }
+    if (empty) {  // every logit is -inf
+#pragma unroll
+      for (int j = 0; j < P; ++j) x[j] = 0.0f;
     }
     if (first + P <= p.V) {
       if constexpr (sizeof(T) == 2)
