@@ -111,42 +111,65 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 }
 
 // ---------------------------------------------------------------------------
-// colsum: part[z][j][k] = sum_{m in split z} (hi[m][j] + lo[m][j]) X^[m][k]
+// colsum: part[z][j][k] = sum_{m in split z} V[m][j] X^[m][k], V = hi + lo + lo2
 // ---------------------------------------------------------------------------
 // m16n8k16 MMAs with D = [16 j][8 columns], the token axis as K: A = V^T from
-// the [m][64] hi / lo split by transposed 8x8 loads, B = X^ decoded in
-// registers.  A lane's B registers are pairs of tokens (2t, 2t + 1 and 2t + 8,
-// 2t + 9) of one column; which column a slot stands for is free, so lane
-// (g, t) takes kCB consecutive code bytes of each of its four token rows, at
-// byte g kCB of the warp's 8 kCB columns, and MMA i takes its i-th byte: the
-// code loads are wide and nothing is exchanged between lanes.
+// the [m][64] parts of V by transposed 8x8 loads, B = X^ decoded in registers.
+// A lane's B registers are pairs of tokens (2t, 2t + 1 and 2t + 8, 2t + 9) of
+// one column; which column a slot stands for is free, so lane (g, t) takes kCB
+// consecutive columns of each of its four token rows, at column g kCB of the
+// warp's 8 kCB, and MMA i takes its i-th: the loads are wide and nothing is
+// exchanged between lanes.  The same kernel takes plain bf16 rows (dB, from dY
+// and U), which only skip the decode.
 //
 // A CTA is 4 column groups x kWT token groups of warps; each warp runs its own
-// ring of cp.async copies (codes: read back by the thread that copied them;
-// V: by the warp), so no CTA barrier sits in the loop.  At the end the token
-// groups' sums are added in shared memory and stored as one partial.
+// ring of cp.async copies (X: read back by the thread that copied it; V: by
+// the warp), so no CTA barrier sits in the loop.  At the end the token groups'
+// sums are added in shared memory and stored as one partial.
 namespace {
 
 constexpr int kCsWC = 4;      // column groups of a CTA
-constexpr int kCsStages = 4;  // ring depth
+constexpr int kCsStages = 3;  // ring depth
+constexpr int kCsParts = 3;   // bf16 parts of V
 
-template <int kRT>
+template <int kFormat, int kRT>
 struct ColsumShape {
-  static constexpr int kCB = kRT == 1 ? 16 : 8;     // code bytes per lane and row
-  static constexpr int kWT = kRT <= 2 ? 4 : 2;      // token groups of a CTA
-  static constexpr int kCols = 8 * kCB;             // columns of a warp
+  static constexpr bool kDense = kFormat == kAct8Dense;
+  static constexpr int kCB = kRT == 1 && !kDense ? 16 : 8;    // columns per lane and row
+  static constexpr int kWT = kRT == 1 || (kRT == 2 && !kDense) ? 4 : 2;  // token groups of a CTA
+  static constexpr int kCols = 8 * kCB;                       // columns of a warp
   static constexpr int kWarps = kCsWC * kWT;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCodeBytes = 16 * kCols;     // one step: 16 tokens
-  static constexpr int kVBytes = 16 * kRT * 16 * 2;  // of one half of the split
-  static constexpr int kStageBytes = kCodeBytes + 2 * kVBytes;
+  static constexpr int kLaneBytes = kCB * (kDense ? 2 : 1);   // of one row
+  static constexpr int kXBytes = 4 * 32 * kLaneBytes;         // one step: 16 tokens
+  static constexpr int kVBytes = 16 * kRT * 16 * 2;           // of one part
+  static constexpr int kStageBytes = kXBytes + kCsParts * kVBytes;
   static constexpr int kRingBytes = kWarps * kCsStages * kStageBytes;
-  static constexpr int kRedPitch = kCols + 4;       // floats
+  static constexpr int kRedPitch = kCols + 4;                 // floats
   static constexpr int kRedBytes = kWarps * kRT * 16 * kRedPitch * 4;
   static constexpr int kSmem = kRingBytes > kRedBytes ? kRingBytes : kRedBytes;
   static constexpr int kCtaCols = kCsWC * kCols;
-  static constexpr int kCtaTokens = kWT * 16;       // tokens of a CTA per step
+  static constexpr int kCtaTokens = kWT * 16;                 // tokens of a CTA per step
+  static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
+
+  // Splits of the tokens: one wave of one CTA per SM on a 148-SM B200.
+  static int splits(int64_t M, int64_t C) {
+    const int64_t cols = (C + kCtaCols - 1) / kCtaCols, steps = (M + kCtaTokens - 1) / kCtaTokens;
+    int64_t s = 148 / cols;
+    if (s > steps) s = steps;
+    return static_cast<int>(s < 1 ? 1 : s);
+  }
 };
+
+// Place of 16-byte chunk `c` of token row `row` in a V tile of 2 kRT chunks per
+// row: permuted so that the eight rows of a transposed 8x8 load fall into
+// different banks (unpermuted, rows of 128 bytes meet in the same four, and
+// those loads bounded the kernel).  Rows of 96 bytes meet two by two as they are.
+template <int kRT>
+__device__ __forceinline__ int v_chunk(int row, int c) {
+  const int key = kRT == 4 ? row & 7 : kRT == 2 ? (row >> 1) & 3 : kRT == 1 ? (row >> 2) & 1 : 0;
+  return row * (2 * kRT) + (c ^ key);
+}
 
 template <int kBytes>
 __device__ __forceinline__ void cp_async_n(void* dst, const void* src, bool valid) {
@@ -158,46 +181,34 @@ __device__ __forceinline__ void cp_async_n(void* dst, const void* src, bool vali
                  : "memory");
 }
 
-int colsum_splits_rt(int64_t M, int64_t K, int cta_cols, int cta_tokens) {
-  const int64_t cols = (K + cta_cols - 1) / cta_cols, steps = (M + cta_tokens - 1) / cta_tokens;
-  int64_t s = 148 / cols;  // one wave of one CTA per SM
-  if (s > steps) s = steps;
-  return static_cast<int>(s < 1 ? 1 : s);
-}
-
-template <int kRT>
-int colsum_splits_of(int64_t M, int64_t K) {
-  return colsum_splits_rt(M, K, ColsumShape<kRT>::kCtaCols, ColsumShape<kRT>::kCtaTokens);
-}
-
 }  // namespace
 
 template <int kFormat, int kRT>
-__global__ void __launch_bounds__(ColsumShape<kRT>::kThreads, 1)
-    act8_colsum_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ step,
-                       const uint16_t* __restrict__ vhi, const uint16_t* __restrict__ vlo, int64_t M, int64_t K,
-                       int splits, float* __restrict__ part) {
-  using S = ColsumShape<kRT>;
+__global__ void __launch_bounds__(ColsumShape<kFormat, kRT>::kThreads, 1)
+    act8_colsum_kernel(Act8View x, const uint16_t* __restrict__ vhi, const uint16_t* __restrict__ vlo,
+                       const uint16_t* __restrict__ vlo2, int splits, float* __restrict__ part) {
+  using S = ColsumShape<kFormat, kRT>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int wc = warp % kCsWC, wt = warp / kCsWC;
+  const int64_t M = x.rows, C = x.cols;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * S::kCtaCols + wc * S::kCols;
   const int z = blockIdx.y;
   const int64_t total = (M + S::kCtaTokens - 1) / S::kCtaTokens;
   const int64_t first = total * z / splits;
   const int n = static_cast<int>(total * (z + 1) / splits - first);
   const int64_t m0 = (first * S::kWT + wt) * 16;  // the warp's first token; kCtaTokens further per step
-  const int64_t kblocks = K / kBlock;
   uint8_t* ring = smem + warp * (kCsStages * S::kStageBytes);
 
-  const int64_t col = c0 + g * S::kCB;  // this lane's columns: in or out of K as a whole (K % 64 == 0)
-  const bool col_ok = col < K;
-  // One step per lane: lane l holds that of token l / 2 of the step and of
-  // the warp's block l % 2 (kCols = 128: two blocks; 64: one).
-  constexpr int kBlocksPerWarp = S::kCols / kBlock;
-  const int64_t blk = c0 / kBlock + (lane & (kBlocksPerWarp - 1));
-  const int step_token = lane / kBlocksPerWarp;
+  const int64_t col = c0 + g * S::kCB;  // this lane's columns: in or out of C as a whole
+  const bool col_ok = col < C;
+  const int64_t row_bytes = C * (S::kDense ? 2 : 1), col_bytes = col * (S::kDense ? 2 : 1);
+  // One step per lane: lane l holds that of token l / blocks of the step and
+  // of the warp's block l % blocks (kCols = 128: two blocks; 64: one).
+  constexpr int kBlocks = S::kCols / kBlock;
+  const int64_t kblocks = C / kBlock, blk = c0 / kBlock + (lane & (kBlocks - 1));
+  const int step_token = lane / kBlocks;
 
   auto issue = [&](int i) {
     if (i < n) {
@@ -207,24 +218,27 @@ __global__ void __launch_bounds__(ColsumShape<kRT>::kThreads, 1)
       for (int q = 0; q < 4; ++q) {
         const int64_t row = m + 2 * t + (q & 1) + (q >> 1) * 8;
         const bool ok = col_ok && row < M;
-        cp_async_n<S::kCB>(st + (q * 32 + lane) * S::kCB, codes + (ok ? row * K + col : 0), ok);
+        cp_async_n<S::kLaneBytes>(st + (q * 32 + lane) * S::kLaneBytes, x.codes + (ok ? row * row_bytes + col_bytes : 0),
+                                  ok);
       }
 #pragma unroll
-      for (int q = 0; q < 2 * kRT; ++q) {
-        const int chunk = q * 32 + lane;            // of 64 kRT: hi, then lo; 2 kRT chunks per token
-        const int half = chunk / (32 * kRT), rest = chunk % (32 * kRT);
-        const int64_t row = m + rest / (2 * kRT);
-        const uint16_t* src = half ? vlo : vhi;
-        cp_async_n<16>(st + S::kCodeBytes + chunk * 16, src + (row < M ? row * kRankPad + (rest % (2 * kRT)) * 8 : 0),
-                       row < M);
+      for (int q = 0; q < kCsParts * kRT; ++q) {
+        const int chunk = q * 32 + lane;  // of 32 kRT for each part: 2 kRT chunks of 8 j per token
+        const int which = chunk / (32 * kRT), rest = chunk % (32 * kRT);
+        const int tok = rest / (2 * kRT), c = rest % (2 * kRT);
+        const int64_t row = m + tok;
+        const uint16_t* src = which == 0 ? vhi : which == 1 ? vlo : vlo2;
+        cp_async_n<16>(st + S::kXBytes + which * S::kVBytes + v_chunk<kRT>(tok, c) * 16,
+                       src + (row < M ? row * kRankPad + c * 8 : 0), row < M);
       }
     }
     cp_async_commit();
   };
   auto load_step = [&](int i) -> uint32_t {
+    if constexpr (S::kDense) return 0u;
     const int64_t row = m0 + static_cast<int64_t>(i) * S::kCtaTokens + step_token;
     const bool ok = i < n && step_token < 16 && row < M && blk < kblocks;
-    return ok ? step[row * kblocks + blk] : 0u;
+    return ok ? x.step[row * kblocks + blk] : 0u;
   };
 
   float acc[kRT][S::kCB][4];
@@ -248,44 +262,64 @@ __global__ void __launch_bounds__(ColsumShape<kRT>::kThreads, 1)
     issue(i + kCsStages - 1);  // into the stage read in the previous iteration
     const uint8_t* st = ring + (i % kCsStages) * S::kStageBytes;
     // Packed steps of the token pairs (2t, 2t + 1) and (2t + 8, 2t + 9), block of column g kCB.
-    const int b = g * S::kCB / kBlock;
-    uint32_t s2[2];
+    uint32_t s2[2] = {0u, 0u};
+    if constexpr (!S::kDense) {
+      const int b = g * S::kCB / kBlock;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = 2 * t + 8 * h;
-      const uint32_t lo = __shfl_sync(0xffffffffu, my_step, tok * kBlocksPerWarp + b);
-      const uint32_t hi = __shfl_sync(0xffffffffu, my_step, (tok + 1) * kBlocksPerWarp + b);
-      s2[h] = lo | (hi << 16);
+      for (int h = 0; h < 2; ++h) {
+        const int tok = 2 * t + 8 * h;
+        const uint32_t lo = __shfl_sync(0xffffffffu, my_step, tok * kBlocks + b);
+        const uint32_t hi = __shfl_sync(0xffffffffu, my_step, (tok + 1) * kBlocks + b);
+        s2[h] = lo | (hi << 16);
+      }
     }
-    uint32_t ah[kRT][4], al[kRT][4];
+    // The lane's columns of its four rows (wide reads: by words they would conflict).
+    uint32_t xr[4][S::kLaneBytes / 4];
 #pragma unroll
-    for (int a = 0; a < kRT; ++a) {
-      // Stored rows are tokens (2 kRT chunks of 8 j each): matrices (tokens 0-7, j lo), (0-7, hi), (8-15, lo), (8-15, hi).
-      const uint32_t addr = smem_u32(st + S::kCodeBytes) + (((mat >> 1) * 8 + rr) * (2 * kRT) + a * 2 + (mat & 1)) * 16;
-      ldmatrix_x4_trans(ah[a], addr);
-      ldmatrix_x4_trans(al[a], addr + S::kVBytes);
+    for (int q = 0; q < 4; ++q) {
+      const uint8_t* src = st + (q * 32 + lane) * S::kLaneBytes;
+      if constexpr (S::kLaneBytes == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src);
+        xr[q][0] = v.x, xr[q][1] = v.y, xr[q][2] = v.z, xr[q][3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        xr[q][0] = v.x, xr[q][1] = v.y;
+      }
     }
+    // Four columns at a time: their B registers, then the parts of V one after
+    // the other, so that an accumulator is used again 4 kRT MMAs later.
 #pragma unroll
     for (int w = 0; w < S::kCB / 4; ++w) {
-      uint32_t c[4];
+      uint32_t bf[4][2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        c[q] = *reinterpret_cast<const uint32_t*>(st + (q * 32 + lane) * S::kCB + 4 * w);
-      // Byte pairs (row 2t, row 2t + 1) of the word's four columns.
-      const uint32_t p[2][2] = {{__byte_perm(c[0], c[1], 0x5140), __byte_perm(c[0], c[1], 0x7362)},
-                                {__byte_perm(c[2], c[3], 0x5140), __byte_perm(c[2], c[3], 0x7362)}};
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (S::kDense) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t bf[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          bf[h] = e % 2 == 0 ? act8_decode2<kFormat, 0>(p[h][e / 2], s2[h]) : act8_decode2<kFormat, 2>(p[h][e / 2], s2[h]);
-#pragma unroll
-        for (int a = 0; a < kRT; ++a) {
-          mma_16816(acc[a][4 * w + e], ah[a], bf);
-          mma_16816(acc[a][4 * w + e], al[a], bf);
+          for (int e = 0; e < 2; ++e) {
+            bf[2 * e][h] = __byte_perm(xr[2 * h][2 * w + e], xr[2 * h + 1][2 * w + e], 0x5410);
+            bf[2 * e + 1][h] = __byte_perm(xr[2 * h][2 * w + e], xr[2 * h + 1][2 * w + e], 0x7632);
+          }
+        } else {
+          // Byte pairs (row 2t, row 2t + 1) of the word's four columns.
+          const uint32_t p0 = __byte_perm(xr[2 * h][w], xr[2 * h + 1][w], 0x5140);
+          const uint32_t p1 = __byte_perm(xr[2 * h][w], xr[2 * h + 1][w], 0x7362);
+          bf[0][h] = act8_decode2<kFormat, 0>(p0, s2[h]);
+          bf[1][h] = act8_decode2<kFormat, 2>(p0, s2[h]);
+          bf[2][h] = act8_decode2<kFormat, 0>(p1, s2[h]);
+          bf[3][h] = act8_decode2<kFormat, 2>(p1, s2[h]);
         }
       }
+#pragma unroll
+      for (int v = 0; v < kCsParts; ++v)
+#pragma unroll
+        for (int a = 0; a < kRT; ++a) {
+          // Stored rows are tokens: matrices (tokens 0-7, j lo), (0-7, j hi), (8-15, j lo), (8-15, j hi).
+          uint32_t af[4];
+          ldmatrix_x4_trans(af, smem_u32(st + S::kXBytes + v * S::kVBytes) +
+                                    v_chunk<kRT>((mat >> 1) * 8 + rr, a * 2 + (mat & 1)) * 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma_16816(acc[a][4 * w + e], af, bf[e]);
+        }
     }
   }
   cp_async_wait<0>();
@@ -296,57 +330,84 @@ __global__ void __launch_bounds__(ColsumShape<kRT>::kThreads, 1)
 #pragma unroll
   for (int a = 0; a < kRT; ++a)
 #pragma unroll
-    for (int b = 0; b < S::kCB; ++b)
+    for (int c = 0; c < 4; ++c) {
+      float* dst = mine + (a * 16 + g + (c >> 1) * 8) * S::kRedPitch + (2 * t + (c & 1)) * S::kCB;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        mine[(a * 16 + g + (c >> 1) * 8) * S::kRedPitch + (2 * t + (c & 1)) * S::kCB + b] = acc[a][b][c];
+      for (int b = 0; b < S::kCB; b += 4)
+        *reinterpret_cast<float4*>(dst + b) =
+            make_float4(acc[a][b][c], acc[a][b + 1][c], acc[a][b + 2][c], acc[a][b + 3][c]);
+    }
   __syncthreads();
-  constexpr int kOut = kRT * 16 * S::kCtaCols;
+  constexpr int kOut = kRT * 16 * S::kCtaCols / 4;  // in fours
   for (int o = threadIdx.x; o < kOut; o += S::kThreads) {
-    const int j = o / S::kCtaCols, c = o % S::kCtaCols;
+    const int j = o / (S::kCtaCols / 4), c = o % (S::kCtaCols / 4) * 4;
     const float* src = red + (c / S::kCols) * (kRT * 16 * S::kRedPitch) + j * S::kRedPitch + c % S::kCols;
-    float s = 0.0f;
+    float4 s = *reinterpret_cast<const float4*>(src);
 #pragma unroll
-    for (int q = 0; q < S::kWT; ++q) s += src[q * (kCsWC * kRT * 16 * S::kRedPitch)];
+    for (int q = 1; q < S::kWT; ++q) {
+      const float4 o4 = *reinterpret_cast<const float4*>(src + q * (kCsWC * kRT * 16 * S::kRedPitch));
+      s.x += o4.x, s.y += o4.y, s.z += o4.z, s.w += o4.w;
+    }
     const int64_t k = static_cast<int64_t>(blockIdx.x) * S::kCtaCols + c;
-    if (k < K) part[(static_cast<int64_t>(z) * (kRT * 16) + j) * K + k] = s;
+    if (k < C) *reinterpret_cast<float4*>(part + (static_cast<int64_t>(z) * (kRT * 16) + j) * C + k) = s;
   }
 }
 
-// dst[j][k] = scale sum_z part[z][j][k]; part rows are r16 = 16 ceil(r / 16) per split.
-__global__ void act8_colsum_reduce_kernel(const float4* __restrict__ part, int64_t k4, int r, int r16, int splits,
-                                          float scale, float* __restrict__ dst) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;  // over r * K / 4
-  if (i >= k4 * r) return;
-  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int z = 0; z < splits; ++z) {
-    const float4 p = part[static_cast<int64_t>(z) * r16 * k4 + i];
-    s.x += p.x;
-    s.y += p.y;
-    s.z += p.z;
-    s.w += p.w;
-  }
-  float* o = dst + 4 * i;  // dst is only 4-byte aligned
-  o[0] = scale * s.x;
-  o[1] = scale * s.y;
-  o[2] = scale * s.z;
-  o[3] = scale * s.w;
-}
+// dst(j, k) = scale sum_z part[z][j][k]; part has r16 = 16 ceil(r / 16) rows
+// per split.  A CTA takes 32 columns of 16 j: four columns of one j per
+// thread.  [cols][r] outputs leave through shared memory, 16 j side by side.
+constexpr int kCrCols = 32;
 
-size_t act8_colsum_partial_bytes(int64_t M, int64_t K) {
-  const int64_t rows[4] = {16 * int64_t{colsum_splits_of<1>(M, K)}, 32 * int64_t{colsum_splits_of<2>(M, K)},
-                           48 * int64_t{colsum_splits_of<3>(M, K)}, 64 * int64_t{colsum_splits_of<4>(M, K)}};
-  int64_t most = 0;
-  for (const int64_t v : rows) most = v > most ? v : most;
-  return static_cast<size_t>(most) * static_cast<size_t>(K) * sizeof(float);
+__global__ void __launch_bounds__(128) act8_colsum_reduce_kernel(const float* __restrict__ part, int64_t C, int r,
+                                                                 int splits, float scale, float* __restrict__ dst,
+                                                                 int dst_rc) {
+  __shared__ float tile[kCrCols][17];
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kCrCols;
+  const int jj = threadIdx.x / (kCrCols / 4), cc = threadIdx.x % (kCrCols / 4) * 4, j = blockIdx.y * 16 + jj;
+  const int64_t slice = static_cast<int64_t>(gridDim.y) * 16 * C;
+  if (j < r && c0 + cc < C) {
+    const float* src = part + j * C + c0 + cc;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int z = 0; z < splits; ++z) {
+      const float4 p = *reinterpret_cast<const float4*>(src + z * slice);
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    const float v[4] = {scale * s.x, scale * s.y, scale * s.z, scale * s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (dst_rc)
+        dst[j * C + c0 + cc + e] = v[e];
+      else
+        tile[cc + e][jj] = v[e];
+    }
+  }
+  if (dst_rc) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = threadIdx.x; i < kCrCols * 16; i += 128) {
+    const int c = i / 16, q = i % 16;
+    if (c0 + c < C && blockIdx.y * 16 + q < r) dst[(c0 + c) * r + blockIdx.y * 16 + q] = tile[c][q];
+  }
 }
 
 namespace {
 
+template <int kFormat>
+int64_t colsum_partial_rows(int64_t M, int64_t C) {
+  const int64_t rows[4] = {16 * int64_t{ColsumShape<kFormat, 1>::splits(M, C)},
+                           32 * int64_t{ColsumShape<kFormat, 2>::splits(M, C)},
+                           48 * int64_t{ColsumShape<kFormat, 3>::splits(M, C)},
+                           64 * int64_t{ColsumShape<kFormat, 4>::splits(M, C)}};
+  int64_t most = 0;
+  for (const int64_t v : rows) most = v > most ? v : most;
+  return most;
+}
+
 template <int kFormat, int kRT>
-cudaError_t launch_colsum_rt(const Act8View& x, const uint16_t* hi, const uint16_t* lo, float* part, int* splits,
-                             cudaStream_t stream) {
-  using S = ColsumShape<kRT>;
+cudaError_t launch_colsum_rt(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2,
+                             float* part, int* splits, cudaStream_t stream) {
+  using S = ColsumShape<kFormat, kRT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -356,36 +417,41 @@ cudaError_t launch_colsum_rt(const Act8View& x, const uint16_t* hi, const uint16
                                 S::kSmem);
   });
   if (e != cudaSuccess) return e;
-  *splits = colsum_splits_of<kRT>(x.rows, x.cols);
+  *splits = S::splits(x.rows, x.cols);
   const dim3 grid(static_cast<unsigned>((x.cols + S::kCtaCols - 1) / S::kCtaCols), static_cast<unsigned>(*splits));
-  act8_colsum_kernel<kFormat, kRT><<<grid, S::kThreads, S::kSmem, stream>>>(x.codes, x.step, hi, lo, x.rows, x.cols,
-                                                                           *splits, part);
+  act8_colsum_kernel<kFormat, kRT><<<grid, S::kThreads, S::kSmem, stream>>>(x, hi, lo, lo2, *splits, part);
   return cudaGetLastError();
 }
 
 template <int kFormat>
-cudaError_t launch_colsum_format(const Act8View& x, const uint16_t* hi, const uint16_t* lo, int rt, float* part,
-                                 int* splits, cudaStream_t stream) {
+cudaError_t launch_colsum_format(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2,
+                                 int rt, float* part, int* splits, cudaStream_t stream) {
   switch (rt) {
-    case 1: return launch_colsum_rt<kFormat, 1>(x, hi, lo, part, splits, stream);
-    case 2: return launch_colsum_rt<kFormat, 2>(x, hi, lo, part, splits, stream);
-    case 3: return launch_colsum_rt<kFormat, 3>(x, hi, lo, part, splits, stream);
-    default: return launch_colsum_rt<kFormat, 4>(x, hi, lo, part, splits, stream);
+    case 1: return launch_colsum_rt<kFormat, 1>(x, hi, lo, lo2, part, splits, stream);
+    case 2: return launch_colsum_rt<kFormat, 2>(x, hi, lo, lo2, part, splits, stream);
+    case 3: return launch_colsum_rt<kFormat, 3>(x, hi, lo, lo2, part, splits, stream);
+    default: return launch_colsum_rt<kFormat, 4>(x, hi, lo, lo2, part, splits, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, int r, float scale,
-                               float* part, float* dst, cudaStream_t stream) {
+size_t act8_colsum_partial_bytes(int64_t M, int64_t C) {
+  const int64_t codes = colsum_partial_rows<kAct8Int8>(M, C), dense = colsum_partial_rows<kAct8Dense>(M, C);
+  return static_cast<size_t>(codes > dense ? codes : dense) * static_cast<size_t>(C) * sizeof(float);
+}
+
+cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2, int r,
+                               float scale, float* part, float* dst, bool dst_rc, cudaStream_t stream) {
   const int rt = (r + 15) / 16;
   int splits = 0;
-  const cudaError_t e = x.format == kAct8Int8 ? launch_colsum_format<kAct8Int8>(x, hi, lo, rt, part, &splits, stream)
-                                              : launch_colsum_format<kAct8E4m3>(x, hi, lo, rt, part, &splits, stream);
+  const cudaError_t e =
+      x.format == kAct8Dense  ? launch_colsum_format<kAct8Dense>(x, hi, lo, lo2, rt, part, &splits, stream)
+      : x.format == kAct8Int8 ? launch_colsum_format<kAct8Int8>(x, hi, lo, lo2, rt, part, &splits, stream)
+                              : launch_colsum_format<kAct8E4m3>(x, hi, lo, lo2, rt, part, &splits, stream);
   if (e != cudaSuccess) return e;
-  const int64_t k4 = x.cols / 4, items = k4 * r;
-  act8_colsum_reduce_kernel<<<static_cast<unsigned>((items + 127) / 128), 128, 0, stream>>>(
-      reinterpret_cast<const float4*>(part), k4, r, 16 * rt, splits, scale, dst);
+  const dim3 grid(static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols), static_cast<unsigned>(rt));
+  act8_colsum_reduce_kernel<<<grid, 128, 0, stream>>>(part, x.cols, r, splits, scale, dst, dst_rc ? 1 : 0);
   return cudaGetLastError();
 }
 

@@ -345,7 +345,7 @@ int64_t max_group_chunks(const qlora_nf4_weight* outs, int32_t count) {
 
 // Linear workspace layout.
 struct LinearWs {
-  size_t wbf, scales, us, uhi, ulo, vs, vhi, vlo, bpad, part, skpart, vdbpart, bt, uht, ult, gu, gy, total;
+  size_t wbf, scales, us, uhi, ulo, ulo2, vs, vhi, vlo, vlo2, bpad, part, skpart, vdbpart, bt, uht, ult, ult2, gu, gy, total;
 };
 
 LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
@@ -365,12 +365,14 @@ LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
   l.us = take(mr * 2);
   l.uhi = take(mr * 2);
   l.ulo = take(mr * 2);
+  l.ulo2 = take(mr * 2);  // third parts: the backward from a checkpoint
   l.vs = take(mr * 2);
   l.vhi = take(mr * 2);
   l.vlo = take(mr * 2);
+  l.vlo2 = take(mr * 2);
   l.bpad = take(static_cast<size_t>(N) * kRankPad * 2);
   const size_t p1 = colsum_partial_bytes(M, N), p2 = colsum_partial_bytes(M, K);
-  l.part = take(std::max({p1, p2, act8_colsum_partial_bytes(M, K)}));
+  l.part = take(std::max({p1, p2, act8_colsum_partial_bytes(M, K), act8_colsum_partial_bytes(M, N)}));
   const size_t s1 = skinny_partial_bytes(M, N), s2 = skinny_partial_bytes(M, K);
   l.skpart = take(s1 > s2 ? s1 : s2);
   // The tensor-core V / dB pass: its partials and the transposed B and U split.
@@ -379,6 +381,7 @@ LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
   l.bt = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(N) * 2 : 0);
   l.uht = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
   l.ult = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
+  l.ult2 = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
   // Decode path (M <= 16): U partials and, for K > 4096, per-chunk fp32 outputs.
   const bool decode = M <= kGemvMaxM;
   l.gu = take(decode ? static_cast<size_t>(gemv_upart_count(K)) * kGemvMaxM * kRankPad * 4 : 0);
@@ -436,6 +439,11 @@ qlora_status check_act8(const qlora_act8* a) {
   if (a->format != QLORA_ACT8_INT8 && a->format != QLORA_ACT8_E4M3) return QLORA_ERR_INVALID_ARG;
   if (!a->codes || !a->step) return QLORA_ERR_INVALID_ARG;
   return aligned(a->codes, 16) && aligned(a->step, 2) ? QLORA_OK : QLORA_ERR_ALIGNMENT;
+}
+
+// A bf16 matrix as a column-sum input (launch_act8_colsum).
+Act8View dense_view(const uint16_t* X, int64_t rows, int64_t cols) {
+  return Act8View{reinterpret_cast<const uint8_t*>(X), nullptr, rows, cols, kAct8Dense};
 }
 
 Act8View view_of(const qlora_act8* a) { return Act8View{a->codes, a->step, a->rows, a->cols, a->format}; }
@@ -902,15 +910,21 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   }
   const uint16_t* Bk = b_direct ? B : at<uint16_t>(ws, lay.bpad);
   const int64_t ldbk = b_direct ? r : kRankPad;
-  // U = X A^T as a bf16 hi/lo pair (from the saved fp32 U, or recomputed).
+  // From a checkpoint U and V are split into three bf16 parts, which hold all
+  // of their fp32 values: dA and dB then keep fp32 accuracy (2 10^-6 with two
+  // parts, against the 10^-3 that the checkpoint itself costs at most).
+  uint16_t* const ulo2 = x8 != nullptr ? at<uint16_t>(ws, lay.ulo2) : nullptr;
+  uint16_t* const vlo2 = x8 != nullptr ? at<uint16_t>(ws, lay.vlo2) : nullptr;
+  // U = X A^T in its bf16 parts (from the saved fp32 U, or recomputed).
   auto u_hilo = [&]() -> cudaError_t {
     if (U != nullptr) {
       Timed tm(kFamSide, s);
-      return launch_split_hilo(U, M, r, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), s);
+      return launch_split_hilo(U, M, r, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, s);
     }
     SkinnyOut uo{};
     uo.ohi = at<uint16_t>(ws, lay.uhi);
     uo.olo = at<uint16_t>(ws, lay.ulo);
+    uo.olo2 = ulo2;
     uo.scale = 1.0f;
     Timed tm(kFamSide, s, 2);
     if (x8 != nullptr) return launch_act8_skinny(view_of(x8), A, r, at<float>(ws, lay.skpart), uo, s);
@@ -928,10 +942,11 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     // The dX GEMM's block scales ride in the pass's reduction launch.
     if (dX != nullptr && !dense) bs = block_scales_job(view_of(w), at<float>(ws, lay.scales));
     Timed tm(kFamSide, s, 3);  // the rank transposes, the pass, the reduction
-    e = launch_vdb_tc(dY, M, N, Bk, ldbk, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), U, r, scale,
+    e = launch_vdb_tc(dY, M, N, Bk, ldbk, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, U, r, scale,
                       at<float>(ws, lay.vdbpart), at<uint16_t>(ws, lay.bt), at<uint16_t>(ws, lay.uht),
-                      at<uint16_t>(ws, lay.ult), at<uint16_t>(ws, lay.vs), at<uint16_t>(ws, lay.vhi),
-                      at<uint16_t>(ws, lay.vlo), dB, bs, status, s);
+                      at<uint16_t>(ws, lay.ult), x8 != nullptr ? at<uint16_t>(ws, lay.ult2) : nullptr,
+                      at<uint16_t>(ws, lay.vs), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, dB, bs,
+                      status, s);
     if (e != cudaSuccess) return from_cuda(e);
   } else {
     // V = dY B (bf16 s*V for the dX rank step; hi/lo split for dA).
@@ -939,6 +954,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     vo.os = at<uint16_t>(ws, lay.vs);
     vo.ohi = at<uint16_t>(ws, lay.vhi);
     vo.olo = at<uint16_t>(ws, lay.vlo);
+    vo.olo2 = vlo2;
     vo.scale = scale;
     {
       Timed tm(kFamSide, s, 2);
@@ -949,8 +965,12 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
       e = u_hilo();
       if (e != cudaSuccess) return from_cuda(e);
       Timed tm(kFamSide, s, 2);
-      e = launch_colsum(dY, M, N, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), r, scale,
-                        at<float>(ws, lay.part), dB, false, status, s);
+      if (x8 != nullptr)
+        e = launch_act8_colsum(dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, r,
+                               scale, at<float>(ws, lay.part), dB, false, s);
+      else
+        e = launch_colsum(dY, M, N, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), r, scale,
+                          at<float>(ws, lay.part), dB, false, status, s);
       if (e != cudaSuccess) return from_cuda(e);
     }
   }
@@ -992,8 +1012,8 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     {
       Timed tm(kFamSide, s, 2);
       if (x8 != nullptr)
-        e = launch_act8_colsum(view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
-                               at<float>(ws, lay.part), dA, s);
+        e = launch_act8_colsum(view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, r, scale,
+                               at<float>(ws, lay.part), dA, true, s);
       else
         e = launch_colsum(X, M, K, at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
                           at<float>(ws, lay.part), dA, true, status, s);

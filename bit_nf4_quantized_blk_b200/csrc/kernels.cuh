@@ -173,12 +173,14 @@ cudaError_t launch_gemv(const GemvParams& p, cudaStream_t stream);
 //   o32   fp32 [M][o32_ld] (j < r)                   (may be null)
 //   os    [M][64] bf16 of scale * out, zero padded   (may be null)
 //   ohi / olo [M][64] bf16 split of out (hi + lo ~ fp32) (may be null)
+//   olo2  [M][64] what hi + lo leave of out (hi + lo + lo2 = out) (may be null)
 struct SkinnyOut {
   float* o32;
   int64_t o32_ld;
   uint16_t* os;
   uint16_t* ohi;
   uint16_t* olo;
+  uint16_t* olo2;
   float scale;
   BlockScalesJob bs;  // run on further threads of the reduction's launch (out null: none)
 };
@@ -189,8 +191,9 @@ cudaError_t launch_skinny(const uint16_t* In, int64_t M, int64_t C, const uint16
 // The reduction of launch_skinny's split partials alone ([splits][M][64] in `part`).
 cudaError_t launch_skinny_finalize(const float* part, int64_t M, int r, int splits, const SkinnyOut& out,
                                    cudaStream_t stream);
-// hi/lo bf16 split of a compact fp32 [M][r] matrix into [M][64] buffers.
-cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, cudaStream_t stream);
+// hi/lo (and, unless null, lo2) bf16 split of a compact fp32 [M][r] matrix into [M][64] buffers.
+cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, uint16_t* lo2,
+                              cudaStream_t stream);
 
 // Column sums over tokens: out(c, j) = scale * sum_m In[m][c] * (hi[m][j] + lo[m][j]).
 // part: [ms][C][64] fp32 partials; then written to dst as [C][r] (dst_rc = false)
@@ -211,7 +214,9 @@ constexpr int kVdbMaxRank = 16;
 // B^T and the transposed U split.  U comes either as the hi / lo split
 // (uhi / ulo [M][64], as launch_skinny writes it; u32 null) or as the saved
 // fp32 U [M][r] (u32; uhi / ulo unused), which the transposes split
-// themselves.
+// themselves.  With ult2 (scratch like ult) and vlo2, U and V are split into
+// three bf16 parts, which lose nothing of the fp32 values; ulo2 is U's third
+// part as launch_skinny writes it.
 struct VdbTcGrid {
   int ct, tt, ncb, ntb;  // column / token tiles per CTA; column / token blocks
 };
@@ -220,14 +225,15 @@ size_t vdb_tc_partial_bytes(int64_t M, int64_t N);
 inline int64_t vdb_tc_ldm(int64_t M) { return (M + 7) / 8 * 8; }  // 16-byte rows for TMA
 // `bs`: a block-scales job run in the reduction's launch (out null: none).
 cudaError_t launch_vdb_tc(const uint16_t* G, int64_t M, int64_t N, const uint16_t* B, int64_t ldb,
-                          const uint16_t* uhi, const uint16_t* ulo, const float* u32, int r, float scale, float* part,
-                          uint16_t* bt, uint16_t* uht, uint16_t* ult, uint16_t* vs, uint16_t* vhi, uint16_t* vlo,
-                          float* dB, const BlockScalesJob& bs, int* status, cudaStream_t stream);
+                          const uint16_t* uhi, const uint16_t* ulo, const uint16_t* ulo2, const float* u32, int r,
+                          float scale, float* part, uint16_t* bt, uint16_t* uht, uint16_t* ult, uint16_t* ult2,
+                          uint16_t* vs, uint16_t* vhi, uint16_t* vlo, uint16_t* vlo2, float* dB,
+                          const BlockScalesJob& bs, int* status, cudaStream_t stream);
 // The fixed-order reduction of vdb partials [ncb][M][16] and [ntb][N][16],
 // plus the block-scales job `bs` on further threads.
 cudaError_t launch_vdb_finalize(const float* vpart, int ncb, const float* dbpart, int ntb, int64_t M, int64_t N,
-                                int r, float scale, uint16_t* vs, uint16_t* vhi, uint16_t* vlo, float* dB,
-                                const BlockScalesJob& bs, cudaStream_t stream);
+                                int r, float scale, uint16_t* vs, uint16_t* vhi, uint16_t* vlo, uint16_t* vlo2,
+                                float* dB, const BlockScalesJob& bs, cudaStream_t stream);
 
 // Copy a bf16 [rows][r] matrix into [rows][64] zero padded, optionally from
 // the transposed source [r][rows].
@@ -238,21 +244,25 @@ cudaError_t launch_pad_rank(const uint16_t* src, bool src_transposed, int64_t ro
 // 8-bit activation checkpoints (act8.cu; the rounding rules in act8.cuh)
 // ---------------------------------------------------------------------------
 
+constexpr int kAct8Dense = -1;  // an Act8View of plain bf16 values (codes: the values, no steps)
+
 struct Act8View {
   const uint8_t* codes;  // [rows][cols]
   const uint16_t* step;  // [rows][cols / 64] bf16
   int64_t rows, cols;
-  int format;            // QLORA_ACT8_*
+  int format;            // QLORA_ACT8_* or kAct8Dense
 };
 
 cudaError_t launch_act8_quantize(const uint16_t* X, int64_t n, int format, uint8_t* codes, uint16_t* step,
                                  cudaStream_t stream);
 cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t stream);
-// dst [r][K] = scale sum_m (hi[m][j] + lo[m][j]) X^[m][k]; `part` is scratch of
-// act8_colsum_partial_bytes(M, K) (enough for every rank).
-size_t act8_colsum_partial_bytes(int64_t M, int64_t K);
-cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, int r, float scale,
-                               float* part, float* dst, cudaStream_t stream);
+// out(j, k) = scale sum_m (hi + lo + lo2)[m][j] X^[m][k] over the rows m of x
+// (a checkpoint, or bf16 values with 16-byte aligned rows), written to dst as
+// [r][cols] (dst_rc) or [cols][r].  `part` is scratch of
+// act8_colsum_partial_bytes(rows, cols), enough for every rank and format.
+size_t act8_colsum_partial_bytes(int64_t M, int64_t C);
+cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2, int r,
+                               float scale, float* part, float* dst, bool dst_rc, cudaStream_t stream);
 // launch_skinny's product X^ A^T from a checkpoint (A [r][K] bf16, 8-byte
 // aligned rows); `part` as for launch_skinny.
 cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, const SkinnyOut& out,

@@ -211,13 +211,17 @@ __global__ void skinny_finalize_kernel(const float* __restrict__ part, int64_t M
     const float r0 = v0 - bf16_bits_to_float(hi & 0xFFFF);
     const float r1 = v1 - bf16_bits_to_float(hi >> 16);
     *reinterpret_cast<uint32_t*>(out.ohi + m * kRankPad + j) = hi;
-    *reinterpret_cast<uint32_t*>(out.olo + m * kRankPad + j) = pack_bf16x2(r0, r1);
+    const uint32_t lo = pack_bf16x2(r0, r1);
+    *reinterpret_cast<uint32_t*>(out.olo + m * kRankPad + j) = lo;
+    if (out.olo2)
+      *reinterpret_cast<uint32_t*>(out.olo2 + m * kRankPad + j) =
+          pack_bf16x2(r0 - bf16_bits_to_float(lo & 0xFFFF), r1 - bf16_bits_to_float(lo >> 16));
   }
 }
 
-// hi/lo bf16 split of a compact fp32 [M][r] matrix into [M][64] (zero padded).
+// hi/lo (lo2) bf16 split of a compact fp32 [M][r] matrix into [M][64] (zero padded).
 __global__ void split_hilo_kernel(const float* __restrict__ src, int64_t M, int r, uint16_t* __restrict__ hi,
-                                  uint16_t* __restrict__ lo) {
+                                  uint16_t* __restrict__ lo, uint16_t* __restrict__ lo2) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= M * (kRankPad / 2)) return;
   const int64_t m = i / (kRankPad / 2);
@@ -226,8 +230,12 @@ __global__ void split_hilo_kernel(const float* __restrict__ src, int64_t M, int 
   const float v1 = j + 1 < r ? src[m * r + j + 1] : 0.0f;
   const uint32_t h = pack_bf16x2(v0, v1);
   *reinterpret_cast<uint32_t*>(hi + m * kRankPad + j) = h;
-  *reinterpret_cast<uint32_t*>(lo + m * kRankPad + j) =
-      pack_bf16x2(v0 - bf16_bits_to_float(h & 0xFFFF), v1 - bf16_bits_to_float(h >> 16));
+  const float r0 = v0 - bf16_bits_to_float(h & 0xFFFF), r1 = v1 - bf16_bits_to_float(h >> 16);
+  const uint32_t l = pack_bf16x2(r0, r1);
+  *reinterpret_cast<uint32_t*>(lo + m * kRankPad + j) = l;
+  if (lo2 != nullptr)
+    *reinterpret_cast<uint32_t*>(lo2 + m * kRankPad + j) =
+        pack_bf16x2(r0 - bf16_bits_to_float(l & 0xFFFF), r1 - bf16_bits_to_float(l >> 16));
 }
 
 int skinny_splits(int64_t M, int64_t C) {
@@ -296,9 +304,10 @@ cudaError_t launch_skinny_finalize(const float* part, int64_t M, int r, int spli
   return cudaGetLastError();
 }
 
-cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, cudaStream_t stream) {
+cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, uint16_t* lo2,
+                              cudaStream_t stream) {
   const int64_t total = M * (kRankPad / 2);
-  split_hilo_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(src, M, r, hi, lo);
+  split_hilo_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(src, M, r, hi, lo, lo2);
   return cudaGetLastError();
 }
 
@@ -486,7 +495,7 @@ cudaError_t launch_colsum(const uint16_t* In, int64_t M, int64_t C, const uint16
 __global__ void vdb_finalize_kernel(const float* __restrict__ vpart, int ncb, const float* __restrict__ dbpart,
                                     int ntb, int64_t M, int64_t N, int r, int r16, float scale,
                                     uint16_t* __restrict__ vs, uint16_t* __restrict__ vhi, uint16_t* __restrict__ vlo,
-                                    float* __restrict__ dB, BlockScalesJob bs) {
+                                    uint16_t* __restrict__ vlo2, float* __restrict__ dB, BlockScalesJob bs) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t nv = M * (kRankPad / 2);
   if (i < nv) {
@@ -504,8 +513,12 @@ __global__ void vdb_finalize_kernel(const float* __restrict__ vpart, int ncb, co
     *reinterpret_cast<uint32_t*>(vs + m * kRankPad + j) = pack_bf16x2(scale * v0, scale * v1);
     const uint32_t hi = pack_bf16x2(v0, v1);
     *reinterpret_cast<uint32_t*>(vhi + m * kRankPad + j) = hi;
-    *reinterpret_cast<uint32_t*>(vlo + m * kRankPad + j) =
-        pack_bf16x2(v0 - bf16_bits_to_float(hi & 0xFFFF), v1 - bf16_bits_to_float(hi >> 16));
+    const float r0 = v0 - bf16_bits_to_float(hi & 0xFFFF), r1 = v1 - bf16_bits_to_float(hi >> 16);
+    const uint32_t lo = pack_bf16x2(r0, r1);
+    *reinterpret_cast<uint32_t*>(vlo + m * kRankPad + j) = lo;
+    if (vlo2 != nullptr)
+      *reinterpret_cast<uint32_t*>(vlo2 + m * kRankPad + j) =
+          pack_bf16x2(r0 - bf16_bits_to_float(lo & 0xFFFF), r1 - bf16_bits_to_float(lo >> 16));
     return;
   }
   const int64_t k = i - nv;
@@ -522,12 +535,12 @@ __global__ void vdb_finalize_kernel(const float* __restrict__ vpart, int ncb, co
 }
 
 cudaError_t launch_vdb_finalize(const float* vpart, int ncb, const float* dbpart, int ntb, int64_t M, int64_t N,
-                                int r, float scale, uint16_t* vs, uint16_t* vhi, uint16_t* vlo, float* dB,
-                                const BlockScalesJob& bs, cudaStream_t stream) {
+                                int r, float scale, uint16_t* vs, uint16_t* vhi, uint16_t* vlo, uint16_t* vlo2,
+                                float* dB, const BlockScalesJob& bs, cudaStream_t stream) {
   const int64_t total =
       M * (kRankPad / 2) + (dB != nullptr ? N * r : 0) + (bs.out != nullptr ? bs.groups : 0);
   vdb_finalize_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(vpart, ncb, dbpart, ntb, M, N,
-                                                                                       r, 16, scale, vs, vhi, vlo, dB,
+                                                                                       r, 16, scale, vs, vhi, vlo, vlo2, dB,
                                                                                        bs);
   return cudaGetLastError();
 }

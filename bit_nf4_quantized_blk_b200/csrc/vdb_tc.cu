@@ -15,6 +15,7 @@
 //                            x B^T tile (B, K-major)
 //   dB: D[128 columns][16] += dY tile read as A MN-major (M = columns,
 //                             K = tokens) x U^T hi tile, then x U^T lo tile
+//                             (and, where U comes in three parts, the third)
 // CTA (zc, zm) covers up to kVtCT column tiles x a range of token tiles,
 // token-tile major.  The V accumulator (16 TMEM columns) is double-buffered
 // and drained to the partial vpart[zc][m][16] after each token tile; the dB
@@ -43,11 +44,13 @@ constexpr int kVtGTile = kVtTok * kVtCol * 2;  // 32 KB: two [128][64] boxes
 constexpr int kVtGBox = kVtGTile / 2;          // 16 KB
 constexpr int kVtSmall = 16 * kVtCol * 2;      // 4 KB: two [16][64] boxes
 constexpr int kVtSmallBox = kVtSmall / 2;      // 2 KB
-constexpr int kVtStage = kVtGTile + 3 * kVtSmall;  // 44 KB
+template <int kParts>  // of U: 2 or 3
+constexpr int kVtStage = kVtGTile + (1 + kParts) * kVtSmall;  // 44 or 48 KB
 constexpr int kVtCTMax = 8;                    // column tiles per CTA
 constexpr int kVtThreads = 192;
 constexpr uint32_t kVtTmemCols = 256;          // V: 2 x 16, dB: up to 8 x 16
-constexpr int kVtSmem = 1024 + kVtStages * kVtStage + 256;
+template <int kParts>
+constexpr int kVtSmem = 1024 + kVtStages * kVtStage<kParts> + 256;
 
 struct VtBarriers {
   uint64_t full[kVtStages];
@@ -90,13 +93,16 @@ __device__ __forceinline__ void store16(float* dst, const uint32_t (&v)[16]) {
 
 }  // namespace
 
+template <int kParts>
 __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
     vdb_tc_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmBt,
-                  const __grid_constant__ CUtensorMap tmUh, const __grid_constant__ CUtensorMap tmUl, int64_t M,
-                  int64_t N, int ct, int tt, float* __restrict__ vpart, float* __restrict__ dbpart, int* status) {
+                  const __grid_constant__ CUtensorMap tmUh, const __grid_constant__ CUtensorMap tmUl,
+                  const __grid_constant__ CUtensorMap tmUl2, int64_t M, int64_t N, int ct, int tt,
+                  float* __restrict__ vpart, float* __restrict__ dbpart, int* status) {
+  constexpr int kStage = kVtStage<kParts>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  VtBarriers* bars = reinterpret_cast<VtBarriers*>(smem + kVtStages * kVtStage);
+  VtBarriers* bars = reinterpret_cast<VtBarriers*>(smem + kVtStages * kStage);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int zc = blockIdx.x, zm = blockIdx.y;
@@ -135,9 +141,9 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
       for (int i = 0; i < nsteps; ++i) {
         const int s = i % kVtStages, u = i / kVtStages;
         if (i >= kVtStages && !mbar_wait(&bars->empty[s], (u - 1) & 1, abort_flag, status)) break;
-        uint8_t* st = smem + s * kVtStage;
+        uint8_t* st = smem + s * kStage;
         const int c = (tc0 + i % ntc) * kVtCol, m = (tm0 + i / ntc) * kVtTok;
-        mbar_arrive_expect_tx(&bars->full[s], kVtStage);
+        mbar_arrive_expect_tx(&bars->full[s], kStage);
         tma_load_2d(st, &tmG, &bars->full[s], c, m);
         tma_load_2d(st + kVtGBox, &tmG, &bars->full[s], c + 64, m);
         tma_load_2d(st + kVtGTile, &tmBt, &bars->full[s], c, 0);
@@ -146,6 +152,10 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
         tma_load_2d(st + kVtGTile + kVtSmall + kVtSmallBox, &tmUh, &bars->full[s], m + 64, 0);
         tma_load_2d(st + kVtGTile + 2 * kVtSmall, &tmUl, &bars->full[s], m, 0);
         tma_load_2d(st + kVtGTile + 2 * kVtSmall + kVtSmallBox, &tmUl, &bars->full[s], m + 64, 0);
+        if constexpr (kParts == 3) {
+          tma_load_2d(st + kVtGTile + 3 * kVtSmall, &tmUl2, &bars->full[s], m, 0);
+          tma_load_2d(st + kVtGTile + 3 * kVtSmall + kVtSmallBox, &tmUl2, &bars->full[s], m + 64, 0);
+        }
         issued = i + 1;
       }
       // Every copy into shared memory has landed before the CTA can exit.
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
           break;
         }
         tc_fence_after();
-        const uint32_t st = smem_u32(smem + s * kVtStage);
+        const uint32_t st = smem_u32(smem + s * kStage);
         // dY tile as the MN-major A of dB: 64-column groups 16 KB apart
         // (the two boxes), 8-token groups 1 KB apart; a K = 16 step is 16
         // tokens = 2 KB.
@@ -190,6 +200,10 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
           const uint32_t acc_db = tmem + 32u + static_cast<uint32_t>(tc * 16);
           tc_mma_bf16_ss(acc_db, a_db, b_hi, idesc_db, (tm > 0 || kk > 0) ? 1u : 0u);
           tc_mma_bf16_ss(acc_db, a_db, b_lo, idesc_db, 1u);
+          if constexpr (kParts == 3) {
+            const uint64_t b_lo2 = smem_desc_k128(st + kVtGTile + 3 * kVtSmall + box * kVtSmallBox) + 2 * sub;
+            tc_mma_bf16_ss(acc_db, a_db, b_lo2, idesc_db, 1u);
+          }
         }
         tc_commit(&bars->empty[s]);
         if (tc == ntc - 1) tc_commit(&bars->v_full[vb]);
@@ -236,15 +250,15 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
   }
 }
 
-// The three rank-16 transposes of one call in one launch: B^T [16][N] from
-// B [N][ldb], and U^T hi / lo [16][ldm] from uhi / ulo [M][64];
+// The rank-16 transposes of one call in one launch: B^T [16][N] from
+// B [N][ldb], and U^T hi / lo (/ lo2) [16][ldm] from uhi / ulo (/ ulo2) [M][64];
 // dst[j][row] = src[row][j] for j < r, 0 for r <= j < 16.  Consecutive
 // threads take consecutive rows of one j, so the stores are contiguous.
 __global__ void rank16_transpose3_kernel(const uint16_t* __restrict__ B, int64_t ldb, int64_t N,
                                          const uint16_t* __restrict__ uhi, const uint16_t* __restrict__ ulo,
-                                         const float* __restrict__ u32, int64_t M, int64_t ldm, int r,
-                                         uint16_t* __restrict__ bt, uint16_t* __restrict__ uht,
-                                         uint16_t* __restrict__ ult) {
+                                         const uint16_t* __restrict__ ulo2, const float* __restrict__ u32, int64_t M,
+                                         int64_t ldm, int r, uint16_t* __restrict__ bt, uint16_t* __restrict__ uht,
+                                         uint16_t* __restrict__ ult, uint16_t* __restrict__ ult2) {
   int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const uint16_t* src;
   uint16_t* dst;
@@ -252,8 +266,8 @@ __global__ void rank16_transpose3_kernel(const uint16_t* __restrict__ B, int64_t
   if (i < 16 * N) {
     src = B, dst = bt, ld = ldb, rows = N, ldd = N;
   } else if (u32 != nullptr) {
-    // The saved fp32 U [M][r]: each thread forms both halves of one element,
-    // hi = bf16(u) and lo = bf16(u - hi).
+    // The saved fp32 U [M][r]: each thread forms the parts of one element,
+    // hi = bf16(u), lo = bf16(u - hi) and, if wanted, lo2 = bf16(u - hi - lo).
     i -= 16 * N;
     if (i >= 16 * M) return;
     const int j = static_cast<int>(i / M);
@@ -261,14 +275,19 @@ __global__ void rank16_transpose3_kernel(const uint16_t* __restrict__ B, int64_t
     const float v = j < r ? u32[row * r + j] : 0.0f;
     const uint32_t h = pack_bf16x2(v, 0.0f) & 0xFFFFu;
     uht[j * ldm + row] = static_cast<uint16_t>(h);
-    ult[j * ldm + row] = static_cast<uint16_t>(pack_bf16x2(v - bf16_bits_to_float(h), 0.0f) & 0xFFFFu);
+    const float rest = v - bf16_bits_to_float(h);
+    const uint32_t l = pack_bf16x2(rest, 0.0f) & 0xFFFFu;
+    ult[j * ldm + row] = static_cast<uint16_t>(l);
+    if (ult2 != nullptr)
+      ult2[j * ldm + row] = static_cast<uint16_t>(pack_bf16x2(rest - bf16_bits_to_float(l), 0.0f) & 0xFFFFu);
     return;
   } else {
     i -= 16 * N;
-    if (i >= 32 * M) return;
-    const bool lo = i >= 16 * M;
-    if (lo) i -= 16 * M;
-    src = lo ? ulo : uhi, dst = lo ? ult : uht, ld = kRankPad, rows = M, ldd = ldm;
+    const int64_t which = i / (16 * M);  // hi, lo, lo2
+    if (which >= (ult2 != nullptr ? 3 : 2)) return;
+    i -= which * 16 * M;
+    src = which == 0 ? uhi : which == 1 ? ulo : ulo2, dst = which == 0 ? uht : which == 1 ? ult : ult2;
+    ld = kRankPad, rows = M, ldd = ldm;
   }
   const int j = static_cast<int>(i / rows);
   const int64_t row = i % rows;
@@ -302,40 +321,54 @@ size_t vdb_tc_partial_bytes(int64_t M, int64_t N) {
          16 * sizeof(float);
 }
 
-cudaError_t launch_vdb_tc(const uint16_t* G, int64_t M, int64_t N, const uint16_t* B, int64_t ldb,
-                          const uint16_t* uhi, const uint16_t* ulo, const float* u32, int r, float scale, float* part,
-                          uint16_t* bt, uint16_t* uht, uint16_t* ult, uint16_t* vs, uint16_t* vhi, uint16_t* vlo,
-                          float* dB, const BlockScalesJob& bs, int* status, cudaStream_t stream) {
-  if (r < 1 || r > 16) return cudaErrorInvalidValue;
+namespace {
+
+template <int kParts>
+cudaError_t launch_vdb_kernel(const CUtensorMap& tg, const CUtensorMap& tbt, const CUtensorMap& tuh,
+                              const CUtensorMap& tul, const CUtensorMap& tul2, int64_t M, int64_t N,
+                              const VdbTcGrid& g, float* vpart, float* dbpart, int* status, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static DeviceOnce configured;
   e = configured.run(dev, [] {
-    return cudaFuncSetAttribute(vdb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kVtSmem);
+    return cudaFuncSetAttribute(vdb_tc_kernel<kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, kVtSmem<kParts>);
   });
   if (e != cudaSuccess) return e;
-  // B^T [16][N] and the hi / lo split of U^T [16][ldm]: the MMAs' K-major
-  // B operands.
+  vdb_tc_kernel<kParts><<<dim3(static_cast<unsigned>(g.ncb), static_cast<unsigned>(g.ntb)), kVtThreads,
+                          kVtSmem<kParts>, stream>>>(tg, tbt, tuh, tul, tul2, M, N, g.ct, g.tt, vpart, dbpart, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_vdb_tc(const uint16_t* G, int64_t M, int64_t N, const uint16_t* B, int64_t ldb,
+                          const uint16_t* uhi, const uint16_t* ulo, const uint16_t* ulo2, const float* u32, int r,
+                          float scale, float* part, uint16_t* bt, uint16_t* uht, uint16_t* ult, uint16_t* ult2,
+                          uint16_t* vs, uint16_t* vhi, uint16_t* vlo, uint16_t* vlo2, float* dB,
+                          const BlockScalesJob& bs, int* status, cudaStream_t stream) {
+  if (r < 1 || r > 16) return cudaErrorInvalidValue;
+  // B^T [16][N] and the split of U^T [16][ldm]: the MMAs' K-major B operands.
   const int64_t ldm = vdb_tc_ldm(M);
-  const int64_t items = 16 * N + (u32 != nullptr ? 16 : 32) * M;
-  rank16_transpose3_kernel<<<static_cast<unsigned>((items + 255) / 256), 256, 0, stream>>>(B, ldb, N, uhi, ulo, u32, M,
-                                                                                          ldm, r, bt, uht, ult);
-  e = cudaGetLastError();
+  const int parts = ult2 != nullptr ? 3 : 2;
+  const int64_t items = 16 * N + (u32 != nullptr ? 16 : 16 * parts) * M;
+  rank16_transpose3_kernel<<<static_cast<unsigned>((items + 255) / 256), 256, 0, stream>>>(
+      B, ldb, N, uhi, ulo, ulo2, u32, M, ldm, r, bt, uht, ult, ult2);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  CUtensorMap tg, tbt, tuh, tul;
+  CUtensorMap tg, tbt, tuh, tul, tul2;
   if (!encode_tensor_map_2d(&tg, G, M, N, kVtTok, 64)) return cudaErrorInvalidValue;
   if (!encode_tensor_map_2d(&tbt, bt, 16, N, 16, 64)) return cudaErrorInvalidValue;
   if (!encode_tensor_map_2d(&tuh, uht, 16, M, 16, 64, true, ldm)) return cudaErrorInvalidValue;
   if (!encode_tensor_map_2d(&tul, ult, 16, M, 16, 64, true, ldm)) return cudaErrorInvalidValue;
+  if (!encode_tensor_map_2d(&tul2, parts == 3 ? ult2 : ult, 16, M, 16, 64, true, ldm)) return cudaErrorInvalidValue;
   const VdbTcGrid g = vdb_tc_grid(M, N);
   float* vpart = part;
   float* dbpart = part + static_cast<int64_t>(g.ncb) * M * 16;
-  vdb_tc_kernel<<<dim3(static_cast<unsigned>(g.ncb), static_cast<unsigned>(g.ntb)), kVtThreads, kVtSmem, stream>>>(
-      tg, tbt, tuh, tul, M, N, g.ct, g.tt, vpart, dbpart, status);
-  e = cudaGetLastError();
+  e = parts == 3 ? launch_vdb_kernel<3>(tg, tbt, tuh, tul, tul2, M, N, g, vpart, dbpart, status, stream)
+                 : launch_vdb_kernel<2>(tg, tbt, tuh, tul, tul2, M, N, g, vpart, dbpart, status, stream);
   if (e != cudaSuccess) return e;
-  return launch_vdb_finalize(vpart, g.ncb, dbpart, g.ntb, M, N, r, scale, vs, vhi, vlo, dB, bs, stream);
+  return launch_vdb_finalize(vpart, g.ncb, dbpart, g.ntb, M, N, r, scale, vs, vhi, vlo, vlo2, dB, bs, stream);
 }
 
 }  // namespace qnf4

@@ -129,15 +129,15 @@ def test_linear_backward(M, N, K, r, fmt, saved_u):
 
     g, b64 = _f64(dY), _f64(B)
     u = U.double().cpu().numpy() if saved_u else xh @ _f64(A).T
-    # V and U enter as bf16 pairs hi + lo, off by at most 2^-16 of the value; V itself is an fp32 sum of N products, and
-    # each output one of M: at most (terms) 2^-24 of the sum of magnitudes each.
+    # V and U enter as three bf16 parts, which hold all of their fp32 values; V itself is an fp32 sum of N products, and
+    # each output one of 3 M: at most (terms) 2^-24 of the sum of magnitudes each.
     absv = np.abs(g) @ np.abs(b64)
     ref = s * (g @ b64).T @ xh
-    tol = (2.0**-16 + (N + M + 2) * 2.0**-24) * s * absv.T @ np.abs(xh) + 1e-30
+    tol = (N + 3 * M + 2) * 2.0**-24 * s * absv.T @ np.abs(xh) + 1e-30
     assert (np.abs(_f64(dA[:r]) - ref) <= tol).all()
     absu = np.abs(u) if saved_u else np.abs(xh) @ np.abs(_f64(A)).T
     ref = s * g.T @ u
-    tol = (2.0**-16 + (M + 2 + (0 if saved_u else K)) * 2.0**-24) * s * np.abs(g).T @ absu + 1e-30
+    tol = (3 * M + 2 + (0 if saved_u else K)) * 2.0**-24 * s * np.abs(g).T @ absu + 1e-30
     assert (np.abs(_f64(dB[:N]) - ref) <= tol).all()
 
     # dX does not depend on X: the same bits as from the bf16 activation.
@@ -145,12 +145,13 @@ def test_linear_backward(M, N, K, r, fmt, saved_u):
     dA2, dB2 = torch.empty((r, K), device="cuda"), torch.empty((N, r), device="cuda")
     binding.qlora_linear_bwd(w, x.cuda(), dYc, Ac, Bc, r, s, dX2, 0, dA2, dB2, ws, U=U)
     assert torch.equal(dX, dX2)
-    if saved_u:
-        assert torch.equal(dB[:N], dB2)
+    if saved_u:  # the bf16 path splits U in two parts
+        assert (dB[:N] - dB2).norm() <= 4e-6 * dB2.norm()
 
 
 def test_linear_backward_agrees_with_the_dequantized_activation():
-    """qlora_linear_bwd on the checkpoint's bf16 values is the same product, summed in another order."""
+    """qlora_linear_bwd on the checkpoint's bf16 values is the same product, from V and U in two bf16 parts (2^-17 at
+    most) and summed in another order."""
     M, N, K, r = 700, 192, 1024, 16
     W, A, B, dY, x = _linear(M, N, K, r, 77)
     w, ws = gpu_quantize(W), workspace(M, N, K, r)
@@ -164,7 +165,7 @@ def test_linear_backward_agrees_with_the_dequantized_activation():
             call(w, X, dY.cuda(), A.cuda(), B.cuda(), r, 1.0, None, 0, dA, dB, ws)
             outs.append((dA, dB))
         for p, q in zip(*outs):
-            assert (p - q).norm() <= 4e-6 * q.norm()
+            assert (p - q).norm() <= 2.0**-17 * q.norm()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
