@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(ColsumShape<kFormat, kRT>::kThreads, 1)
                        const uint16_t* __restrict__ vlo2, int splits, float* __restrict__ part) {
   using S = ColsumShape<kFormat, kRT>;
   extern __shared__ __align__(16) uint8_t smem[];
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int wc = warp % kCsWC, wt = warp / kCsWC;
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(128) act8_colsum_reduce_kernel(const float* __
                                                                  int splits, float scale, float* __restrict__ dst,
                                                                  int dst_rc) {
   __shared__ float tile[kCrCols][17];
+  pdl_wait_prior();
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kCrCols;
   const int jj = threadIdx.x / (kCrCols / 4), cc = threadIdx.x % (kCrCols / 4) * 4, j = blockIdx.y * 16 + jj;
   const int64_t slice = static_cast<int64_t>(gridDim.y) * 16 * C;
@@ -451,24 +453,61 @@ cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint
                               : launch_colsum_format<kAct8E4m3>(x, hi, lo, lo2, rt, part, &splits, stream);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols), static_cast<unsigned>(rt));
-  act8_colsum_reduce_kernel<<<grid, 128, 0, stream>>>(part, x.cols, r, splits, scale, dst, dst_rc ? 1 : 0);
-  return cudaGetLastError();
+  return launch_dependent(act8_colsum_reduce_kernel, grid, 128, stream, part, x.cols, r, splits, scale, dst,
+                          dst_rc ? 1 : 0);
 }
 
 // ---------------------------------------------------------------------------
 // skinny: part[z][m][j] = sum_{k in split z} X^[m][k] A[j][k]
 // ---------------------------------------------------------------------------
-// m16n8k16 MMAs with D = [16 tokens][8 j], K = the columns.  Within a 64-column
-// block lane (g, t) holds the 16 columns 16t .. 16t + 15 of its rows, and MMA
-// step s takes columns 16t + 4s .. + 3 as the lane's four K slots in both
-// operands (a permutation of the block's columns): 16 code bytes per row and
-// two 16-byte loads per row of A.  A warp covers 32 tokens, so A (from L1) is
-// read once per two token tiles.
+// m16n8k16 MMAs with D = [16 tokens][8 j], K = the columns.  Which column a K
+// slot stands for is free as long as both operands agree: in each half (32
+// columns) of a 64-column block lane (g, t) takes columns 8t .. 8t + 7, of its
+// token rows (8 code bytes) and of its rows of A (16 bytes), and MMA step s of
+// the half takes columns 8t + 4s .. + 3 as the lane's four slots.  Every load
+// is 8 or 16 bytes and feeds its registers as it is.
+//
+// A CTA is kSkWT groups of 32 tokens x kSkWK column shares: warps of one share
+// read the same blocks of A (once from L2, then from L1), and the shares' sums
+// are added in shared memory in a fixed order.  The codes and steps of a
+// warp's next block are loaded before its current one is multiplied.
 namespace {
 
-constexpr int kSkWarps = 4;
-constexpr int kSkMT = 2;  // 16-token tiles per warp
-constexpr int kSkTokens = kSkWarps * kSkMT * 16;
+constexpr int kSkWT = 4, kSkWK = 2;
+constexpr int kSkWarps = kSkWT * kSkWK;
+constexpr int kSkMT = 2;  // 16-token tiles of a warp
+constexpr int kSkWarpTokens = kSkMT * 16, kSkTokens = kSkWT * kSkWarpTokens;
+
+int act8_skinny_splits(int64_t M, int64_t K) {
+  const int64_t tiles = (M + kSkTokens - 1) / kSkTokens, blocks = K / kBlock;
+  int64_t s = (148 + tiles - 1) / tiles;  // a CTA per SM
+  const int64_t most = (blocks + kSkWK - 1) / kSkWK;  // a block per warp at least
+  if (s > most) s = most;
+  const int64_t room = skinny_splits(M, K);  // what the workspace's partials are sized for
+  return static_cast<int>(s < room ? s : room);
+}
+
+template <int kFormat>
+struct SkinnyX {  // one lane's part of a 64-column block of 32 tokens
+  uint2 c[kSkMT][2][2];     // [tile][row g, g + 8][half]
+  uint32_t s[kSkMT][2];     // packed steps
+
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint16_t* step, int64_t M, int64_t K, int64_t m0,
+                                       int64_t kb, bool live) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int a = 0; a < kSkMT; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t row = m0 + a * 16 + h * 8 + g;
+        const bool ok = live && row < M;
+        const uint2* src = reinterpret_cast<const uint2*>(codes + (ok ? row * K + kb * kBlock + t * 8 : 0));
+        c[a][h][0] = ok ? __ldg(src) : make_uint2(0, 0);
+        c[a][h][1] = ok ? __ldg(src + 4) : make_uint2(0, 0);
+        s[a][h] = ok ? __ldg(step + row * (K / kBlock) + kb) : 0u;
+      }
+  }
+};
 
 }  // namespace
 
@@ -478,13 +517,14 @@ __global__ void __launch_bounds__(32 * kSkWarps) act8_skinny_kernel(const uint8_
                                                                     const uint16_t* __restrict__ A, int64_t M,
                                                                     int64_t K, int r, int splits,
                                                                     float* __restrict__ part) {
+  constexpr int kPitch = NT * 8 + 8;  // floats: rows g apart by 8 banks, so the lanes' pairs never meet
+  extern __shared__ __align__(16) float sums[];  // [kSkWK][kSkTokens][kPitch]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSkTokens + warp * (kSkMT * 16);
-  if (m0 >= M) return;
+  const int g = lane >> 2, t = lane & 3, wt = warp % kSkWT, wk = warp / kSkWT;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSkTokens + wt * kSkWarpTokens;
   const int z = blockIdx.y;
   const int64_t kblocks = K / kBlock;
-  const int64_t b0 = kblocks * z / splits, b1 = kblocks * (z + 1) / splits;
+  const int64_t b0 = kblocks * z / splits + wk, b1 = kblocks * (z + 1) / splits;
 
   float acc[kSkMT][NT][4];
 #pragma unroll
@@ -494,72 +534,93 @@ __global__ void __launch_bounds__(32 * kSkWarps) act8_skinny_kernel(const uint8_
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.0f;
 
-  for (int64_t kb = b0; kb < b1; ++kb) {
-    uint4 c[kSkMT][2];
-    uint32_t s[kSkMT][2];
+  SkinnyX<kFormat> next;
+  next.load(codes, step, M, K, m0, b0, b0 < b1);
+  for (int64_t kb = b0; kb < b1; kb += kSkWK) {
+    SkinnyX<kFormat> x = next;
+    next.load(codes, step, M, K, m0, kb + kSkWK, kb + kSkWK < b1);
 #pragma unroll
-    for (int a = 0; a < kSkMT; ++a)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t row = m0 + a * 16 + h * 8 + g;
-        const bool ok = row < M;
-        c[a][h] = ok ? ld_stream_u4(codes + row * K + kb * kBlock + t * 16) : make_uint4(0, 0, 0, 0);
-        s[a][h] = ok ? __ldg(step + row * kblocks + kb) : 0u;
-        s[a][h] |= s[a][h] << 16;
-      }
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {  // columns 16t + 4w .. + 3
-      uint32_t af[kSkMT][4];
-#pragma unroll
-      for (int a = 0; a < kSkMT; ++a)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t word = w == 0 ? c[a][h].x : w == 1 ? c[a][h].y : w == 2 ? c[a][h].z : c[a][h].w;
-          af[a][h] = act8_decode2<kFormat, 0>(word, s[a][h]);
-          af[a][h + 2] = act8_decode2<kFormat, 2>(word, s[a][h]);
-        }
+    for (int half = 0; half < 2; ++half) {
+      uint4 av[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int j = nt * 8 + g;
-        uint2 v = make_uint2(0, 0);
-        if (j < r) v = __ldg(reinterpret_cast<const uint2*>(A + j * K + kb * kBlock + t * 16 + w * 4));
-        const uint32_t bf[2] = {v.x, v.y};
+        av[nt] = j < r ? __ldg(reinterpret_cast<const uint4*>(A + j * K + kb * kBlock + half * 32 + t * 8))
+                       : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-        for (int a = 0; a < kSkMT; ++a) mma_16816(acc[a][nt], af[a], bf);
+      for (int w = 0; w < 2; ++w) {  // columns 8t + 4w .. + 3 of the half
+        uint32_t af[kSkMT][4];
+#pragma unroll
+        for (int a = 0; a < kSkMT; ++a)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t word = w == 0 ? x.c[a][h][half].x : x.c[a][h][half].y;
+            const uint32_t s2 = x.s[a][h] | (x.s[a][h] << 16);
+            af[a][h] = act8_decode2<kFormat, 0>(word, s2);
+            af[a][h + 2] = act8_decode2<kFormat, 2>(word, s2);
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t bf[2] = {w == 0 ? av[nt].x : av[nt].z, w == 0 ? av[nt].y : av[nt].w};
+#pragma unroll
+          for (int a = 0; a < kSkMT; ++a) mma_16816(acc[a][nt], af[a], bf);
+        }
       }
     }
   }
 #pragma unroll
   for (int a = 0; a < kSkMT; ++a)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t row = m0 + a * 16 + h * 8 + g;
-      if (row >= M) continue;
-      float* dst = part + (static_cast<int64_t>(z) * M + row) * kRankPad;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<float2*>(dst + nt * 8 + 2 * t) = make_float2(acc[a][nt][2 * h], acc[a][nt][2 * h + 1]);
+        *reinterpret_cast<float2*>(sums + ((wk * kSkTokens) + wt * kSkWarpTokens + a * 16 + h * 8 + g) * kPitch + nt * 8 +
+                                   2 * t) = make_float2(acc[a][nt][2 * h], acc[a][nt][2 * h + 1]);
+  __syncthreads();
+  constexpr int kOut = kSkTokens * NT * 2;  // in fours
+  for (int i = threadIdx.x; i < kOut; i += 32 * kSkWarps) {
+    const int m = i / (NT * 2), j = i % (NT * 2) * 4;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kSkTokens + m;
+    if (row >= M) break;
+    float4 s = *reinterpret_cast<const float4*>(sums + m * kPitch + j);
+#pragma unroll
+    for (int w = 1; w < kSkWK; ++w) {
+      const float4 o = *reinterpret_cast<const float4*>(sums + (w * kSkTokens + m) * kPitch + j);
+      s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
     }
+    *reinterpret_cast<float4*>(part + (static_cast<int64_t>(z) * M + row) * kRankPad + j) = s;
+  }
 }
 
 namespace {
 
-template <int kFormat>
-void launch_skinny_format(const Act8View& x, const uint16_t* A, int r, int splits, float* part, cudaStream_t stream) {
+template <int kFormat, int NT>
+cudaError_t launch_skinny_nt(const Act8View& x, const uint16_t* A, int r, int splits, float* part,
+                             cudaStream_t stream) {
+  constexpr int smem = kSkWK * kSkTokens * (NT * 8 + 8) * static_cast<int>(sizeof(float));
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static DeviceOnce configured;
+  e = configured.run(dev, [] {
+    return cudaFuncSetAttribute(act8_skinny_kernel<kFormat, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.rows + kSkTokens - 1) / kSkTokens), static_cast<unsigned>(splits));
-  const int threads = 32 * kSkWarps;
+  act8_skinny_kernel<kFormat, NT><<<grid, 32 * kSkWarps, smem, stream>>>(x.codes, x.step, A, x.rows, x.cols, r, splits,
+                                                                        part);
+  return cudaGetLastError();
+}
+
+template <int kFormat>
+cudaError_t launch_skinny_format(const Act8View& x, const uint16_t* A, int r, int splits, float* part,
+                                 cudaStream_t stream) {
   switch ((r + 15) / 16) {
-    case 1:
-      act8_skinny_kernel<kFormat, 2><<<grid, threads, 0, stream>>>(x.codes, x.step, A, x.rows, x.cols, r, splits, part);
-      break;
-    case 2:
-      act8_skinny_kernel<kFormat, 4><<<grid, threads, 0, stream>>>(x.codes, x.step, A, x.rows, x.cols, r, splits, part);
-      break;
-    case 3:
-      act8_skinny_kernel<kFormat, 6><<<grid, threads, 0, stream>>>(x.codes, x.step, A, x.rows, x.cols, r, splits, part);
-      break;
-    default:
-      act8_skinny_kernel<kFormat, 8><<<grid, threads, 0, stream>>>(x.codes, x.step, A, x.rows, x.cols, r, splits, part);
+    case 1: return launch_skinny_nt<kFormat, 2>(x, A, r, splits, part, stream);
+    case 2: return launch_skinny_nt<kFormat, 4>(x, A, r, splits, part, stream);
+    case 3: return launch_skinny_nt<kFormat, 6>(x, A, r, splits, part, stream);
+    default: return launch_skinny_nt<kFormat, 8>(x, A, r, splits, part, stream);
   }
 }
 
@@ -567,12 +628,9 @@ void launch_skinny_format(const Act8View& x, const uint16_t* A, int r, int split
 
 cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, const SkinnyOut& out,
                                cudaStream_t stream) {
-  const int splits = skinny_splits(x.rows, x.cols);
-  if (x.format == kAct8Int8)
-    launch_skinny_format<kAct8Int8>(x, A, r, splits, part, stream);
-  else
-    launch_skinny_format<kAct8E4m3>(x, A, r, splits, part, stream);
-  const cudaError_t e = cudaGetLastError();
+  const int splits = act8_skinny_splits(x.rows, x.cols);
+  const cudaError_t e = x.format == kAct8Int8 ? launch_skinny_format<kAct8Int8>(x, A, r, splits, part, stream)
+                                              : launch_skinny_format<kAct8E4m3>(x, A, r, splits, part, stream);
   if (e != cudaSuccess) return e;
   return launch_skinny_finalize(part, x.rows, r, splits, out, stream);
 }

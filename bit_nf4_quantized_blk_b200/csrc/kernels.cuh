@@ -7,6 +7,22 @@
 
 namespace qnf4 {
 
+// Launch a kernel that starts with pdl_wait_prior() behind one that lets its
+// dependents go early (pdl_launch_dependents): its launch overlaps that one.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---------------------------------------------------------------------------
 // Quantize + double quantize (quantize.cu)
 // ---------------------------------------------------------------------------
@@ -263,7 +279,7 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 size_t act8_colsum_partial_bytes(int64_t M, int64_t C);
 cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2, int r,
                                float scale, float* part, float* dst, bool dst_rc, cudaStream_t stream);
-// launch_skinny's product X^ A^T from a checkpoint (A [r][K] bf16, 8-byte
+// launch_skinny's product X^ A^T from a checkpoint (A [r][K] bf16, 16-byte
 // aligned rows); `part` as for launch_skinny.
 cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, const SkinnyOut& out,
                                cudaStream_t stream);

@@ -194,6 +194,7 @@ __global__ void skinny_finalize_kernel(const float* __restrict__ part, int64_t M
   const int j = static_cast<int>(i % (kRankPad / 2)) * 2;
   float v0 = 0.0f, v1 = 0.0f;
   if (j < r) {
+#pragma unroll 8
     for (int z = 0; z < splits; ++z) {
       const float2 p = *reinterpret_cast<const float2*>(part + (static_cast<int64_t>(z) * M + m) * kRankPad + j);
       v0 += p.x;
@@ -503,6 +504,7 @@ __global__ void vdb_finalize_kernel(const float* __restrict__ vpart, int ncb, co
     const int j = static_cast<int>(i % (kRankPad / 2)) * 2;
     float v0 = 0.0f, v1 = 0.0f;
     if (j < r) {
+#pragma unroll 8
       for (int z = 0; z < ncb; ++z) {
         const float2 p = *reinterpret_cast<const float2*>(vpart + (static_cast<int64_t>(z) * M + m) * r16 + j);
         v0 += p.x;
@@ -530,6 +532,7 @@ __global__ void vdb_finalize_kernel(const float* __restrict__ vpart, int ncb, co
   const int64_t c = k / r;
   const int j = static_cast<int>(k % r);
   float s = 0.0f;
+#pragma unroll 8
   for (int z = 0; z < ntb; ++z) s += dbpart[(static_cast<int64_t>(z) * N + c) * r16 + j];
   dB[c * r + j] = scale * s;
 }

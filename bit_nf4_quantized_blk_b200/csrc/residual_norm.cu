@@ -25,6 +25,7 @@
 // The backward's column sums stay in registers over all rows of a CTA; each
 // CTA writes one partial row and residual_norm_finish_kernel adds those in a
 // fixed order (no atomics).
+#include <algorithm>
 #include <type_traits>
 
 #include "act8.cuh"
@@ -305,6 +306,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
   uint8_t* factor_branch = factor_pre + W::kBytes;
   __shared__ __align__(16) float sums[4][32];
   const int tid = threadIdx.x % TPR;
+  pdl_launch_dependents();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
   const TRes* dh_out = static_cast<const TRes*>(p.dh_out);
@@ -492,6 +494,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
 // 32 columns; its 32 warps take every 32nd row, then add in a fixed tree.
 __global__ void __launch_bounds__(1024) residual_norm_finish_kernel(ResidualNormBwd p, int count) {
   __shared__ float sums[32][33];
+  pdl_wait_prior();
   if (blockIdx.y == 0 ? p.dw_pre == nullptr : p.dgate == nullptr && p.dw_post == nullptr) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t d0 = static_cast<int64_t>(blockIdx.x) * 32;
@@ -594,7 +597,13 @@ cudaError_t launch_bwd(const ResidualNormBwd& p, cudaStream_t stream) {
 
 }  // namespace
 
-int residual_norm_bwd_ctas(int64_t M, int64_t D) { return static_cast<int>(norm_ctas(M, D, kBwdResident)); }
+int residual_norm_bwd_ctas(int64_t M, int64_t D) {
+  // Every CTA leaves a partial row of the column sums: with few rows, four or
+  // more per CTA keep those below the operands themselves.
+  const int64_t full = norm_ctas(M, D, kBwdResident);
+  const int64_t few = std::max<int64_t>(std::min<int64_t>(full, 148), M / 4);
+  return static_cast<int>(std::min(full, few));
+}
 
 cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cudaStream_t stream) {
   return res_fp32 ? launch_fwd<float>(p, stream) : launch_fwd<uint16_t>(p, stream);
@@ -603,9 +612,8 @@ cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cud
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cudaStream_t stream) {
   const cudaError_t e = res_fp32 ? launch_bwd<float>(p, stream) : launch_bwd<uint16_t>(p, stream);
   if (e != cudaSuccess || (!p.dw_pre && !p.dgate && !p.dw_post)) return e;
-  residual_norm_finish_kernel<<<dim3(static_cast<unsigned>(p.D / 32), 2), 1024, 0, stream>>>(
-      p, residual_norm_bwd_ctas(p.M, p.D));
-  return cudaGetLastError();
+  return launch_dependent(residual_norm_finish_kernel, dim3(static_cast<unsigned>(p.D / 32), 2), 1024, stream, p,
+                          residual_norm_bwd_ctas(p.M, p.D));
 }
 
 }  // namespace qnf4
