@@ -467,20 +467,37 @@ cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint
 // the half takes columns 8t + 4s .. + 3 as the lane's four slots.  Every load
 // is 8 or 16 bytes and feeds its registers as it is.
 //
-// A CTA is kSkWT groups of 32 tokens x kSkWK column shares: warps of one share
-// read the same blocks of A (once from L2, then from L1), and the shares' sums
-// are added in shared memory in a fixed order.  The codes and steps of a
-// warp's next block are loaded before its current one is multiplied.
+// A CTA is kSkWT groups of 32 tokens x kSkWK column shares.  The shares' blocks
+// of A come through a ring in shared memory (read through L1, the rows of a
+// block, 2 K bytes apart, evict each other where K is a power of two: five
+// times slower at K = 8192), and the shares' sums are added in shared memory
+// in a fixed order.  The codes and steps of a warp's next block are loaded
+// before its current one is multiplied.
 namespace {
 
 constexpr int kSkWT = 4, kSkWK = 2;
 constexpr int kSkWarps = kSkWT * kSkWK;
 constexpr int kSkMT = 2;  // 16-token tiles of a warp
 constexpr int kSkWarpTokens = kSkMT * 16, kSkTokens = kSkWT * kSkWarpTokens;
+constexpr int kSkStages = 3;
+
+template <int NT>
+struct SkinnyShape {
+  static constexpr int kTile = NT * 8 * 128;  // one block of A: [j][64 columns]
+  static constexpr int kRing = kSkStages * kSkWK * kTile;
+  static constexpr int kPitch = NT * 8 + 8;   // floats: rows g apart by 8 banks, so the lanes' pairs never meet
+  static constexpr int kSums = kSkWK * kSkTokens * kPitch * static_cast<int>(sizeof(float));
+  static constexpr int kSmem = kRing > kSums ? kRing : kSums;
+};
+
+// Byte offset of 16-byte chunk c of row j in a block of A: odd rows have their
+// halves exchanged, so that two rows' 64 bytes make a conflict-free read.
+__device__ __forceinline__ int sk_chunk(int j, int c) { return j * 128 + (c ^ ((j & 1) << 2)) * 16; }
 
 int act8_skinny_splits(int64_t M, int64_t K) {
   const int64_t tiles = (M + kSkTokens - 1) / kSkTokens, blocks = K / kBlock;
-  int64_t s = (148 + tiles - 1) / tiles;  // a CTA per SM
+  int64_t s = 148 / tiles;  // one wave of a CTA per SM
+  if (s < 1) s = 1;
   const int64_t most = (blocks + kSkWK - 1) / kSkWK;  // a block per warp at least
   if (s > most) s = most;
   const int64_t room = skinny_splits(M, K);  // what the workspace's partials are sized for
@@ -517,14 +534,31 @@ __global__ void __launch_bounds__(32 * kSkWarps) act8_skinny_kernel(const uint8_
                                                                     const uint16_t* __restrict__ A, int64_t M,
                                                                     int64_t K, int r, int splits,
                                                                     float* __restrict__ part) {
-  constexpr int kPitch = NT * 8 + 8;  // floats: rows g apart by 8 banks, so the lanes' pairs never meet
-  extern __shared__ __align__(16) float sums[];  // [kSkWK][kSkTokens][kPitch]
+  using S = SkinnyShape<NT>;
+  constexpr int kPitch = S::kPitch;
+  extern __shared__ __align__(16) uint8_t ring[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3, wt = warp % kSkWT, wk = warp / kSkWT;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSkTokens + wt * kSkWarpTokens;
   const int z = blockIdx.y;
   const int64_t kblocks = K / kBlock;
-  const int64_t b0 = kblocks * z / splits + wk, b1 = kblocks * (z + 1) / splits;
+  const int64_t first = kblocks * z / splits, b1 = kblocks * (z + 1) / splits;
+  const int steps = static_cast<int>((b1 - first + kSkWK - 1) / kSkWK);  // of kSkWK blocks
+
+  auto issue = [&](int i) {
+    if (i < steps) {
+      uint8_t* st = ring + (i % kSkStages) * (kSkWK * S::kTile);
+#pragma unroll
+      for (int q = 0; q < kSkWK * S::kTile / 16 / (32 * kSkWarps); ++q) {
+        const int chunk = q * (32 * kSkWarps) + threadIdx.x;
+        const int share = chunk / (S::kTile / 16), rest = chunk % (S::kTile / 16), j = rest / 8, c = rest % 8;
+        const int64_t kb = first + static_cast<int64_t>(i) * kSkWK + share;
+        const bool ok = j < r && kb < b1;
+        cp_async_16(st + share * S::kTile + sk_chunk(j, c), A + (ok ? j * K + kb * kBlock + c * 8 : 0), ok);
+      }
+    }
+    cp_async_commit();
+  };
 
   float acc[kSkMT][NT][4];
 #pragma unroll
@@ -534,20 +568,24 @@ __global__ void __launch_bounds__(32 * kSkWarps) act8_skinny_kernel(const uint8_
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.0f;
 
+#pragma unroll
+  for (int i = 0; i < kSkStages - 1; ++i) issue(i);
   SkinnyX<kFormat> next;
-  next.load(codes, step, M, K, m0, b0, b0 < b1);
-  for (int64_t kb = b0; kb < b1; kb += kSkWK) {
+  next.load(codes, step, M, K, m0, first + wk, first + wk < b1);
+  for (int i = 0; i < steps; ++i) {
+    const int64_t kb = first + static_cast<int64_t>(i) * kSkWK + wk;
     SkinnyX<kFormat> x = next;
     next.load(codes, step, M, K, m0, kb + kSkWK, kb + kSkWK < b1);
+    cp_async_wait<kSkStages - 2>();
+    __syncthreads();  // everyone's copies of this stage are there, and the one before is read
+    issue(i + kSkStages - 1);
+    const uint8_t* tile = ring + (i % kSkStages) * (kSkWK * S::kTile) + wk * S::kTile;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint4 av[NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int j = nt * 8 + g;
-        av[nt] = j < r ? __ldg(reinterpret_cast<const uint4*>(A + j * K + kb * kBlock + half * 32 + t * 8))
-                       : make_uint4(0, 0, 0, 0);
-      }
+      for (int nt = 0; nt < NT; ++nt)
+        av[nt] = *reinterpret_cast<const uint4*>(tile + sk_chunk(nt * 8 + g, half * 4 + t));
 #pragma unroll
       for (int w = 0; w < 2; ++w) {  // columns 8t + 4w .. + 3 of the half
         uint32_t af[kSkMT][4];
@@ -569,6 +607,9 @@ __global__ void __launch_bounds__(32 * kSkWarps) act8_skinny_kernel(const uint8_
       }
     }
   }
+  cp_async_wait<0>();
+  __syncthreads();  // the ring's space takes the sums
+  float* sums = reinterpret_cast<float*>(ring);  // [kSkWK][kSkTokens][kPitch]
 #pragma unroll
   for (int a = 0; a < kSkMT; ++a)
 #pragma unroll
@@ -598,7 +639,7 @@ namespace {
 template <int kFormat, int NT>
 cudaError_t launch_skinny_nt(const Act8View& x, const uint16_t* A, int r, int splits, float* part,
                              cudaStream_t stream) {
-  constexpr int smem = kSkWK * kSkTokens * (NT * 8 + 8) * static_cast<int>(sizeof(float));
+  constexpr int smem = SkinnyShape<NT>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
