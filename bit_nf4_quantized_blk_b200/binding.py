@@ -184,13 +184,15 @@ def _dev(t, name: str, dtypes=None, need: int | None = None) -> int:
         raise TypeError(f"{name}: dtype {t.dtype}, expected one of {', '.join(str(d) for d in dtypes)}")
     if need is not None and t.numel() < need:
         raise ValueError(f"{name}: {t.numel()} elements, needs at least {need}")
-    _check_placement(t, name)
+    device = t.get_device()
+    if device < 0 or device != _current_device():
+        _check_placement(t, name)
     return t.data_ptr()
 
 
 # The current device and its current stream, once a CUDA tensor exists (so CUDA is initialised): the calls behind
-# torch.cuda.current_device / current_stream without their initialisation check and Stream object, which took half of
-# a short call's host time (one call per tensor argument).
+# torch.cuda.current_device / current_stream without their initialisation check and Stream object.  A short call is
+# bound by the host, and these were half of its time.
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -219,7 +221,7 @@ def _rank_ok(r: int) -> bool:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        if _raw_stream is None or not torch.cuda.is_initialized():
+        if _raw_stream is None:
             return torch.cuda.current_stream().cuda_stream
         return _raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -576,10 +578,10 @@ def qlora_linear_bwd_act8(w: NF4Weight, X: Act8, dY, A, B, r: int, scale: float,
     gp = _dev(dY, "dY", _BF16_BITS, M * N if known else None)
     ap = _dev(A, "A", _BF16_BITS, r * K if sized else None)
     bp = _dev(B, "B", _BF16_BITS, N * r if sized else None)
-    up = _dev_opt(U, "U", _F32, M * r if sized else None)
-    dxp = _dev_opt(dX, "dX", _BF16_BITS, M * K if known else None)
-    dap = _dev_opt(dA, "dA", _F32, r * K if sized else None)
-    dbp = _dev_opt(dB, "dB", _F32, N * r if sized else None)
+    up = None if U is None else _dev(U, "U", _F32, M * r if sized else None)
+    dxp = None if dX is None else _dev(dX, "dX", _BF16_BITS, M * K if known else None)
+    dap = None if dA is None else _dev(dA, "dA", _F32, r * K if sized else None)
+    dbp = None if dB is None else _dev(dB, "dB", _F32, N * r if sized else None)
     wsp, wsb = _ws(ws)
     _check("qlora_linear_bwd_act8",
            lib().qlora_linear_bwd_act8(ctypes.byref(st), ctypes.byref(sx), gp, ap, bp, r, float(scale), up, dxp,
@@ -602,15 +604,15 @@ def qlora_residual_norm_fwd(h, y, w_post, gate, scale: float, w_pre, eps: float,
     M, D, res = _stream_shape(h, "h")
     n, rd = M * D, (h.dtype,)
     hp = _dev(h, "h")
-    yp = _dev_opt(y, "y", _BF16_BITS, n)
-    wpp = _dev_opt(w_post, "w_post", _F32, D)
-    gp = _dev_opt(gate, "gate", _F32, D)
-    wrp = _dev_opt(w_pre, "w_pre", _F32, D)
-    hop = _dev_opt(h_out, "h_out", rd, n)
-    xp = _dev_opt(x, "x", _BF16_BITS, n)
+    yp = None if y is None else _dev(y, "y", _BF16_BITS, n)
+    wpp = None if w_post is None else _dev(w_post, "w_post", _F32, D)
+    gp = None if gate is None else _dev(gate, "gate", _F32, D)
+    wrp = None if w_pre is None else _dev(w_pre, "w_pre", _F32, D)
+    hop = None if h_out is None else _dev(h_out, "h_out", rd, n)
+    xp = None if x is None else _dev(x, "x", _BF16_BITS, n)
     cp = None if ckpt is None else ctypes.byref(ckpt.c_struct())
-    rpp = _dev_opt(rstd_post, "rstd_post", _F32, M)
-    rrp = _dev_opt(rstd_pre, "rstd_pre", _F32, M)
+    rpp = None if rstd_post is None else _dev(rstd_post, "rstd_post", _F32, M)
+    rrp = None if rstd_pre is None else _dev(rstd_pre, "rstd_pre", _F32, M)
     _check("qlora_residual_norm_fwd",
            lib().qlora_residual_norm_fwd(hp, yp, wpp, gp, float(scale), wrp, float(eps), M, D, res, hop, xp, cp, rpp,
                                          rrp, _stream(stream)))
@@ -628,20 +630,20 @@ def qlora_residual_norm_bwd(dh_out, dx, h_out, y, w_post, gate, scale: float, w_
         raise ValueError("one of dh_out, h_out and dh gives the shape")
     M, D, res = _stream_shape(*shaped)
     n, rd = M * D, (shaped[0].dtype,)
-    dhop = _dev_opt(dh_out, "dh_out", rd, n)
-    dxp = _dev_opt(dx, "dx", _BF16_BITS, n)
-    hp = _dev_opt(h_out, "h_out", rd, n)
-    yp = _dev_opt(y, "y", _BF16_BITS, n)
-    wpp = _dev_opt(w_post, "w_post", _F32, D)
-    gp = _dev_opt(gate, "gate", _F32, D)
-    wrp = _dev_opt(w_pre, "w_pre", _F32, D)
-    rpp = _dev_opt(rstd_post, "rstd_post", _F32, M)
-    rrp = _dev_opt(rstd_pre, "rstd_pre", _F32, M)
-    dhp = _dev_opt(dh, "dh", rd, n)
-    dyp = _dev_opt(dy, "dy", _BF16_BITS, n)
-    dwp = _dev_opt(dw_post, "dw_post", _F32, D)
-    dgp = _dev_opt(dgate, "dgate", _F32, D)
-    dwr = _dev_opt(dw_pre, "dw_pre", _F32, D)
+    dhop = None if dh_out is None else _dev(dh_out, "dh_out", rd, n)
+    dxp = None if dx is None else _dev(dx, "dx", _BF16_BITS, n)
+    hp = None if h_out is None else _dev(h_out, "h_out", rd, n)
+    yp = None if y is None else _dev(y, "y", _BF16_BITS, n)
+    wpp = None if w_post is None else _dev(w_post, "w_post", _F32, D)
+    gp = None if gate is None else _dev(gate, "gate", _F32, D)
+    wrp = None if w_pre is None else _dev(w_pre, "w_pre", _F32, D)
+    rpp = None if rstd_post is None else _dev(rstd_post, "rstd_post", _F32, M)
+    rrp = None if rstd_pre is None else _dev(rstd_pre, "rstd_pre", _F32, M)
+    dhp = None if dh is None else _dev(dh, "dh", rd, n)
+    dyp = None if dy is None else _dev(dy, "dy", _BF16_BITS, n)
+    dwp = None if dw_post is None else _dev(dw_post, "dw_post", _F32, D)
+    dgp = None if dgate is None else _dev(dgate, "dgate", _F32, D)
+    dwr = None if dw_pre is None else _dev(dw_pre, "dw_pre", _F32, D)
     wsp, wsb = (None, 0) if ws is None else _ws(ws)
     _check("qlora_residual_norm_bwd",
            lib().qlora_residual_norm_bwd(dhop, dxp, hp, yp, wpp, gp, float(scale), wrp, rpp, rrp, M, D, res, dhp, dyp,
@@ -666,7 +668,9 @@ def _rows(t, name: str) -> tuple[int, int, int, int, int]:
         ld = (V + 7) // 8 * 8
     if (V > 1 and t.stride(1) != 1) or ld < V:
         raise ValueError(f"{name}: rows must be contiguous and not overlap")
-    _check_placement(t, name)
+    device = t.get_device()
+    if device < 0 or device != _current_device():
+        _check_placement(t, name)
     return t.data_ptr(), _LOGITS[t.dtype], M, V, ld
 
 
@@ -674,12 +678,12 @@ def qlora_token_logprobs_fwd(logits, targets, inv_temperature: float, logprob, e
                              top_ids, top_logprob, stream=None) -> None:
     """logits [M, V] bf16 or fp32 (rows may be padded), targets int64 [M]; outputs may be None as the header says."""
     lp, dtype, M, V, ld = _rows(logits, "logits")
-    tp = _dev_opt(targets, "targets", (torch.int64,), M)
-    outs = [_dev_opt(t, name, _F32, M) for t, name in ((logprob, "logprob"), (entropy, "entropy"),
-                                                       (row_max, "row_max"), (log_sum, "log_sum"))]
+    tp = None if targets is None else _dev(targets, "targets", (torch.int64,), M)
+    outs = [None if t is None else _dev(t, name, _F32, M)
+            for t, name in ((logprob, "logprob"), (entropy, "entropy"), (row_max, "row_max"), (log_sum, "log_sum"))]
     n = M * k if k > 0 else None
-    ip = _dev_opt(top_ids, "top_ids", (torch.int32,), n)
-    tlp = _dev_opt(top_logprob, "top_logprob", _F32, n)
+    ip = None if top_ids is None else _dev(top_ids, "top_ids", (torch.int32,), n)
+    tlp = None if top_logprob is None else _dev(top_logprob, "top_logprob", _F32, n)
     _check("qlora_token_logprobs_fwd",
            lib().qlora_token_logprobs_fwd(lp, dtype, M, V, ld, tp, float(inv_temperature), *outs, int(k), ip, tlp,
                                           _stream(stream)))
@@ -692,10 +696,10 @@ def qlora_token_logprobs_bwd(logits, targets, inv_temperature: float, row_max, l
     dp, ddtype, dM, dV, ldd = _rows(dlogits, "dlogits")
     if (ddtype, dM, dV) != (dtype, M, V):
         raise ValueError(f"dlogits: {dlogits.dtype} {list(dlogits.shape)}, logits are {logits.dtype} {[M, V]}")
-    tp = _dev_opt(targets, "targets", (torch.int64,), M)
-    ins = [_dev_opt(t, name, _F32, M) for t, name in ((row_max, "row_max"), (log_sum, "log_sum"),
-                                                      (entropy, "entropy"), (g_logprob, "g_logprob"),
-                                                      (g_entropy, "g_entropy"))]
+    tp = None if targets is None else _dev(targets, "targets", (torch.int64,), M)
+    ins = [None if t is None else _dev(t, name, _F32, M)
+           for t, name in ((row_max, "row_max"), (log_sum, "log_sum"), (entropy, "entropy"),
+                           (g_logprob, "g_logprob"), (g_entropy, "g_entropy"))]
     _check("qlora_token_logprobs_bwd",
            lib().qlora_token_logprobs_bwd(lp, dtype, M, V, ld, tp, float(inv_temperature), *ins, dp, ldd,
                                           _stream(stream)))

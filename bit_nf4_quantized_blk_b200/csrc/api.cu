@@ -270,13 +270,19 @@ constexpr size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 qlora_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA; }
 
+// Compute capability 10.0, asked once per device.
 qlora_status check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QLORA_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return QLORA_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return QLORA_ERR_CUDA;
-  return (major == 10 && minor == 0) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
+  static DeviceValue capability;
+  const int cc = capability.get(dev, [dev] {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return -1;
+    if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return -1;
+    return 10 * major + minor;
+  });
+  if (cc < 0) return QLORA_ERR_CUDA;
+  return cc == 100 ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
 }
 
 qlora_status check_weight(const qlora_nf4_weight* w) {
