@@ -453,7 +453,7 @@ cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint
                               : launch_colsum_format<kAct8E4m3>(x, hi, lo, lo2, rt, part, &splits, stream);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols), static_cast<unsigned>(rt));
-  return launch_dependent(act8_colsum_reduce_kernel, grid, 128, stream, part, x.cols, r, splits, scale, dst,
+  return launch_dependent(act8_colsum_reduce_kernel, grid, 128, 0, stream, part, x.cols, r, splits, scale, dst,
                           dst_rc ? 1 : 0);
 }
 
@@ -537,6 +537,7 @@ __global__ void __launch_bounds__(32 * kSkWarps) act8_skinny_kernel(const uint8_
   using S = SkinnyShape<NT>;
   constexpr int kPitch = S::kPitch;
   extern __shared__ __align__(16) uint8_t ring[];
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3, wt = warp % kSkWT, wk = warp / kSkWT;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSkTokens + wt * kSkWarpTokens;

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(const __grid_constant_
   constexpr int kSmallTile = 128 * kR16;
   constexpr int kStage = kInTile + kSmallTile;
   extern __shared__ uint8_t smem_raw[];
+  pdl_launch_dependents();  // the reduction's launch
   uint8_t* smem = align1024(smem_raw);
   PipeBarriers* bars = reinterpret_cast<PipeBarriers*>(smem + kStages * kStage);
   volatile int* abort_flag = &bars->abort_flag;
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(const __grid_constant_
 // out(m, j) = sum_z part[z][m][j] (fixed order); j >= r gives 0.
 // Threads past the M * 32 pairs run out.bs (the GEMM's block scales) when set.
 __global__ void skinny_finalize_kernel(const float* __restrict__ part, int64_t M, int r, int splits, SkinnyOut out) {
+  pdl_wait_prior();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;  // over M * 32 pairs
   if (i >= M * (kRankPad / 2)) {
     const int64_t q = i - M * (kRankPad / 2);
@@ -301,8 +303,8 @@ cudaError_t launch_skinny(const uint16_t* In, int64_t M, int64_t C, const uint16
 cudaError_t launch_skinny_finalize(const float* part, int64_t M, int r, int splits, const SkinnyOut& out,
                                    cudaStream_t stream) {
   const int64_t total = M * (kRankPad / 2) + (out.bs.out != nullptr ? out.bs.groups : 0);
-  skinny_finalize_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(part, M, r, splits, out);
-  return cudaGetLastError();
+  return launch_dependent(skinny_finalize_kernel, dim3(static_cast<unsigned>((total + 255) / 256)), 256, 0, stream, part,
+                          M, r, splits, out);
 }
 
 cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, uint16_t* lo2,
@@ -497,6 +499,7 @@ __global__ void vdb_finalize_kernel(const float* __restrict__ vpart, int ncb, co
                                     int ntb, int64_t M, int64_t N, int r, int r16, float scale,
                                     uint16_t* __restrict__ vs, uint16_t* __restrict__ vhi, uint16_t* __restrict__ vlo,
                                     uint16_t* __restrict__ vlo2, float* __restrict__ dB, BlockScalesJob bs) {
+  pdl_wait_prior();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t nv = M * (kRankPad / 2);
   if (i < nv) {
@@ -542,10 +545,8 @@ cudaError_t launch_vdb_finalize(const float* vpart, int ncb, const float* dbpart
                                 float* dB, const BlockScalesJob& bs, cudaStream_t stream) {
   const int64_t total =
       M * (kRankPad / 2) + (dB != nullptr ? N * r : 0) + (bs.out != nullptr ? bs.groups : 0);
-  vdb_finalize_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(vpart, ncb, dbpart, ntb, M, N,
-                                                                                       r, 16, scale, vs, vhi, vlo, vlo2, dB,
-                                                                                       bs);
-  return cudaGetLastError();
+  return launch_dependent(vdb_finalize_kernel, dim3(static_cast<unsigned>((total + 255) / 256)), 256, 0, stream, vpart,
+                          ncb, dbpart, ntb, M, N, r, 16, scale, vs, vhi, vlo, vlo2, dB, bs);
 }
 
 // ---------------------------------------------------------------------------

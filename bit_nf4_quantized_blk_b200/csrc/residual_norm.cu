@@ -612,7 +612,7 @@ cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cud
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cudaStream_t stream) {
   const cudaError_t e = res_fp32 ? launch_bwd<float>(p, stream) : launch_bwd<uint16_t>(p, stream);
   if (e != cudaSuccess || (!p.dw_pre && !p.dgate && !p.dw_post)) return e;
-  return launch_dependent(residual_norm_finish_kernel, dim3(static_cast<unsigned>(p.D / 32), 2), 1024, stream, p,
+  return launch_dependent(residual_norm_finish_kernel, dim3(static_cast<unsigned>(p.D / 32), 2), 1024, 0, stream, p,
                           residual_norm_bwd_ctas(p.M, p.D));
 }
 

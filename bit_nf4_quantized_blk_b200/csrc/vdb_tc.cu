@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
                   const __grid_constant__ CUtensorMap tmUl2, int64_t M, int64_t N, int ct, int tt,
                   float* __restrict__ vpart, float* __restrict__ dbpart, int* status) {
   constexpr int kStage = kVtStage<kParts>;
+  pdl_launch_dependents();  // the reduction's launch
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   VtBarriers* bars = reinterpret_cast<VtBarriers*>(smem + kVtStages * kStage);
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
+  pdl_wait_prior();  // the transposes (the setup above overlaps them)
 
   if (warp == 0) {
     if (lane == 0) {
@@ -259,6 +261,7 @@ __global__ void rank16_transpose3_kernel(const uint16_t* __restrict__ B, int64_t
                                          const uint16_t* __restrict__ ulo2, const float* __restrict__ u32, int64_t M,
                                          int64_t ldm, int r, uint16_t* __restrict__ bt, uint16_t* __restrict__ uht,
                                          uint16_t* __restrict__ ult, uint16_t* __restrict__ ult2) {
+  pdl_launch_dependents();
   int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const uint16_t* src;
   uint16_t* dst;
@@ -335,9 +338,9 @@ cudaError_t launch_vdb_kernel(const CUtensorMap& tg, const CUtensorMap& tbt, con
     return cudaFuncSetAttribute(vdb_tc_kernel<kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, kVtSmem<kParts>);
   });
   if (e != cudaSuccess) return e;
-  vdb_tc_kernel<kParts><<<dim3(static_cast<unsigned>(g.ncb), static_cast<unsigned>(g.ntb)), kVtThreads,
-                          kVtSmem<kParts>, stream>>>(tg, tbt, tuh, tul, tul2, M, N, g.ct, g.tt, vpart, dbpart, status);
-  return cudaGetLastError();
+  return launch_dependent(vdb_tc_kernel<kParts>, dim3(static_cast<unsigned>(g.ncb), static_cast<unsigned>(g.ntb)),
+                          kVtThreads, kVtSmem<kParts>, stream, tg, tbt, tuh, tul, tul2, M, N, g.ct, g.tt, vpart, dbpart,
+                          status);
 }
 
 }  // namespace
