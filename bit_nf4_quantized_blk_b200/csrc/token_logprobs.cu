@@ -21,9 +21,10 @@
 // shared memory, still one launch without a workspace.
 //
 // The k largest come from the same pass.  The k-th largest (or a little less)
-// of the threads' maxima is a bound that at least k logits reach, and only the
-// vectors of the threads whose maximum reaches it are looked through once more
-// (they are in L2).  Should ties put more logits at the bound than the list
+// of the threads' maxima is a bound that at least k logits reach, and only
+// threads whose maximum reaches it are looked through once more (in L2): the
+// one step that held it, or everything where a second step's maximum reaches
+// the bound as well.  Should ties put more logits at the bound than the list
 // holds, those above the bound are ranked and the rest taken from the row's
 // start, where the lowest ids are; should that many be above it (the largest
 // logits sitting in a few threads), they are taken one by one.
@@ -204,8 +205,9 @@ struct LpShared {
   uint64_t best[kLpWarps];
   uint32_t order[kLpThreads];  // the threads' maxima, as lp_order
   uint32_t bound;
-  int listed[2], cands[2];
-  uint8_t cand[kLpThreads];
+  int listed[2], deep[2], shallow[2];
+  uint8_t cand[kLpThreads];  // deep ones from the front, shallow ones from the back
+  int step[kLpThreads];      // of the shallow ones: the step of the maximum
 };
 
 // The same shared object in CTA `rank` of the cluster.
@@ -253,39 +255,46 @@ __device__ __forceinline__ uint32_t lp_threads_bound(const LpShared& sh, int k, 
   return lp_bound(v, k, slack);
 }
 
-// Lists the threads whose maximum reaches the bound (their number is *cands, zero before).
-__device__ __forceinline__ void lp_candidates(LpShared& sh, uint32_t order, uint32_t bound, int* cands) {
-  const uint32_t in = __ballot_sync(0xffffffffu, order >= bound);
-  if (in == 0) return;
+// Adds this warp's threads with `in` to a list from sh.cand[0] on or, with
+// kBack, from its end back; *count, zero before, becomes their number.
+template <bool kBack>
+__device__ __forceinline__ void lp_candidates(LpShared& sh, bool in, int* count) {
+  const uint32_t all = __ballot_sync(0xffffffffu, in);
+  if (all == 0) return;
   const int lane = threadIdx.x & 31;
   int at = 0;
-  if (lane == 0) at = atomicAdd(cands, __popc(in));
-  at = __shfl_sync(0xffffffffu, at, 0) + __popc(in & ((1u << lane) - 1u));
-  if ((in >> lane) & 1) sh.cand[at] = static_cast<uint8_t>(threadIdx.x);
+  if (lane == 0) at = atomicAdd(count, __popc(all));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1u));
+  if (in) sh.cand[kBack ? kLpThreads - 1 - at : at] = static_cast<uint8_t>(threadIdx.x);
 }
 
-// f(value, id) of the logits that are not below `least` in the vectors of the
-// `cands` listed threads, by the whole CTA; thread c has the vectors
-// seg.first + c, + kLpThreads, ...
+// f(value, id) of a vector's logits that are not below `least`.
+template <typename T, typename F>
+__device__ __forceinline__ void lp_scan_vector(const T* row, int64_t V, const LpSegment& seg, int64_t vec, float least,
+                                               F&& f) {
+  constexpr int P = kLpPer<T>;
+  if (vec >= seg.end) return;
+  float x[P];
+  lp_values<T>(lp_load(row, V, vec), x);
+  bool any = false;
+#pragma unroll
+  for (int j = 0; j < P; ++j) any = any || !(x[j] < least);
+  if (!any) return;
+#pragma unroll
+  for (int j = 0; j < P; ++j)
+    if (!(x[j] < least) && vec * P + j < V) f(x[j], vec * P + j);
+}
+
+// lp_scan_vector of every vector of the `cands` listed threads, by the whole
+// CTA; thread c has the vectors seg.first + c, + kLpThreads, ...
 template <typename T, typename F>
 __device__ __forceinline__ void lp_scan(const LpShared& sh, const T* row, int64_t V, const LpSegment& seg, int cands,
                                         float least, F&& f) {
-  constexpr int P = kLpPer<T>;
   const uint32_t per = static_cast<uint32_t>((seg.end - seg.first + kLpThreads - 1) / kLpThreads), items = cands * per;
 #pragma unroll 1
   for (uint32_t i = threadIdx.x; i < items; i += kLpThreads) {
     const uint32_t c = i / per;
-    const int64_t vec = seg.first + sh.cand[c] + static_cast<int64_t>(i - c * per) * kLpThreads;
-    if (vec >= seg.end) continue;
-    float x[P];
-    lp_values<T>(lp_load(row, V, vec), x);
-    bool any = false;
-#pragma unroll
-    for (int j = 0; j < P; ++j) any = any || !(x[j] < least);
-    if (!any) continue;
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-      if (!(x[j] < least) && vec * P + j < V) f(x[j], vec * P + j);
+    lp_scan_vector(row, V, seg, seg.first + sh.cand[c] + static_cast<int64_t>(i - c * per) * kLpThreads, least, f);
   }
 }
 
@@ -310,14 +319,14 @@ __device__ void lp_select_many(LpShared& sh, const T* row, int64_t V, const LpSe
   __syncthreads();  // everyone has read the count
   if (warp == 0) {
     const uint32_t exact = lp_threads_bound(sh, k, 0);
-    if (lane == 0) sh.bound = exact, sh.listed[turn] = sh.cands[turn] = 0;
+    if (lane == 0) sh.bound = exact, sh.listed[turn] = sh.deep[turn] = 0;
   }
   __syncthreads();
   const uint32_t bound = sh.bound;
   const float least = lp_least(bound);
-  lp_candidates(sh, order, bound, &sh.cands[turn]);
+  lp_candidates<false>(sh, order >= bound, &sh.deep[turn]);
   __syncthreads();
-  const int cands = sh.cands[turn];
+  const int cands = sh.deep[turn];
   lp_scan(sh, row, V, seg, cands, least, [&](float x, int64_t id) {
     if (lp_order(x) <= bound) return;
     const int at = atomicAdd(&sh.listed[turn], 1);
@@ -465,8 +474,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
         q2 = fma2(e, tt, q2);
       }
     };
-    auto raise = [&](float mx) {  // take in a step's maximum
-      if (mx <= a.m || a.m != a.m) return;
+    float second = kNegInf;  // the largest maximum of the steps but best_step
+    int best_step = 0;       // the first step with the thread's maximum
+    auto raise = [&](float mx, int step) {  // take in a step's maximum
+      if (mx <= a.m || a.m != a.m) {
+        if (kTop) second = max_nan(second, mx);
+        return;
+      }
+      if (kTop) second = a.m, best_step = step;
       a.s = s2.x + s2.y, a.q = q2.x + q2.y;
       a.move(mx, c2);
       s2 = F2{a.s, 0.0f}, q2 = F2{a.q, 0.0f};
@@ -480,7 +495,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
         u[i] = *reinterpret_cast<const uint4*>(ring + ((st * kLpVecs + i) * kLpThreads + tid) * 16);
       fetch(st);
       st = st + 1 == kLpStages ? 0 : st + 1;
-      raise(lp_max<T>(u));
+      raise(lp_max<T>(u), step);
       const F2 s0 = s2, q0 = q2;
 #pragma unroll
       for (int i = 0; i < kLpVecs; ++i) add(std::false_type{}, u[i]);
@@ -505,7 +520,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
         float mx = x[0];
 #pragma unroll
         for (int j = 1; j < P; ++j) mx = max_nan(mx, x[j]);
-        raise(mx);
+        raise(mx, full);
         add(std::true_type{}, u);
       }
       fetch(st);
@@ -551,7 +566,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
     } else {
       if (kTop && warp == 1) {  // beside warp 0's joins
         const uint32_t bound = lp_threads_bound(sh, p.k, 2);
-        if (lane == 0) sh.bound = bound, sh.listed[turn] = sh.cands[turn] = 0;
+        if (lane == 0) sh.bound = bound, sh.listed[turn] = sh.deep[turn] = sh.shallow[turn] = 0;
         __syncwarp();
       }
       if constexpr (kCluster) cluster_sync();
@@ -569,13 +584,24 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_fwd_kerne
       };
       __syncthreads();  // sh.bound, sh.row
       const uint32_t bound = sh.bound;
-      lp_candidates(sh, order, bound, &sh.cands[turn]);
+      const float least = lp_least(bound);
+      const bool deep = lp_order(second) >= bound;
+      lp_candidates<false>(sh, order >= bound && deep, &sh.deep[turn]);
+      lp_candidates<true>(sh, order >= bound && !deep, &sh.shallow[turn]);
+      if (order >= bound && !deep) sh.step[tid] = best_step;
       __syncthreads();
-      lp_scan(sh, row, p.V, seg, sh.cands[turn], lp_least(bound), [&](float x, int64_t id) {
+      auto list = [&](float x, int64_t id) {
         if (lp_order(x) < bound) return;
         const int at = atomicAdd(&sh.listed[turn], 1);
         if (at < kLpList) sh.list[at] = lp_key(x, id);  // in any order: the keys are ranked
-      });
+      };
+#pragma unroll 1
+      for (int i = tid; i < sh.shallow[turn] * kLpVecs; i += kLpThreads) {
+        const int c = sh.cand[kLpThreads - 1 - i / kLpVecs];
+        const int64_t v0 = seg.first + static_cast<int64_t>(sh.step[c]) * (kLpThreads * kLpVecs) + c;
+        lp_scan_vector(row, p.V, seg, v0 + i % kLpVecs * kLpThreads, least, list);
+      }
+      lp_scan(sh, row, p.V, seg, sh.deep[turn], least, list);
       __syncthreads();
       const int n = sh.listed[turn];
       if (n <= kLpList)
