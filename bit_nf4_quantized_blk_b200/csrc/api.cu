@@ -1201,7 +1201,7 @@ extern "C" qlora_status qlora_token_logprobs_fwd(const void* logits, int32_t dty
   qlora_status st = check_logits(logits, dtype, M, V, ld);
   if (st != QLORA_OK) return st;
   if (M > INT32_MAX) return QLORA_ERR_UNSUPPORTED;
-  if (!std::isfinite(inv_temperature) || inv_temperature <= 0.0f) return QLORA_ERR_INVALID_ARG;
+  if (!(inv_temperature > 0.0f && inv_temperature <= 0x1p100f)) return QLORA_ERR_INVALID_ARG;
   if ((targets != nullptr) != (logprob != nullptr)) return QLORA_ERR_INVALID_ARG;
   if (k < 0 || k > kLogprobsMaxTop || k > V || (k > 0) != (top_ids != nullptr) || (k > 0) != (top_logprob != nullptr))
     return QLORA_ERR_INVALID_ARG;
@@ -1227,7 +1227,7 @@ extern "C" qlora_status qlora_token_logprobs_bwd(const void* logits, int32_t dty
   st = check_logits(dlogits, dtype, M, V, ldd);
   if (st != QLORA_OK) return st;
   if (dlogits == logits && ldd != ld) return QLORA_ERR_INVALID_ARG;
-  if (!std::isfinite(inv_temperature) || inv_temperature <= 0.0f) return QLORA_ERR_INVALID_ARG;
+  if (!(inv_temperature > 0.0f && inv_temperature <= 0x1p100f)) return QLORA_ERR_INVALID_ARG;
   if (!row_max || !log_sum || (!g_logprob && !g_entropy)) return QLORA_ERR_INVALID_ARG;
   if ((g_logprob != nullptr) != (targets != nullptr) || (g_entropy != nullptr) != (entropy != nullptr))
     return QLORA_ERR_INVALID_ARG;

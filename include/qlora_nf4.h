@@ -511,7 +511,7 @@ qlora_status qlora_residual_norm_bwd(const void *dh_out, const uint16_t *dx, con
  *             Nothing past column V - 1 is read.
  *   targets : int64 [M], NULL exactly when logprob is.  A negative target is not
  *             scored (logprob 0); one of V or more gives NaN.
- *   inv_temperature : finite, > 0.
+ *   inv_temperature : > 0, at most 2^100.
  *   logprob, entropy, row_max (m), log_sum : fp32 [M] outputs, each may be NULL.
  *             Keep row_max, log_sum (and entropy) for the backward.
  *   k       : 0 .. 32, at most V.  top_ids (int32 [M, k]) receives the ids of the

@@ -103,6 +103,15 @@ def test_temperature(it):
     _check_forward(_logits(6, 3001, FP32, 1), _targets(6, 3001, 2), it, 10)
 
 
+@pytest.mark.parametrize("it", [2.0**-100, 2.0**100])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_extreme_temperature(dtype, it):
+    x = _logits(6, 1000, dtype, 31)
+    t = _targets(6, 1000, 32)
+    x[1, 7] = x[1, 500] = 40.0  # two maxima share the row at low temperature
+    _check_forward(x, t, it=it, k=2)
+
+
 def test_large_and_shifted_logits():
     for shift in (-3e4, 2e5):
         x = _logits(4, 1500, FP32, 3)

@@ -25,6 +25,7 @@ def test_forward(lib):
     assert f(x=None) == 1 and f(dtype=2) == 1 and f(M=0) == 1 and f(V=0) == 1 and f(ld=96) == 1
     assert f(V=1 << 31, ld=1 << 31, M=1) == 7 and f(M=1 << 40) == 7 and f(M=1 << 31, V=8, ld=8) == 7
     assert f(it=0.0) == 1 and f(it=-1.0) == 1 and f(it=float("inf")) == 1 and f(it=float("nan")) == 1
+    assert f(it=2.0**100) in ready and f(it=2.0**101) == 1
     assert f(t=None) == 1 and f(lp=None) == 1
     assert f(k=-1) == 1 and f(k=33) == 1 and f(k=5, V=4) == 1 and f(k=0) == 1 and f(ids=None) == 1 and f(lps=None) == 1
     assert f(t=None, lp=None, H=None, m=None, ls=None, k=0, ids=None, lps=None) == 1
