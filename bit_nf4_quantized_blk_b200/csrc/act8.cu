@@ -113,244 +113,275 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 // ---------------------------------------------------------------------------
 // colsum: part[z][j][k] = sum_{m in split z} V[m][j] X^[m][k], V = hi + lo + lo2
 // ---------------------------------------------------------------------------
-// m16n8k16 MMAs with D = [16 j][8 columns], the token axis as K: A = V^T from
-// the [m][64] parts of V by transposed 8x8 loads, B = X^ decoded in registers.
-// A lane's B registers are pairs of tokens (2t, 2t + 1 and 2t + 8, 2t + 9) of
-// one column; which column a slot stands for is free, so lane (g, t) takes kCB
-// consecutive columns of each of its four token rows, at column g kCB of the
-// warp's 8 kCB, and MMA i takes its i-th: the loads are wide and nothing is
-// exchanged between lanes.  The same kernel takes plain bf16 rows (dB, from dY
-// and U), which only skip the decode.
+// One tcgen05 product D[columns k][j] with the token axis as K.  Both operands
+// are MN-major, so rows of tokens go to shared memory as they are: A is the
+// X^ tile, B the three parts of V side by side (N = 192), so that A, whose
+// reads bound the MMA at a small N, is read once for all three.  Their sums
+// stay apart in tensor memory until the epilogue adds them.
 //
-// A CTA is 4 column groups x kWT token groups of warps; each warp runs its own
-// ring of cp.async copies (X: read back by the thread that copied it; V: by
-// the warp), so no CTA barrier sits in the loop.  At the end the token groups'
-// sums are added in shared memory and stored as one partial.
+// A CTA takes 256 columns (two M = 128 tiles) and a range of the tokens, 64 per
+// step.  Warps 0-15 decode: each thread copies its 16 codes of two tokens to
+// its own shared-memory slots four steps ahead (cp.async, read back by the same
+// thread, so without a barrier), and writes them as bf16 in the 128-byte
+// swizzle the descriptors name.  Warp 16 brings the parts of V by TMA (and X
+// itself where it is plain bf16: dB, from dY and U), warp 17 issues the MMAs.
+// At the end warps 0-15 read the accumulators: a lane is a column, so each j
+// leaves as 128 contiguous bytes per warp.  Every barrier wait is bounded.
+//
+// The decoders' instructions bound it (about 1,500 cycles per step, the MMAs
+// take 640), and some 6 us of launch, first loads and epilogue: 15.3 us at
+// 1999 x 8192 and rank 64 (16.8 MB of codes), 7.7 us for dY at 1999 x 2048.
+// Warp-level MMAs from registers, the same sums: 29.9 and 12 us.
 namespace {
 
-constexpr int kCsWC = 4;      // column groups of a CTA
-constexpr int kCsStages = 3;  // ring depth
-constexpr int kCsParts = 3;   // bf16 parts of V
+constexpr int kCsTok = 64;                          // tokens per step
+constexpr int kCsCols = 256;                        // columns of a CTA
+constexpr int kCsStages = 3;                        // operand tiles
+constexpr int kCsSlots = 3;                         // code slots: steps in flight
+constexpr int kCsParts = 3;                         // bf16 parts of V
+constexpr int kCsBox = kCsTok * 128;                // [64 tokens][64 columns or j] bf16
+constexpr int kCsXTile = kCsCols / 64 * kCsBox;
+constexpr int kCsStage = kCsXTile + kCsParts * kCsBox;
+constexpr int kCsDecoders = 512;                    // threads
+constexpr int kCsWarps = kCsDecoders / 32;
+constexpr int kCsThreads = kCsDecoders + 64;
+constexpr int kCsPasses = kCsTok * kCsCols / 16 / kCsDecoders;  // 16 codes per thread and pass
+constexpr int kCsSlot = kCsPasses * kCsDecoders * 16;
+constexpr int kCsN = kCsParts * kRankPad;           // MMA N
+constexpr uint32_t kCsTmemCols = 512;               // two tiles of kCsN, in a power of two
+constexpr int kCsBarriers = 256;
 
-template <int kFormat, int kRT>
-struct ColsumShape {
-  static constexpr bool kDense = kFormat == kAct8Dense;
-  static constexpr int kCB = kRT == 1 && !kDense ? 16 : 8;    // columns per lane and row
-  static constexpr int kWT = kRT == 1 || (kRT == 2 && !kDense) ? 4 : 2;  // token groups of a CTA
-  static constexpr int kCols = 8 * kCB;                       // columns of a warp
-  static constexpr int kWarps = kCsWC * kWT;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kLaneBytes = kCB * (kDense ? 2 : 1);   // of one row
-  static constexpr int kXBytes = 4 * 32 * kLaneBytes;         // one step: 16 tokens
-  static constexpr int kVBytes = 16 * kRT * 16 * 2;           // of one part
-  static constexpr int kStageBytes = kXBytes + kCsParts * kVBytes;
-  static constexpr int kRingBytes = kWarps * kCsStages * kStageBytes;
-  static constexpr int kRedPitch = kCols + 4;                 // floats
-  static constexpr int kRedBytes = kWarps * kRT * 16 * kRedPitch * 4;
-  static constexpr int kSmem = kRingBytes > kRedBytes ? kRingBytes : kRedBytes;
-  static constexpr int kCtaCols = kCsWC * kCols;
-  static constexpr int kCtaTokens = kWT * 16;                 // tokens of a CTA per step
-  static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
+template <int kFormat>
+constexpr int kCsSmem = 1024 + kCsStages * kCsStage + kCsBarriers + (kFormat == kAct8Dense ? 0 : kCsSlots * kCsSlot);
 
-  // Splits of the tokens: one wave of one CTA per SM on a 148-SM B200.
-  static int splits(int64_t M, int64_t C) {
-    const int64_t cols = (C + kCtaCols - 1) / kCtaCols, steps = (M + kCtaTokens - 1) / kCtaTokens;
-    int64_t s = 148 / cols;
-    if (s > steps) s = steps;
-    return static_cast<int>(s < 1 ? 1 : s);
-  }
+struct CsBarriers {
+  uint64_t x_full[kCsStages];  // decoded: one arrival per decoder warp
+  uint64_t full[kCsStages];    // TMA
+  uint64_t empty[kCsStages];
+  uint64_t done, drain;
+  uint32_t tmem;
+  int abort_flag;
 };
 
-// Place of 16-byte chunk `c` of token row `row` in a V tile of 2 kRT chunks per
-// row: permuted so that the eight rows of a transposed 8x8 load fall into
-// different banks (unpermuted, rows of 128 bytes meet in the same four, and
-// those loads bounded the kernel).  Rows of 96 bytes meet two by two as they are.
-template <int kRT>
-__device__ __forceinline__ int v_chunk(int row, int c) {
-  const int key = kRT == 4 ? row & 7 : kRT == 2 ? (row >> 1) & 3 : kRT == 1 ? (row >> 2) & 1 : 0;
-  return row * (2 * kRT) + (c ^ key);
+// Splits of the tokens: one wave of one CTA per SM on a 148-SM B200.
+int cs_splits(int64_t M, int64_t C) {
+  const int64_t cols = (C + kCsCols - 1) / kCsCols, steps = (M + kCsTok - 1) / kCsTok;
+  int64_t s = 148 / cols;
+  if (s > steps) s = steps;
+  return static_cast<int>(s < 1 ? 1 : s);
 }
 
-template <int kBytes>
-__device__ __forceinline__ void cp_async_n(void* dst, const void* src, bool valid) {
-  const int n = valid ? kBytes : 0;
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n), "n"(kBytes)
+__device__ __forceinline__ bool cs_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, status);
+  ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  if (ok) (void)mbar_try_wait(bar, parity);
+  return ok;
+}
+
+// tcgen05.wait::ld that hands the loaded registers on, so no use of them can
+// be scheduled before the wait.
+__device__ __forceinline__ void cs_wait_ld(uint32_t (&r)[kCsParts][16]) {
+#pragma unroll
+  for (int i = 0; i < kCsParts; ++i)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[i][0]), "+r"(r[i][1]), "+r"(r[i][2]), "+r"(r[i][3]), "+r"(r[i][4]), "+r"(r[i][5]),
+                   "+r"(r[i][6]), "+r"(r[i][7]), "+r"(r[i][8]), "+r"(r[i][9]), "+r"(r[i][10]), "+r"(r[i][11]),
+                   "+r"(r[i][12]), "+r"(r[i][13]), "+r"(r[i][14]), "+r"(r[i][15])
+                 :
                  : "memory");
 }
 
 }  // namespace
 
-template <int kFormat, int kRT>
-__global__ void __launch_bounds__(ColsumShape<kFormat, kRT>::kThreads, 1)
-    act8_colsum_kernel(Act8View x, const uint16_t* __restrict__ vhi, const uint16_t* __restrict__ vlo,
-                       const uint16_t* __restrict__ vlo2, int splits, float* __restrict__ part) {
-  using S = ColsumShape<kFormat, kRT>;
-  extern __shared__ __align__(16) uint8_t smem[];
+template <int kFormat>
+__global__ void __launch_bounds__(kCsThreads, 1)
+    act8_colsum_kernel(Act8View x, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmHi,
+                       const __grid_constant__ CUtensorMap tmLo, const __grid_constant__ CUtensorMap tmLo2, int r16,
+                       int splits, float* __restrict__ part, int* status) {
+  constexpr bool kDense = kFormat == kAct8Dense;
+  extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int wc = warp % kCsWC, wt = warp / kCsWC;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  CsBarriers* bars = reinterpret_cast<CsBarriers*>(smem + kCsStages * kCsStage);
+  uint8_t* slots = smem + kCsStages * kCsStage + kCsBarriers;
+  volatile int* abort_flag = &bars->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t M = x.rows, C = x.cols;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * S::kCtaCols + wc * S::kCols;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kCsCols;
   const int z = blockIdx.y;
-  const int64_t total = (M + S::kCtaTokens - 1) / S::kCtaTokens;
-  const int64_t first = total * z / splits;
-  const int n = static_cast<int>(total * (z + 1) / splits - first);
-  const int64_t m0 = (first * S::kWT + wt) * 16;  // the warp's first token; kCtaTokens further per step
-  uint8_t* ring = smem + warp * (kCsStages * S::kStageBytes);
+  const int64_t total = (M + kCsTok - 1) / kCsTok, first = total * z / splits;
+  const int n = static_cast<int>(total * (z + 1) / splits - first);  // steps, at least one
 
-  const int64_t col = c0 + g * S::kCB;  // this lane's columns: in or out of C as a whole
-  const bool col_ok = col < C;
-  const int64_t row_bytes = C * (S::kDense ? 2 : 1), col_bytes = col * (S::kDense ? 2 : 1);
-  // One step per lane: lane l holds that of token l / blocks of the step and
-  // of the warp's block l % blocks (kCols = 128: two blocks; 64: one).
-  constexpr int kBlocks = S::kCols / kBlock;
-  const int64_t kblocks = C / kBlock, blk = c0 / kBlock + (lane & (kBlocks - 1));
-  const int step_token = lane / kBlocks;
-
-  auto issue = [&](int i) {
-    if (i < n) {
-      uint8_t* st = ring + (i % kCsStages) * S::kStageBytes;
-      const int64_t m = m0 + static_cast<int64_t>(i) * S::kCtaTokens;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t row = m + 2 * t + (q & 1) + (q >> 1) * 8;
-        const bool ok = col_ok && row < M;
-        cp_async_n<S::kLaneBytes>(st + (q * 32 + lane) * S::kLaneBytes, x.codes + (ok ? row * row_bytes + col_bytes : 0),
-                                  ok);
-      }
-#pragma unroll
-      for (int q = 0; q < kCsParts * kRT; ++q) {
-        const int chunk = q * 32 + lane;  // of 32 kRT for each part: 2 kRT chunks of 8 j per token
-        const int which = chunk / (32 * kRT), rest = chunk % (32 * kRT);
-        const int tok = rest / (2 * kRT), c = rest % (2 * kRT);
-        const int64_t row = m + tok;
-        const uint16_t* src = which == 0 ? vhi : which == 1 ? vlo : vlo2;
-        cp_async_n<16>(st + S::kXBytes + which * S::kVBytes + v_chunk<kRT>(tok, c) * 16,
-                       src + (row < M ? row * kRankPad + c * 8 : 0), row < M);
-      }
+  if (tid == 0) {
+    for (int s = 0; s < kCsStages; ++s) {
+      mbar_init(&bars->x_full[s], kCsWarps);
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
     }
-    cp_async_commit();
-  };
-  auto load_step = [&](int i) -> uint32_t {
-    if constexpr (S::kDense) return 0u;
-    const int64_t row = m0 + static_cast<int64_t>(i) * S::kCtaTokens + step_token;
-    const bool ok = i < n && step_token < 16 && row < M && blk < kblocks;
-    return ok ? x.step[row * kblocks + blk] : 0u;
-  };
+    mbar_init(&bars->done, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kCsWarps + 1) {
+    tmem_alloc(&bars->tmem, kCsTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
 
-  float acc[kRT][S::kCB][4];
-#pragma unroll
-  for (int a = 0; a < kRT; ++a)
-#pragma unroll
-    for (int b = 0; b < S::kCB; ++b)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.0f;
-
-#pragma unroll
-  for (int i = 0; i < kCsStages - 1; ++i) issue(i);
-  uint32_t next_step = load_step(0);
-
-  const int mat = lane >> 3, rr = lane & 7;
-  for (int i = 0; i < n; ++i) {
-    const uint32_t my_step = next_step;
-    next_step = load_step(i + 1);
-    cp_async_wait<kCsStages - 2>();
-    __syncwarp();
-    issue(i + kCsStages - 1);  // into the stage read in the previous iteration
-    const uint8_t* st = ring + (i % kCsStages) * S::kStageBytes;
-    // Packed steps of the token pairs (2t, 2t + 1) and (2t + 8, 2t + 9), block of column g kCB.
-    uint32_t s2[2] = {0u, 0u};
-    if constexpr (!S::kDense) {
-      const int b = g * S::kCB / kBlock;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = 2 * t + 8 * h;
-        const uint32_t lo = __shfl_sync(0xffffffffu, my_step, tok * kBlocks + b);
-        const uint32_t hi = __shfl_sync(0xffffffffu, my_step, (tok + 1) * kBlocks + b);
-        s2[h] = lo | (hi << 16);
+  if (warp == kCsWarps) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int i = 0; i < n; ++i) {
+        const int s = i % kCsStages, u = i / kCsStages;
+        if (i >= kCsStages && !mbar_wait(&bars->empty[s], (u - 1) & 1, abort_flag, status)) break;
+        uint8_t* st = smem + s * kCsStage;
+        const int m = static_cast<int>((first + i) * kCsTok);
+        mbar_arrive_expect_tx(&bars->full[s], kDense ? kCsStage : kCsParts * kCsBox);
+        if constexpr (kDense)
+          for (int g = 0; g < kCsCols / 64; ++g)
+            tma_load_2d(st + g * kCsBox, &tmX, &bars->full[s], static_cast<int>(c0) + g * 64, m);
+        tma_load_2d(st + kCsXTile, &tmHi, &bars->full[s], 0, m);
+        tma_load_2d(st + kCsXTile + kCsBox, &tmLo, &bars->full[s], 0, m);
+        tma_load_2d(st + kCsXTile + 2 * kCsBox, &tmLo2, &bars->full[s], 0, m);
+        issued = i + 1;
       }
+      // Every copy into shared memory has landed before the CTA can exit.
+      for (int i = (issued > kCsStages ? issued - kCsStages : 0); i < issued; ++i)
+        mbar_wait_teardown(&bars->full[i % kCsStages], (i / kCsStages) & 1, status);
     }
-    // The lane's columns of its four rows (wide reads: by words they would conflict).
-    uint32_t xr[4][S::kLaneBytes / 4];
+  } else if (warp == kCsWarps + 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, kCsN, true) | (1u << 15);  // A and B MN-major
+      // Groups of 64 columns (or of 64 j: one part) are a box apart, groups of
+      // 8 tokens 1 KB; a K = 16 step is 16 tokens = 2 KB.
+      const uint64_t a0 = smem_desc_mn128(smem_u32(smem), kCsBox, 1024);
+      bool ok = true;
+      for (int u = 0; ok && u * kCsStages < n; ++u)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint8_t* src = st + (q * 32 + lane) * S::kLaneBytes;
-      if constexpr (S::kLaneBytes == 16) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src);
-        xr[q][0] = v.x, xr[q][1] = v.y, xr[q][2] = v.z, xr[q][3] = v.w;
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(src);
-        xr[q][0] = v.x, xr[q][1] = v.y;
-      }
-    }
-    // Four columns at a time: their B registers, then the parts of V one after
-    // the other, so that an accumulator is used again 4 kRT MMAs later.
+        for (int s = 0; s < kCsStages; ++s) {
+          const int i = u * kCsStages + s;
+          if (!ok || i >= n) break;
+          ok = mbar_wait(&bars->full[s], u & 1, abort_flag, status) &&
+               (kDense || mbar_wait(&bars->x_full[s], u & 1, abort_flag, status));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-    for (int w = 0; w < S::kCB / 4; ++w) {
-      uint32_t bf[4][2];
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (S::kDense) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            bf[2 * e][h] = __byte_perm(xr[2 * h][2 * w + e], xr[2 * h + 1][2 * w + e], 0x5410);
-            bf[2 * e + 1][h] = __byte_perm(xr[2 * h][2 * w + e], xr[2 * h + 1][2 * w + e], 0x7632);
-          }
-        } else {
-          // Byte pairs (row 2t, row 2t + 1) of the word's four columns.
-          const uint32_t p0 = __byte_perm(xr[2 * h][w], xr[2 * h + 1][w], 0x5140);
-          const uint32_t p1 = __byte_perm(xr[2 * h][w], xr[2 * h + 1][w], 0x7362);
-          bf[0][h] = act8_decode2<kFormat, 0>(p0, s2[h]);
-          bf[1][h] = act8_decode2<kFormat, 2>(p0, s2[h]);
-          bf[2][h] = act8_decode2<kFormat, 0>(p1, s2[h]);
-          bf[3][h] = act8_decode2<kFormat, 2>(p1, s2[h]);
+            for (int kk = 0; kk < kCsTok / 16; ++kk)
+              tc_mma_bf16_ss(tmem + static_cast<uint32_t>(h * 256), a0 + ((s * kCsStage + h * 2 * kCsBox + kk * 2048) >> 4),
+                             a0 + ((s * kCsStage + kCsXTile + kk * 2048) >> 4), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(&bars->empty[s]);
         }
-      }
+      if (ok) tc_commit(&bars->done);
+      tc_commit(&bars->drain);
+      mbar_wait_teardown(&bars->drain, 0, status);
+    }
+  } else {
+    bool ok = true;
+    if constexpr (!kDense) {
+      constexpr int kPassTok = kCsTok / kCsPasses;
+      const int seg = tid % 16, tok0 = tid / 16;  // 16 columns of token tok0 + kPassTok pass
+      const int64_t col = c0 + seg * 16;          // in or out of C as a whole
+      // Rows left from this thread's first one; none if its columns are not there.
+      const int64_t m0 = first * kCsTok + tok0;
+      const int rows = col < C ? static_cast<int>(min(M - m0, static_cast<int64_t>(n) * kCsTok)) : 0;
+      const uint8_t* const codes = x.codes + (rows > 0 ? m0 * C + col : 0);
+      const uint16_t* const steps = x.step + (rows > 0 ? (m0 * C + col) / kBlock : 0);
+      uint8_t* const slot = slots + tid * 16;
+      auto fetch = [&](int i, int sl) {
+        const uint8_t* src = codes + static_cast<int64_t>(i) * (kCsTok * C);
 #pragma unroll
-      for (int v = 0; v < kCsParts; ++v)
-#pragma unroll
-        for (int a = 0; a < kRT; ++a) {
-          // Stored rows are tokens: matrices (tokens 0-7, j lo), (0-7, j hi), (8-15, j lo), (8-15, j hi).
-          uint32_t af[4];
-          ldmatrix_x4_trans(af, smem_u32(st + S::kXBytes + v * S::kVBytes) +
-                                    v_chunk<kRT>((mat >> 1) * 8 + rr, a * 2 + (mat & 1)) * 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mma_16816(acc[a][4 * w + e], af, bf[e]);
+        for (int q = 0; q < kCsPasses; ++q) {
+          const bool in = i * kCsTok + q * kPassTok < rows;
+          cp_async_16(slot + sl * kCsSlot + q * (kCsDecoders * 16), in ? src + q * (kPassTok * C) : codes, in);
         }
+        cp_async_commit();
+      };
+      auto load_steps = [&](int i, uint32_t (&s)[kCsPasses]) {
+        const uint16_t* src = steps + static_cast<int64_t>(i) * (kCsTok * C / kBlock);
+#pragma unroll
+        for (int q = 0; q < kCsPasses; ++q)
+          s[q] = i * kCsTok + q * kPassTok < rows ? __ldg(src + q * (kPassTok * C / kBlock)) : 0u;
+      };
+      // Odd groups of 64 columns take their second eight first, so that the
+      // groups of a store meet no bank twice.
+      const int group = seg / 4, odd = group & 1, chunk = (seg & 3) * 2, key = tok0 & 7;
+      static_assert(kPassTok % 8 == 0, "one swizzle key for all passes");
+      const int out0 = group * kCsBox + tok0 * 128 + (((chunk + odd) ^ key) << 4);
+      const int out1 = group * kCsBox + tok0 * 128 + (((chunk + 1 - odd) ^ key) << 4);
+      // Step i = kCsStages u + st, whose scales are in s; they are replaced by
+      // those of step i + kCsStages in place (a copy from a set still loading
+      // would wait for it).
+      static_assert(kCsStages == kCsSlots, "one index for tiles and slots");
+      auto decode = [&](int u, int st, uint32_t (&s)[kCsPasses]) {
+        const int i = u * kCsStages + st;
+        if (i >= n) return true;
+        cp_async_wait<kCsSlots - 1>();
+        uint2 c[kCsPasses][2];
+#pragma unroll
+        for (int q = 0; q < kCsPasses; ++q) {
+          const uint8_t* src = slot + st * kCsSlot + q * (kCsDecoders * 16);
+          c[q][0] = *reinterpret_cast<const uint2*>(src + odd * 8);
+          c[q][1] = *reinterpret_cast<const uint2*>(src + 8 - odd * 8);
+        }
+        if (u > 0 && !cs_warp_wait(&bars->empty[st], (u - 1) & 1, abort_flag, status)) return false;
+        uint8_t* dst = smem + st * kCsStage;
+#pragma unroll
+        for (int q = 0; q < kCsPasses; ++q) {
+          const uint32_t s2 = s[q] | (s[q] << 16);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<uint4*>(dst + (e == 0 ? out0 : out1) + q * (kPassTok * 128)) =
+                make_uint4(act8_decode2<kFormat, 0>(c[q][e].x, s2), act8_decode2<kFormat, 2>(c[q][e].x, s2),
+                           act8_decode2<kFormat, 0>(c[q][e].y, s2), act8_decode2<kFormat, 2>(c[q][e].y, s2));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the MMA reads them
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->x_full[st]);
+        fetch(i + kCsSlots, st);  // into the slot read above
+        load_steps(i + kCsSlots, s);
+        return true;
+      };
+      uint32_t scale[kCsSlots][kCsPasses];
+#pragma unroll
+      for (int i = 0; i < kCsSlots; ++i) {
+        fetch(i, i);
+        load_steps(i, scale[i]);
+      }
+      for (int u = 0; ok && u * kCsStages < n; ++u)
+#pragma unroll
+        for (int st = 0; st < kCsStages; ++st) ok = ok && decode(u, st, scale[st]);
+      cp_async_wait<0>();
+    }
+    if (ok && cs_warp_wait(&bars->done, 0, abort_flag, status)) {
+      tc_fence_after();
+      const int quad = warp & 3, h = (warp >> 2) & 1;  // TMEM lanes 32 quad .. + 31 of column tile h
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(h * 256);
+      const int64_t k = c0 + h * 128 + quad * 32 + lane;
+      for (int j0 = warp / 8 * 16; j0 < r16; j0 += kCsWarps / 8 * 16) {
+        uint32_t v[kCsParts][16];
+#pragma unroll
+        for (int i = 0; i < kCsParts; ++i) tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(i * kRankPad + j0), v[i]);
+        cs_wait_ld(v);
+        if (k >= C) continue;
+        float* dst = part + (static_cast<int64_t>(z) * r16 + j0) * C + k;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          dst[j * C] = __uint_as_float(v[0][j]) + (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+      }
     }
   }
-  cp_async_wait<0>();
-  __syncthreads();  // every ring is free: its space takes the warps' sums
-
-  float* red = reinterpret_cast<float*>(smem);
-  float* mine = red + warp * (kRT * 16 * S::kRedPitch);
-#pragma unroll
-  for (int a = 0; a < kRT; ++a)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float* dst = mine + (a * 16 + g + (c >> 1) * 8) * S::kRedPitch + (2 * t + (c & 1)) * S::kCB;
-#pragma unroll
-      for (int b = 0; b < S::kCB; b += 4)
-        *reinterpret_cast<float4*>(dst + b) =
-            make_float4(acc[a][b][c], acc[a][b + 1][c], acc[a][b + 2][c], acc[a][b + 3][c]);
-    }
+  tc_fence_before();
   __syncthreads();
-  constexpr int kOut = kRT * 16 * S::kCtaCols / 4;  // in fours
-  for (int o = threadIdx.x; o < kOut; o += S::kThreads) {
-    const int j = o / (S::kCtaCols / 4), c = o % (S::kCtaCols / 4) * 4;
-    const float* src = red + (c / S::kCols) * (kRT * 16 * S::kRedPitch) + j * S::kRedPitch + c % S::kCols;
-    float4 s = *reinterpret_cast<const float4*>(src);
-#pragma unroll
-    for (int q = 1; q < S::kWT; ++q) {
-      const float4 o4 = *reinterpret_cast<const float4*>(src + q * (kCsWC * kRT * 16 * S::kRedPitch));
-      s.x += o4.x, s.y += o4.y, s.z += o4.z, s.w += o4.w;
-    }
-    const int64_t k = static_cast<int64_t>(blockIdx.x) * S::kCtaCols + c;
-    if (k < C) *reinterpret_cast<float4*>(part + (static_cast<int64_t>(z) * (kRT * 16) + j) * C + k) = s;
+  if (warp == kCsWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCsTmemCols);
   }
 }
 
@@ -396,61 +427,43 @@ __global__ void __launch_bounds__(128) act8_colsum_reduce_kernel(const float* __
 namespace {
 
 template <int kFormat>
-int64_t colsum_partial_rows(int64_t M, int64_t C) {
-  const int64_t rows[4] = {16 * int64_t{ColsumShape<kFormat, 1>::splits(M, C)},
-                           32 * int64_t{ColsumShape<kFormat, 2>::splits(M, C)},
-                           48 * int64_t{ColsumShape<kFormat, 3>::splits(M, C)},
-                           64 * int64_t{ColsumShape<kFormat, 4>::splits(M, C)}};
-  int64_t most = 0;
-  for (const int64_t v : rows) most = v > most ? v : most;
-  return most;
-}
-
-template <int kFormat, int kRT>
-cudaError_t launch_colsum_rt(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2,
-                             float* part, int* splits, cudaStream_t stream) {
-  using S = ColsumShape<kFormat, kRT>;
+cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4], int r16, int splits, float* part,
+                                 int* status, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static DeviceOnce configured;
   e = configured.run(dev, [] {
-    return cudaFuncSetAttribute(act8_colsum_kernel<kFormat, kRT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                S::kSmem);
+    return cudaFuncSetAttribute(act8_colsum_kernel<kFormat>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kCsSmem<kFormat>);
   });
   if (e != cudaSuccess) return e;
-  *splits = S::splits(x.rows, x.cols);
-  const dim3 grid(static_cast<unsigned>((x.cols + S::kCtaCols - 1) / S::kCtaCols), static_cast<unsigned>(*splits));
-  act8_colsum_kernel<kFormat, kRT><<<grid, S::kThreads, S::kSmem, stream>>>(x, hi, lo, lo2, *splits, part);
+  const dim3 grid(static_cast<unsigned>((x.cols + kCsCols - 1) / kCsCols), static_cast<unsigned>(splits));
+  act8_colsum_kernel<kFormat><<<grid, kCsThreads, kCsSmem<kFormat>, stream>>>(x, maps[0], maps[1], maps[2], maps[3], r16,
+                                                                             splits, part, status);
   return cudaGetLastError();
-}
-
-template <int kFormat>
-cudaError_t launch_colsum_format(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2,
-                                 int rt, float* part, int* splits, cudaStream_t stream) {
-  switch (rt) {
-    case 1: return launch_colsum_rt<kFormat, 1>(x, hi, lo, lo2, part, splits, stream);
-    case 2: return launch_colsum_rt<kFormat, 2>(x, hi, lo, lo2, part, splits, stream);
-    case 3: return launch_colsum_rt<kFormat, 3>(x, hi, lo, lo2, part, splits, stream);
-    default: return launch_colsum_rt<kFormat, 4>(x, hi, lo, lo2, part, splits, stream);
-  }
 }
 
 }  // namespace
 
 size_t act8_colsum_partial_bytes(int64_t M, int64_t C) {
-  const int64_t codes = colsum_partial_rows<kAct8Int8>(M, C), dense = colsum_partial_rows<kAct8Dense>(M, C);
-  return static_cast<size_t>(codes > dense ? codes : dense) * static_cast<size_t>(C) * sizeof(float);
+  return static_cast<size_t>(cs_splits(M, C)) * kRankPad * static_cast<size_t>(C) * sizeof(float);
 }
 
 cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2, int r,
-                               float scale, float* part, float* dst, bool dst_rc, cudaStream_t stream) {
-  const int rt = (r + 15) / 16;
-  int splits = 0;
+                               float scale, float* part, float* dst, bool dst_rc, int* status, cudaStream_t stream) {
+  const bool dense = x.format == kAct8Dense;
+  const uint16_t* parts[kCsParts] = {hi, lo, lo2};
+  CUtensorMap maps[4];  // X (plain bf16 only; else any valid map) and the parts of V
+  for (int i = 0; i < kCsParts; ++i)
+    if (!encode_tensor_map_2d(&maps[1 + i], parts[i], x.rows, kRankPad, kCsTok, 64)) return cudaErrorInvalidValue;
+  maps[0] = maps[1];
+  if (dense && !encode_tensor_map_2d(&maps[0], x.codes, x.rows, x.cols, kCsTok, 64)) return cudaErrorInvalidValue;
+  const int rt = (r + 15) / 16, splits = cs_splits(x.rows, x.cols);
   const cudaError_t e =
-      x.format == kAct8Dense  ? launch_colsum_format<kAct8Dense>(x, hi, lo, lo2, rt, part, &splits, stream)
-      : x.format == kAct8Int8 ? launch_colsum_format<kAct8Int8>(x, hi, lo, lo2, rt, part, &splits, stream)
-                              : launch_colsum_format<kAct8E4m3>(x, hi, lo, lo2, rt, part, &splits, stream);
+      dense                   ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, part, status, stream)
+      : x.format == kAct8Int8 ? launch_colsum_format<kAct8Int8>(x, maps, 16 * rt, splits, part, status, stream)
+                              : launch_colsum_format<kAct8E4m3>(x, maps, 16 * rt, splits, part, status, stream);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols), static_cast<unsigned>(rt));
   return launch_dependent(act8_colsum_reduce_kernel, grid, 128, 0, stream, part, x.cols, r, splits, scale, dst,

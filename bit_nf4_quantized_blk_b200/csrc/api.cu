@@ -973,7 +973,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
       Timed tm(kFamSide, s, 2);
       if (x8 != nullptr)
         e = launch_act8_colsum(dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, r,
-                               scale, at<float>(ws, lay.part), dB, false, s);
+                               scale, at<float>(ws, lay.part), dB, false, status, s);
       else
         e = launch_colsum(dY, M, N, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), r, scale,
                           at<float>(ws, lay.part), dB, false, status, s);
@@ -1019,7 +1019,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
       Timed tm(kFamSide, s, 2);
       if (x8 != nullptr)
         e = launch_act8_colsum(view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, r, scale,
-                               at<float>(ws, lay.part), dA, true, s);
+                               at<float>(ws, lay.part), dA, true, status, s);
       else
         e = launch_colsum(X, M, K, at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
                           at<float>(ws, lay.part), dA, true, status, s);

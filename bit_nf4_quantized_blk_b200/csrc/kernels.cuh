@@ -280,7 +280,7 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 // act8_colsum_partial_bytes(rows, cols), enough for every rank and format.
 size_t act8_colsum_partial_bytes(int64_t M, int64_t C);
 cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2, int r,
-                               float scale, float* part, float* dst, bool dst_rc, cudaStream_t stream);
+                               float scale, float* part, float* dst, bool dst_rc, int* status, cudaStream_t stream);
 // launch_skinny's product X^ A^T from a checkpoint (A [r][K] bf16, 16-byte
 // aligned rows); `part` as for launch_skinny.
 cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, const SkinnyOut& out,
