@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         for (int st = 0; st < kCsStages; ++st) ok = ok && decode(u, st, scale[st]);
       cp_async_wait<0>();
     }
+    pdl_wait_prior();  // an overlapped launch ends after the kernel before it
     if (ok && cs_warp_wait(&bars->done, 0, abort_flag, status)) {
       tc_fence_after();
       const int quad = warp & 3, h = (warp >> 2) & 1;  // TMEM lanes 32 quad .. + 31 of column tile h
@@ -388,14 +389,28 @@ __global__ void __launch_bounds__(kCsThreads, 1)
 // dst(j, k) = scale sum_z part[z][j][k]; part has r16 = 16 ceil(r / 16) rows
 // per split.  A CTA takes 32 columns of 16 j: four columns of one j per
 // thread.  [cols][r] outputs leave through shared memory, 16 j side by side.
+// The CTAs of a second job follow the first's.
 constexpr int kCrCols = 32;
 
-__global__ void __launch_bounds__(128) act8_colsum_reduce_kernel(const float* __restrict__ part, int64_t C, int r,
-                                                                 int splits, float scale, float* __restrict__ dst,
-                                                                 int dst_rc) {
+struct ColsumReduceJob {
+  const float* part;
+  int64_t C;
+  int splits;
+  float* dst;
+  int dst_rc;
+};
+
+__global__ void __launch_bounds__(128)
+    act8_colsum_reduce_kernel(const __grid_constant__ ColsumReduceJob job0, const __grid_constant__ ColsumReduceJob job1,
+                              unsigned first, int r, float scale) {
   __shared__ float tile[kCrCols][17];
   pdl_wait_prior();
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kCrCols;
+  const ColsumReduceJob& job = blockIdx.x < first ? job0 : job1;
+  const float* __restrict__ part = job.part;
+  float* __restrict__ dst = job.dst;
+  const int64_t C = job.C;
+  const int splits = job.splits, dst_rc = job.dst_rc;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x < first ? blockIdx.x : blockIdx.x - first) * kCrCols;
   const int jj = threadIdx.x / (kCrCols / 4), cc = threadIdx.x % (kCrCols / 4) * 4, j = blockIdx.y * 16 + jj;
   const int64_t slice = static_cast<int64_t>(gridDim.y) * 16 * C;
   if (j < r && c0 + cc < C) {
@@ -428,7 +443,7 @@ namespace {
 
 template <int kFormat>
 cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4], int r16, int splits, float* part,
-                                 int* status, cudaStream_t stream) {
+                                 bool overlap, int* status, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -439,6 +454,9 @@ cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4]
   });
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.cols + kCsCols - 1) / kCsCols), static_cast<unsigned>(splits));
+  if (overlap)
+    return launch_dependent(act8_colsum_kernel<kFormat>, grid, kCsThreads, kCsSmem<kFormat>, stream, x, maps[0], maps[1],
+                            maps[2], maps[3], r16, splits, part, status);
   act8_colsum_kernel<kFormat><<<grid, kCsThreads, kCsSmem<kFormat>, stream>>>(x, maps[0], maps[1], maps[2], maps[3], r16,
                                                                              splits, part, status);
   return cudaGetLastError();
@@ -450,24 +468,34 @@ size_t act8_colsum_partial_bytes(int64_t M, int64_t C) {
   return static_cast<size_t>(cs_splits(M, C)) * kRankPad * static_cast<size_t>(C) * sizeof(float);
 }
 
-cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2, int r,
-                               float scale, float* part, float* dst, bool dst_rc, int* status, cudaStream_t stream) {
-  const bool dense = x.format == kAct8Dense;
-  const uint16_t* parts[kCsParts] = {hi, lo, lo2};
-  CUtensorMap maps[4];  // X (plain bf16 only; else any valid map) and the parts of V
-  for (int i = 0; i < kCsParts; ++i)
-    if (!encode_tensor_map_2d(&maps[1 + i], parts[i], x.rows, kRankPad, kCsTok, 64)) return cudaErrorInvalidValue;
-  maps[0] = maps[1];
-  if (dense && !encode_tensor_map_2d(&maps[0], x.codes, x.rows, x.cols, kCsTok, 64)) return cudaErrorInvalidValue;
-  const int rt = (r + 15) / 16, splits = cs_splits(x.rows, x.cols);
-  const cudaError_t e =
-      dense                   ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, part, status, stream)
-      : x.format == kAct8Int8 ? launch_colsum_format<kAct8Int8>(x, maps, 16 * rt, splits, part, status, stream)
-                              : launch_colsum_format<kAct8E4m3>(x, maps, 16 * rt, splits, part, status, stream);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols), static_cast<unsigned>(rt));
-  return launch_dependent(act8_colsum_reduce_kernel, grid, 128, 0, stream, part, x.cols, r, splits, scale, dst,
-                          dst_rc ? 1 : 0);
+cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, int* status,
+                                cudaStream_t stream) {
+  const int rt = (r + 15) / 16;
+  ColsumReduceJob reduce[2];
+  unsigned blocks[2] = {0, 0};
+  for (int i = 0; i < count; ++i) {
+    const ColsumJob& job = jobs[i];
+    const Act8View& x = job.x;
+    const bool dense = x.format == kAct8Dense, overlap = i > 0;
+    const uint16_t* parts[kCsParts] = {job.hi, job.lo, job.lo2};
+    CUtensorMap maps[4];  // X (plain bf16 only; else any valid map) and the parts of V
+    for (int q = 0; q < kCsParts; ++q)
+      if (!encode_tensor_map_2d(&maps[1 + q], parts[q], x.rows, kRankPad, kCsTok, 64)) return cudaErrorInvalidValue;
+    maps[0] = maps[1];
+    if (dense && !encode_tensor_map_2d(&maps[0], x.codes, x.rows, x.cols, kCsTok, 64)) return cudaErrorInvalidValue;
+    const int splits = cs_splits(x.rows, x.cols);
+    const cudaError_t e =
+        dense ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, job.part, overlap, status, stream)
+        : x.format == kAct8Int8
+            ? launch_colsum_format<kAct8Int8>(x, maps, 16 * rt, splits, job.part, overlap, status, stream)
+            : launch_colsum_format<kAct8E4m3>(x, maps, 16 * rt, splits, job.part, overlap, status, stream);
+    if (e != cudaSuccess) return e;
+    reduce[i] = ColsumReduceJob{job.part, x.cols, splits, job.dst, job.dst_rc ? 1 : 0};
+    blocks[i] = static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols);
+  }
+  const dim3 grid(blocks[0] + blocks[1], static_cast<unsigned>(rt));
+  return launch_dependent(act8_colsum_reduce_kernel, grid, 128, 0, stream, reduce[0], reduce[count - 1], blocks[0], r,
+                          scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -681,13 +709,11 @@ cudaError_t launch_skinny_format(const Act8View& x, const uint16_t* A, int r, in
 
 }  // namespace
 
-cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, const SkinnyOut& out,
+cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, int* splits,
                                cudaStream_t stream) {
-  const int splits = act8_skinny_splits(x.rows, x.cols);
-  const cudaError_t e = x.format == kAct8Int8 ? launch_skinny_format<kAct8Int8>(x, A, r, splits, part, stream)
-                                              : launch_skinny_format<kAct8E4m3>(x, A, r, splits, part, stream);
-  if (e != cudaSuccess) return e;
-  return launch_skinny_finalize(part, x.rows, r, splits, out, stream);
+  *splits = act8_skinny_splits(x.rows, x.cols);
+  return x.format == kAct8Int8 ? launch_skinny_format<kAct8Int8>(x, A, r, *splits, part, stream)
+                               : launch_skinny_format<kAct8E4m3>(x, A, r, *splits, part, stream);
 }
 
 }  // namespace qnf4

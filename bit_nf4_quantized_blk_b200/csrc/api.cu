@@ -351,7 +351,7 @@ int64_t max_group_chunks(const qlora_nf4_weight* outs, int32_t count) {
 
 // Linear workspace layout.
 struct LinearWs {
-  size_t wbf, scales, us, uhi, ulo, ulo2, vs, vhi, vlo, vlo2, bpad, part, skpart, vdbpart, bt, uht, ult, ult2, gu, gy, total;
+  size_t wbf, scales, us, uhi, ulo, ulo2, vs, vhi, vlo, vlo2, bpad, part, dbpart, skpart, vdbpart, bt, uht, ult, ult2, gu, gy, total;
 };
 
 LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
@@ -378,8 +378,10 @@ LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
   l.vlo2 = take(mr * 2);
   l.bpad = take(static_cast<size_t>(N) * kRankPad * 2);
   const size_t p1 = colsum_partial_bytes(M, N), p2 = colsum_partial_bytes(M, K);
-  l.part = take(std::max({p1, p2, act8_colsum_partial_bytes(M, K), act8_colsum_partial_bytes(M, N)}));
   const size_t s1 = skinny_partial_bytes(M, N), s2 = skinny_partial_bytes(M, K);
+  // From a checkpoint, U's partials and later dA's share `part`, while V's and dB's have their own.
+  l.part = take(std::max({p1, p2, s2, act8_colsum_partial_bytes(M, K)}));
+  l.dbpart = take(act8_colsum_partial_bytes(M, N));
   l.skpart = take(s1 > s2 ? s1 : s2);
   // The tensor-core V / dB pass: its partials and the transposed B and U split.
   const bool vdb = M > kGemvMaxM;
@@ -921,21 +923,34 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   // parts, against the 10^-3 that the checkpoint itself costs at most).
   uint16_t* const ulo2 = x8 != nullptr ? at<uint16_t>(ws, lay.ulo2) : nullptr;
   uint16_t* const vlo2 = x8 != nullptr ? at<uint16_t>(ws, lay.vlo2) : nullptr;
+  SkinnyOut uo{};
+  uo.ohi = at<uint16_t>(ws, lay.uhi);
+  uo.olo = at<uint16_t>(ws, lay.ulo);
+  uo.olo2 = ulo2;
+  uo.scale = 1.0f;
   // U = X A^T in its bf16 parts (from the saved fp32 U, or recomputed).
   auto u_hilo = [&]() -> cudaError_t {
     if (U != nullptr) {
       Timed tm(kFamSide, s);
       return launch_split_hilo(U, M, r, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, s);
     }
-    SkinnyOut uo{};
-    uo.ohi = at<uint16_t>(ws, lay.uhi);
-    uo.olo = at<uint16_t>(ws, lay.ulo);
-    uo.olo2 = ulo2;
-    uo.scale = 1.0f;
     Timed tm(kFamSide, s, 2);
-    if (x8 != nullptr) return launch_act8_skinny(view_of(x8), A, r, at<float>(ws, lay.skpart), uo, s);
+    if (x8 != nullptr) {
+      SkinnyJob job{at<float>(ws, lay.part), 0, uo};
+      const cudaError_t err = launch_act8_skinny(view_of(x8), A, r, at<float>(ws, lay.part), &job.splits, s);
+      return err != cudaSuccess ? err : launch_skinny_finalize(&job, 1, M, r, s);
+    }
     return launch_skinny(X, M, K, A, true, r, 0, at<float>(ws, lay.skpart), uo, status, s);
   };
+  // The column sums from a checkpoint.
+  ColsumJob da_job{}, db_job{};
+  if (x8 != nullptr) {
+    da_job = ColsumJob{view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, at<float>(ws, lay.part),
+                       dA, true};
+    db_job = ColsumJob{dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2,
+                       at<float>(ws, lay.dbpart), dB, false};
+  }
+  bool da_done = false;
   BlockScalesJob bs{};  // the dX GEMM's block scales, when a kernel before it carries them
   if (dB != nullptr && r <= kVdbMaxRank && M > kGemvMaxM) {
     // V = dY B (s*V for the dX rank step, hi/lo for dA) and dB = s dY^T U in one pass over dY.
@@ -962,21 +977,33 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     vo.olo = at<uint16_t>(ws, lay.vlo);
     vo.olo2 = vlo2;
     vo.scale = scale;
-    {
-      Timed tm(kFamSide, s, 2);
-      e = launch_skinny(dY, M, N, Bk, false, r, ldbk, at<float>(ws, lay.skpart), vo, status, s);
+    if (x8 != nullptr && dB != nullptr && U == nullptr) {
+      // U too: V's product runs beside U's, and one reduction ends both.
+      Timed tm(kFamSide, s, 3);
+      SkinnyJob jobs[2] = {{at<float>(ws, lay.part), 0, uo}, {at<float>(ws, lay.skpart), 0, vo}};
+      e = launch_act8_skinny(view_of(x8), A, r, at<float>(ws, lay.part), &jobs[0].splits, s);
+      if (e == cudaSuccess)
+        e = launch_skinny_partials(dY, M, N, Bk, false, r, ldbk, at<float>(ws, lay.skpart), &jobs[1].splits, true, status,
+                                   s);
+      if (e == cudaSuccess) e = launch_skinny_finalize(jobs, 2, M, r, s);
+    } else {
+      {
+        Timed tm(kFamSide, s, 2);
+        e = launch_skinny(dY, M, N, Bk, false, r, ldbk, at<float>(ws, lay.skpart), vo, status, s);
+      }
+      if (e == cudaSuccess && dB != nullptr) e = u_hilo();
     }
     if (e != cudaSuccess) return from_cuda(e);
-    if (dB != nullptr) {  // dB = s dY^T U
-      e = u_hilo();
+    if (dB != nullptr && x8 != nullptr) {  // dB = s dY^T U, with dA beside it
+      const ColsumJob jobs[2] = {db_job, da_job};
+      da_done = dA != nullptr;
+      Timed tm(kFamSide, s, da_done ? 3 : 2);
+      e = launch_act8_colsums(jobs, da_done ? 2 : 1, r, scale, status, s);
       if (e != cudaSuccess) return from_cuda(e);
+    } else if (dB != nullptr) {  // dB = s dY^T U
       Timed tm(kFamSide, s, 2);
-      if (x8 != nullptr)
-        e = launch_act8_colsum(dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, r,
-                               scale, at<float>(ws, lay.part), dB, false, status, s);
-      else
-        e = launch_colsum(dY, M, N, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), r, scale,
-                          at<float>(ws, lay.part), dB, false, status, s);
+      e = launch_colsum(dY, M, N, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), r, scale,
+                        at<float>(ws, lay.part), dB, false, status, s);
       if (e != cudaSuccess) return from_cuda(e);
     }
   }
@@ -1014,12 +1041,11 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     }
     if (e != cudaSuccess) return from_cuda(e);
   }
-  if (dA != nullptr) {  // dA = s V^T X
+  if (dA != nullptr && !da_done) {  // dA = s V^T X
     {
       Timed tm(kFamSide, s, 2);
       if (x8 != nullptr)
-        e = launch_act8_colsum(view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, r, scale,
-                               at<float>(ws, lay.part), dA, true, status, s);
+        e = launch_act8_colsums(&da_job, 1, r, scale, status, s);
       else
         e = launch_colsum(X, M, K, at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
                           at<float>(ws, lay.part), dA, true, status, s);

@@ -206,8 +206,19 @@ int skinny_splits(int64_t M, int64_t C);
 size_t skinny_partial_bytes(int64_t M, int64_t C);
 cudaError_t launch_skinny(const uint16_t* In, int64_t M, int64_t C, const uint16_t* Wt, bool wt_is_rc, int r,
                           int64_t ldw, float* part, const SkinnyOut& out, int* status, cudaStream_t stream);
-// The reduction of launch_skinny's split partials alone ([splits][M][64] in `part`).
-cudaError_t launch_skinny_finalize(const float* part, int64_t M, int r, int splits, const SkinnyOut& out,
+// The reduction of split partials ([splits][M][64] in `part`) alone, of one or
+// two products at once.
+struct SkinnyJob {
+  const float* part;
+  int splits;
+  SkinnyOut out;
+};
+cudaError_t launch_skinny_finalize(const SkinnyJob* jobs, int count, int64_t M, int r, cudaStream_t stream);
+// launch_skinny's product alone, its reduction left to launch_skinny_finalize.
+// `overlap`: may run beside the previous kernel of the stream, which writes
+// nothing that this one reads (it ends after that kernel in any case).
+cudaError_t launch_skinny_partials(const uint16_t* In, int64_t M, int64_t C, const uint16_t* Wt, bool wt_is_rc, int r,
+                                   int64_t ldw, float* part, int* splits, bool overlap, int* status,
                                    cudaStream_t stream);
 // hi/lo (and, unless null, lo2) bf16 split of a compact fp32 [M][r] matrix into [M][64] buffers.
 cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, uint16_t* lo2,
@@ -278,12 +289,21 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 // (a checkpoint, or bf16 values with 16-byte aligned rows), written to dst as
 // [r][cols] (dst_rc) or [cols][r].  `part` is scratch of
 // act8_colsum_partial_bytes(rows, cols), enough for every rank and format.
+// One or two jobs: the second product starts where the first leaves room, and
+// one reduction ends both.
+struct ColsumJob {
+  Act8View x;
+  const uint16_t *hi, *lo, *lo2;
+  float* part;
+  float* dst;
+  bool dst_rc;
+};
 size_t act8_colsum_partial_bytes(int64_t M, int64_t C);
-cudaError_t launch_act8_colsum(const Act8View& x, const uint16_t* hi, const uint16_t* lo, const uint16_t* lo2, int r,
-                               float scale, float* part, float* dst, bool dst_rc, int* status, cudaStream_t stream);
-// launch_skinny's product X^ A^T from a checkpoint (A [r][K] bf16, 16-byte
-// aligned rows); `part` as for launch_skinny.
-cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, const SkinnyOut& out,
+cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, int* status,
+                                cudaStream_t stream);
+// launch_skinny_partials' product X^ A^T from a checkpoint (A [r][K] bf16,
+// 16-byte aligned rows); `part` as for launch_skinny.
+cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, int* splits,
                                cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
