@@ -15,8 +15,8 @@
 //  act8_colsum_kernel      part[z][j][k] = sum over the tokens m of split z of
 //                          V[m][j] X^[m][k], then act8_colsum_reduce_kernel
 //                          adds the splits in a fixed order (dA).
-//  act8_skinny_kernel      part[z][m][j] = sum over the columns of split z of
-//                          X^[m][k] A[j][k] (U).
+//  act8_rowsum_kernel      part[z][m][j] = sum over the columns of split z of
+//                          X^[m][k] A[j][k] (U), or of dY[m][k] B[k][j] (V).
 // Deterministic: every sum runs in a fixed order; no atomics.
 #include "act8.cuh"
 #include "kernels.cuh"
@@ -111,67 +111,73 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 }
 
 // ---------------------------------------------------------------------------
-// colsum: part[z][j][k] = sum_{m in split z} V[m][j] X^[m][k], V = hi + lo + lo2
+// Decoded tiles for the tensor cores
 // ---------------------------------------------------------------------------
-// One tcgen05 product D[columns k][j] with the token axis as K.  Both operands
-// are MN-major, so rows of tokens go to shared memory as they are: A is the
-// X^ tile, B the three parts of V side by side (N = 192), so that A, whose
-// reads bound the MMA at a small N, is read once for all three.  Their sums
-// stay apart in tensor memory until the epilogue adds them.
-//
-// A CTA takes 256 columns (two M = 128 tiles) and a range of the tokens, 64 per
-// step.  Warps 0-15 decode: each thread copies its 16 codes of two tokens to
-// its own shared-memory slots four steps ahead (cp.async, read back by the same
-// thread, so without a barrier), and writes them as bf16 in the 128-byte
-// swizzle the descriptors name.  Warp 16 brings the parts of V by TMA (and X
-// itself where it is plain bf16: dB, from dY and U), warp 17 issues the MMAs.
-// At the end warps 0-15 read the accumulators: a lane is a column, so each j
-// leaves as 128 contiguous bytes per warp.  Every barrier wait is bounded.
-//
-// The decoders' instructions bound it (about 1,500 cycles per step, the MMAs
-// take 640), and some 6 us of launch, first loads and epilogue: 15.3 us at
-// 1999 x 8192 and rank 64 (16.8 MB of codes), 7.7 us for dY at 1999 x 2048.
-// Warp-level MMAs from registers, the same sums: 29.9 and 12 us.
+// Both products below are tcgen05 MMAs whose A operand is X^.  Warps 0-15
+// decode: per step each thread takes two runs of 16 codes, which it copies to
+// its own shared-memory slots three steps ahead (cp.async; read back by the
+// same thread, so without a barrier), and writes them as bf16 in the 128-byte
+// swizzle that the descriptors name.  Warp 16 brings the other operand by TMA
+// (and X itself where it is plain bf16), warp 17 issues the MMAs.  At the end
+// warps 0-15 read the accumulators.  Every barrier wait is bounded.
 namespace {
 
-constexpr int kCsTok = 64;                          // tokens per step
-constexpr int kCsCols = 256;                        // columns of a CTA
-constexpr int kCsStages = 3;                        // operand tiles
-constexpr int kCsSlots = 3;                         // code slots: steps in flight
-constexpr int kCsParts = 3;                         // bf16 parts of V
-constexpr int kCsBox = kCsTok * 128;                // [64 tokens][64 columns or j] bf16
-constexpr int kCsXTile = kCsCols / 64 * kCsBox;
-constexpr int kCsStage = kCsXTile + kCsParts * kCsBox;
-constexpr int kCsDecoders = 512;                    // threads
-constexpr int kCsWarps = kCsDecoders / 32;
-constexpr int kCsThreads = kCsDecoders + 64;
-constexpr int kCsPasses = kCsTok * kCsCols / 16 / kCsDecoders;  // 16 codes per thread and pass
-constexpr int kCsSlot = kCsPasses * kCsDecoders * 16;
-constexpr int kCsN = kCsParts * kRankPad;           // MMA N
-constexpr uint32_t kCsTmemCols = 512;               // two tiles of kCsN, in a power of two
-constexpr int kCsBarriers = 256;
+constexpr int kTcDecoders = 512;  // threads
+constexpr int kTcWarps = kTcDecoders / 32;
+constexpr int kTcThreads = kTcDecoders + 64;
+constexpr int kTcStages = 3;      // tiles, and code slots, in flight
+constexpr int kTcPasses = 2;      // runs of 16 codes per thread and step
+constexpr int kTcSlot = kTcPasses * kTcDecoders * 16;
+constexpr int kTcBarriers = 256;
 
-template <int kFormat>
-constexpr int kCsSmem = 1024 + kCsStages * kCsStage + kCsBarriers + (kFormat == kAct8Dense ? 0 : kCsSlots * kCsSlot);
-
-struct CsBarriers {
-  uint64_t x_full[kCsStages];  // decoded: one arrival per decoder warp
-  uint64_t full[kCsStages];    // TMA
-  uint64_t empty[kCsStages];
+struct TcBarriers {
+  uint64_t x_full[kTcStages];  // decoded: one arrival per decoder warp
+  uint64_t full[kTcStages];    // TMA
+  uint64_t empty[kTcStages];
   uint64_t done, drain;
   uint32_t tmem;
   int abort_flag;
 };
+static_assert(sizeof(TcBarriers) <= kTcBarriers, "room for the barriers");
 
-// Splits of the tokens: one wave of one CTA per SM on a 148-SM B200.
-int cs_splits(int64_t M, int64_t C) {
-  const int64_t cols = (C + kCsCols - 1) / kCsCols, steps = (M + kCsTok - 1) / kCsTok;
-  int64_t s = 148 / cols;
-  if (s > steps) s = steps;
-  return static_cast<int>(s < 1 ? 1 : s);
+template <int kFormat>
+constexpr int tc_smem(int stage) {
+  return 1024 + kTcStages * stage + kTcBarriers + (kFormat == kAct8Dense ? 0 : kTcStages * kTcSlot);
 }
 
-__device__ __forceinline__ bool cs_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+// The barriers and the accumulators' `columns` of tensor memory; by the CTA.
+__device__ __forceinline__ uint32_t tc_setup(TcBarriers* bars, uint32_t columns) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTcStages; ++s) {
+      mbar_init(&bars->x_full[s], kTcWarps);
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->done, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x >> 5 == kTcWarps + 1) {
+    tmem_alloc(&bars->tmem, columns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return bars->tmem;
+}
+
+__device__ __forceinline__ void tc_teardown(uint32_t tmem, uint32_t columns) {
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x >> 5 == kTcWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, columns);
+  }
+}
+
+__device__ __forceinline__ bool tc_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, status);
   ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -181,21 +187,172 @@ __device__ __forceinline__ bool cs_warp_wait(uint64_t* bar, uint32_t parity, vol
 
 // tcgen05.wait::ld that hands the loaded registers on, so no use of them can
 // be scheduled before the wait.
-__device__ __forceinline__ void cs_wait_ld(uint32_t (&r)[kCsParts][16]) {
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Warp 16's thread: `load(stage, bar, i)` issues the copies of step i, of
+// `bytes` in all, for each of the n steps.
+template <typename Load>
+__device__ __forceinline__ void tc_produce(uint8_t* smem, int stage_bytes, TcBarriers* bars, int n, uint32_t bytes,
+                                           int* status, Load&& load) {
+  int issued = 0;
+  for (int i = 0; i < n; ++i) {
+    const int s = i % kTcStages, u = i / kTcStages;
+    if (i >= kTcStages && !mbar_wait(&bars->empty[s], (u - 1) & 1, &bars->abort_flag, status)) break;
+    mbar_arrive_expect_tx(&bars->full[s], bytes);
+    load(smem + s * stage_bytes, &bars->full[s], i);
+    issued = i + 1;
+  }
+  // Every copy into shared memory has landed before the CTA can exit.
+  for (int i = (issued > kTcStages ? issued - kTcStages : 0); i < issued; ++i)
+    mbar_wait_teardown(&bars->full[i % kTcStages], (i / kTcStages) & 1, status);
+}
+
+// Warp 17's thread: `mma(stage, i)` issues the MMAs of step i.
+template <bool kDense, typename Mma>
+__device__ __forceinline__ void tc_issue(TcBarriers* bars, int n, int* status, Mma&& mma) {
+  bool ok = true;
+  for (int u = 0; ok && u * kTcStages < n; ++u)
 #pragma unroll
-  for (int i = 0; i < kCsParts; ++i)
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[i][0]), "+r"(r[i][1]), "+r"(r[i][2]), "+r"(r[i][3]), "+r"(r[i][4]), "+r"(r[i][5]),
-                   "+r"(r[i][6]), "+r"(r[i][7]), "+r"(r[i][8]), "+r"(r[i][9]), "+r"(r[i][10]), "+r"(r[i][11]),
-                   "+r"(r[i][12]), "+r"(r[i][13]), "+r"(r[i][14]), "+r"(r[i][15])
-                 :
-                 : "memory");
+    for (int s = 0; s < kTcStages; ++s) {
+      const int i = u * kTcStages + s;
+      if (!ok || i >= n) break;
+      ok = mbar_wait(&bars->full[s], u & 1, &bars->abort_flag, status) &&
+           (kDense || mbar_wait(&bars->x_full[s], u & 1, &bars->abort_flag, status));
+      if (!ok) break;
+      tc_fence_after();
+      mma(s, i);
+      tc_commit(&bars->empty[s]);
+    }
+  if (ok) tc_commit(&bars->done);
+  tc_commit(&bars->drain);
+  mbar_wait_teardown(&bars->drain, 0, status);
+}
+
+// The decoders: n tiles of kRows rows x 16 kSegs columns, the first one's
+// corner at (row0, col0) and `advance` elements from one to the next, as
+// [box of 64 columns][row][64 bf16] at the start of each stage.  in(i, row,
+// col): whether a run of 16 at (row, col) of tile i exists; others are zero.
+template <int kFormat, int kSegs, int kRows, int kStage, typename In>
+__device__ __forceinline__ bool tc_decode(const Act8View& x, int64_t row0, int64_t col0, int64_t advance, int n,
+                                          uint8_t* smem, uint8_t* slots, TcBarriers* bars, int* status, In&& in) {
+  constexpr int kPassRows = kTcDecoders / kSegs;
+  static_assert(kPassRows * kTcPasses == kRows && kPassRows % 8 == 0, "whole passes, one swizzle key for all of them");
+  const int seg = threadIdx.x % kSegs, tok = threadIdx.x / kSegs;
+  const int64_t C = x.cols, at = (row0 + tok) * C + col0 + seg * 16;
+  uint8_t* const slot = slots + threadIdx.x * 16;
+  auto fetch = [&](int i, int sl) {
+    const uint8_t* src = x.codes + at + i * advance;
+#pragma unroll
+    for (int q = 0; q < kTcPasses; ++q) {
+      const bool ok = i < n && in(i, tok + q * kPassRows, seg * 16);
+      cp_async_16(slot + sl * kTcSlot + q * (kTcDecoders * 16), ok ? src + q * (kPassRows * C) : x.codes, ok);
+    }
+    cp_async_commit();
+  };
+  auto load_steps = [&](int i, uint32_t (&s)[kTcPasses]) {
+    const uint16_t* src = x.step + (at + i * advance) / kBlock;
+#pragma unroll
+    for (int q = 0; q < kTcPasses; ++q)
+      s[q] = i < n && in(i, tok + q * kPassRows, seg * 16) ? __ldg(src + q * (kPassRows * C / kBlock)) : 0u;
+  };
+  // Odd boxes take their second eight columns first, so that the boxes of a
+  // store meet no bank twice.
+  const int box = seg / 4, odd = box & 1, chunk = (seg & 3) * 2, key = tok & 7;
+  const int out0 = box * (kRows * 128) + tok * 128 + (((chunk + odd) ^ key) << 4);
+  const int out1 = box * (kRows * 128) + tok * 128 + (((chunk + 1 - odd) ^ key) << 4);
+  // Tile i = kTcStages u + st, whose scales are in s; they are replaced by
+  // those of tile i + kTcStages in place (a copy from a set still loading would
+  // wait for it).
+  auto decode = [&](int u, int st, uint32_t (&s)[kTcPasses]) {
+    const int i = u * kTcStages + st;
+    if (i >= n) return true;
+    cp_async_wait<kTcStages - 1>();
+    uint2 c[kTcPasses][2];
+#pragma unroll
+    for (int q = 0; q < kTcPasses; ++q) {
+      const uint8_t* src = slot + st * kTcSlot + q * (kTcDecoders * 16);
+      c[q][0] = *reinterpret_cast<const uint2*>(src + odd * 8);
+      c[q][1] = *reinterpret_cast<const uint2*>(src + 8 - odd * 8);
+    }
+    if (u > 0 && !tc_warp_wait(&bars->empty[st], (u - 1) & 1, &bars->abort_flag, status)) return false;
+    uint8_t* dst = smem + st * kStage;
+#pragma unroll
+    for (int q = 0; q < kTcPasses; ++q) {
+      const uint32_t s2 = s[q] | (s[q] << 16);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<uint4*>(dst + (e == 0 ? out0 : out1) + q * (kPassRows * 128)) =
+            make_uint4(act8_decode2<kFormat, 0>(c[q][e].x, s2), act8_decode2<kFormat, 2>(c[q][e].x, s2),
+                       act8_decode2<kFormat, 0>(c[q][e].y, s2), act8_decode2<kFormat, 2>(c[q][e].y, s2));
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the MMA reads them
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->x_full[st]);
+    fetch(i + kTcStages, st);  // into the slot read above
+    load_steps(i + kTcStages, s);
+    return true;
+  };
+  uint32_t scale[kTcStages][kTcPasses];
+#pragma unroll
+  for (int i = 0; i < kTcStages; ++i) {
+    fetch(i, i);
+    load_steps(i, scale[i]);
+  }
+  bool ok = true;
+  for (int u = 0; ok && u * kTcStages < n; ++u)
+#pragma unroll
+    for (int st = 0; st < kTcStages; ++st) ok = ok && decode(u, st, scale[st]);
+  cp_async_wait<0>();
+  return ok;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// colsum: part[z][j][k] = sum_{m in split z} V[m][j] X^[m][k], V = hi + lo + lo2
+// ---------------------------------------------------------------------------
+// D[columns k][j] with the token axis as K.  Both operands are MN-major, so
+// rows of tokens go to shared memory as they are: A is the X^ tile, B the three
+// parts of V side by side (N = 192), so that A, whose reads bound the MMA at a
+// small N, is read once for all three.  Their sums stay apart in tensor memory
+// until the epilogue adds them.  A CTA takes 256 columns (two M = 128 tiles)
+// and a range of the tokens, 64 per step; it takes dY and U for dB the same
+// way.  In the epilogue a lane is a column, so each j leaves as 128 contiguous
+// bytes per warp.
+//
+// The decoders' instructions bound it (about 1,500 cycles per step, the MMAs
+// take 640), and some 6 us of launch, first loads and epilogue: 14.8 us at
+// 1999 x 8192 and rank 64 (16.8 MB of codes), 7.4 us for dY at 1999 x 2048.
+// Warp-level MMAs from registers, the same sums: 29.9 and 12 us.
+namespace {
+
+constexpr int kCsTok = 64;                          // tokens per step
+constexpr int kCsCols = 256;                        // columns of a CTA
+constexpr int kCsParts = 3;                         // bf16 parts of V
+constexpr int kCsBox = kCsTok * 128;                // [64 tokens][64 columns or j] bf16
+constexpr int kCsXTile = kCsCols / 64 * kCsBox;
+constexpr int kCsStage = kCsXTile + kCsParts * kCsBox;
+constexpr int kCsN = kCsParts * kRankPad;           // MMA N
+constexpr uint32_t kCsTmemCols = 512;               // two tiles of kCsN, in a power of two
+
+// Splits of the tokens: one wave of one CTA per SM on a 148-SM B200.
+int cs_splits(int64_t M, int64_t C) {
+  const int64_t cols = (C + kCsCols - 1) / kCsCols, steps = (M + kCsTok - 1) / kCsTok;
+  int64_t s = 148 / cols;
+  if (s > steps) s = steps;
+  return static_cast<int>(s < 1 ? 1 : s);
 }
 
 }  // namespace
 
 template <int kFormat>
-__global__ void __launch_bounds__(kCsThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
     act8_colsum_kernel(Act8View x, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmHi,
                        const __grid_constant__ CUtensorMap tmLo, const __grid_constant__ CUtensorMap tmLo2, int r16,
                        int splits, float* __restrict__ part, int* status) {
@@ -203,173 +360,64 @@ __global__ void __launch_bounds__(kCsThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  CsBarriers* bars = reinterpret_cast<CsBarriers*>(smem + kCsStages * kCsStage);
-  uint8_t* slots = smem + kCsStages * kCsStage + kCsBarriers;
-  volatile int* abort_flag = &bars->abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  TcBarriers* bars = reinterpret_cast<TcBarriers*>(smem + kTcStages * kCsStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t M = x.rows, C = x.cols;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kCsCols;
   const int z = blockIdx.y;
   const int64_t total = (M + kCsTok - 1) / kCsTok, first = total * z / splits;
   const int n = static_cast<int>(total * (z + 1) / splits - first);  // steps, at least one
+  const uint32_t tmem = tc_setup(bars, kCsTmemCols);
 
-  if (tid == 0) {
-    for (int s = 0; s < kCsStages; ++s) {
-      mbar_init(&bars->x_full[s], kCsWarps);
-      mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], 1);
-    }
-    mbar_init(&bars->done, 1);
-    mbar_init(&bars->drain, 1);
-    bars->abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == kCsWarps + 1) {
-    tmem_alloc(&bars->tmem, kCsTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars->tmem;
-
-  if (warp == kCsWarps) {
-    if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int s = i % kCsStages, u = i / kCsStages;
-        if (i >= kCsStages && !mbar_wait(&bars->empty[s], (u - 1) & 1, abort_flag, status)) break;
-        uint8_t* st = smem + s * kCsStage;
-        const int m = static_cast<int>((first + i) * kCsTok);
-        mbar_arrive_expect_tx(&bars->full[s], kDense ? kCsStage : kCsParts * kCsBox);
-        if constexpr (kDense)
-          for (int g = 0; g < kCsCols / 64; ++g)
-            tma_load_2d(st + g * kCsBox, &tmX, &bars->full[s], static_cast<int>(c0) + g * 64, m);
-        tma_load_2d(st + kCsXTile, &tmHi, &bars->full[s], 0, m);
-        tma_load_2d(st + kCsXTile + kCsBox, &tmLo, &bars->full[s], 0, m);
-        tma_load_2d(st + kCsXTile + 2 * kCsBox, &tmLo2, &bars->full[s], 0, m);
-        issued = i + 1;
-      }
-      // Every copy into shared memory has landed before the CTA can exit.
-      for (int i = (issued > kCsStages ? issued - kCsStages : 0); i < issued; ++i)
-        mbar_wait_teardown(&bars->full[i % kCsStages], (i / kCsStages) & 1, status);
-    }
-  } else if (warp == kCsWarps + 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, kCsN, true) | (1u << 15);  // A and B MN-major
-      // Groups of 64 columns (or of 64 j: one part) are a box apart, groups of
-      // 8 tokens 1 KB; a K = 16 step is 16 tokens = 2 KB.
-      const uint64_t a0 = smem_desc_mn128(smem_u32(smem), kCsBox, 1024);
-      bool ok = true;
-      for (int u = 0; ok && u * kCsStages < n; ++u)
+  if (warp == kTcWarps) {
+    if (lane == 0)
+      tc_produce(smem, kCsStage, bars, n, kDense ? kCsStage : kCsParts * kCsBox, status,
+                 [&](uint8_t* st, uint64_t* bar, int i) {
+                   const int m = static_cast<int>((first + i) * kCsTok);
+                   if constexpr (kDense)
+                     for (int g = 0; g < kCsCols / 64; ++g)
+                       tma_load_2d(st + g * kCsBox, &tmX, bar, static_cast<int>(c0) + g * 64, m);
+                   tma_load_2d(st + kCsXTile, &tmHi, bar, 0, m);
+                   tma_load_2d(st + kCsXTile + kCsBox, &tmLo, bar, 0, m);
+                   tma_load_2d(st + kCsXTile + 2 * kCsBox, &tmLo2, bar, 0, m);
+                 });
+  } else if (warp == kTcWarps + 1) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kCsN, true) | (1u << 15);  // A and B MN-major
+    // Groups of 64 columns (or of 64 j: one part) are a box apart, groups of
+    // 8 tokens 1 KB; a K = 16 step is 16 tokens = 2 KB.
+    const uint64_t base = smem_desc_mn128(smem_u32(smem), kCsBox, 1024);
+    if (lane == 0)
+      tc_issue<kDense>(bars, n, status, [&](int s, int i) {
 #pragma unroll
-        for (int s = 0; s < kCsStages; ++s) {
-          const int i = u * kCsStages + s;
-          if (!ok || i >= n) break;
-          ok = mbar_wait(&bars->full[s], u & 1, abort_flag, status) &&
-               (kDense || mbar_wait(&bars->x_full[s], u & 1, abort_flag, status));
-          if (!ok) break;
-          tc_fence_after();
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int kk = 0; kk < kCsTok / 16; ++kk)
-              tc_mma_bf16_ss(tmem + static_cast<uint32_t>(h * 256), a0 + ((s * kCsStage + h * 2 * kCsBox + kk * 2048) >> 4),
-                             a0 + ((s * kCsStage + kCsXTile + kk * 2048) >> 4), idesc, (i > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(&bars->empty[s]);
-        }
-      if (ok) tc_commit(&bars->done);
-      tc_commit(&bars->drain);
-      mbar_wait_teardown(&bars->drain, 0, status);
-    }
+          for (int kk = 0; kk < kCsTok / 16; ++kk)
+            tc_mma_bf16_ss(tmem + static_cast<uint32_t>(h * 256),
+                           base + static_cast<uint64_t>((s * kCsStage + h * 2 * kCsBox + kk * 2048) >> 4),
+                           base + static_cast<uint64_t>((s * kCsStage + kCsXTile + kk * 2048) >> 4), idesc,
+                           (i > 0 || kk > 0) ? 1u : 0u);
+      });
   } else {
     bool ok = true;
     if constexpr (!kDense) {
-      constexpr int kPassTok = kCsTok / kCsPasses;
-      const int seg = tid % 16, tok0 = tid / 16;  // 16 columns of token tok0 + kPassTok pass
-      const int64_t col = c0 + seg * 16;          // in or out of C as a whole
-      // Rows left from this thread's first one; none if its columns are not there.
-      const int64_t m0 = first * kCsTok + tok0;
-      const int rows = col < C ? static_cast<int>(min(M - m0, static_cast<int64_t>(n) * kCsTok)) : 0;
-      const uint8_t* const codes = x.codes + (rows > 0 ? m0 * C + col : 0);
-      const uint16_t* const steps = x.step + (rows > 0 ? (m0 * C + col) / kBlock : 0);
-      uint8_t* const slot = slots + tid * 16;
-      auto fetch = [&](int i, int sl) {
-        const uint8_t* src = codes + static_cast<int64_t>(i) * (kCsTok * C);
-#pragma unroll
-        for (int q = 0; q < kCsPasses; ++q) {
-          const bool in = i * kCsTok + q * kPassTok < rows;
-          cp_async_16(slot + sl * kCsSlot + q * (kCsDecoders * 16), in ? src + q * (kPassTok * C) : codes, in);
-        }
-        cp_async_commit();
-      };
-      auto load_steps = [&](int i, uint32_t (&s)[kCsPasses]) {
-        const uint16_t* src = steps + static_cast<int64_t>(i) * (kCsTok * C / kBlock);
-#pragma unroll
-        for (int q = 0; q < kCsPasses; ++q)
-          s[q] = i * kCsTok + q * kPassTok < rows ? __ldg(src + q * (kPassTok * C / kBlock)) : 0u;
-      };
-      // Odd groups of 64 columns take their second eight first, so that the
-      // groups of a store meet no bank twice.
-      const int group = seg / 4, odd = group & 1, chunk = (seg & 3) * 2, key = tok0 & 7;
-      static_assert(kPassTok % 8 == 0, "one swizzle key for all passes");
-      const int out0 = group * kCsBox + tok0 * 128 + (((chunk + odd) ^ key) << 4);
-      const int out1 = group * kCsBox + tok0 * 128 + (((chunk + 1 - odd) ^ key) << 4);
-      // Step i = kCsStages u + st, whose scales are in s; they are replaced by
-      // those of step i + kCsStages in place (a copy from a set still loading
-      // would wait for it).
-      static_assert(kCsStages == kCsSlots, "one index for tiles and slots");
-      auto decode = [&](int u, int st, uint32_t (&s)[kCsPasses]) {
-        const int i = u * kCsStages + st;
-        if (i >= n) return true;
-        cp_async_wait<kCsSlots - 1>();
-        uint2 c[kCsPasses][2];
-#pragma unroll
-        for (int q = 0; q < kCsPasses; ++q) {
-          const uint8_t* src = slot + st * kCsSlot + q * (kCsDecoders * 16);
-          c[q][0] = *reinterpret_cast<const uint2*>(src + odd * 8);
-          c[q][1] = *reinterpret_cast<const uint2*>(src + 8 - odd * 8);
-        }
-        if (u > 0 && !cs_warp_wait(&bars->empty[st], (u - 1) & 1, abort_flag, status)) return false;
-        uint8_t* dst = smem + st * kCsStage;
-#pragma unroll
-        for (int q = 0; q < kCsPasses; ++q) {
-          const uint32_t s2 = s[q] | (s[q] << 16);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<uint4*>(dst + (e == 0 ? out0 : out1) + q * (kPassTok * 128)) =
-                make_uint4(act8_decode2<kFormat, 0>(c[q][e].x, s2), act8_decode2<kFormat, 2>(c[q][e].x, s2),
-                           act8_decode2<kFormat, 0>(c[q][e].y, s2), act8_decode2<kFormat, 2>(c[q][e].y, s2));
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the MMA reads them
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->x_full[st]);
-        fetch(i + kCsSlots, st);  // into the slot read above
-        load_steps(i + kCsSlots, s);
-        return true;
-      };
-      uint32_t scale[kCsSlots][kCsPasses];
-#pragma unroll
-      for (int i = 0; i < kCsSlots; ++i) {
-        fetch(i, i);
-        load_steps(i, scale[i]);
-      }
-      for (int u = 0; ok && u * kCsStages < n; ++u)
-#pragma unroll
-        for (int st = 0; st < kCsStages; ++st) ok = ok && decode(u, st, scale[st]);
-      cp_async_wait<0>();
+      const int rows = static_cast<int>(min(M - first * kCsTok, static_cast<int64_t>(n) * kCsTok));
+      const int cols = static_cast<int>(min(C - c0, static_cast<int64_t>(kCsCols)));
+      ok = tc_decode<kFormat, kCsCols / 16, kCsTok, kCsStage>(
+          x, first * kCsTok, c0, kCsTok * C, n, smem, smem + kTcStages * kCsStage + kTcBarriers, bars, status,
+          [&](int i, int row, int col) { return i * kCsTok + row < rows && col < cols; });
     }
     pdl_wait_prior();  // an overlapped launch ends after the kernel before it
-    if (ok && cs_warp_wait(&bars->done, 0, abort_flag, status)) {
+    if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status)) {
       tc_fence_after();
       const int quad = warp & 3, h = (warp >> 2) & 1;  // TMEM lanes 32 quad .. + 31 of column tile h
       const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(h * 256);
       const int64_t k = c0 + h * 128 + quad * 32 + lane;
-      for (int j0 = warp / 8 * 16; j0 < r16; j0 += kCsWarps / 8 * 16) {
+      for (int j0 = warp / 8 * 16; j0 < r16; j0 += kTcWarps / 8 * 16) {
         uint32_t v[kCsParts][16];
 #pragma unroll
         for (int i = 0; i < kCsParts; ++i) tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(i * kRankPad + j0), v[i]);
-        cs_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < kCsParts; ++i) tc_wait_ld(v[i]);
         if (k >= C) continue;
         float* dst = part + (static_cast<int64_t>(z) * r16 + j0) * C + k;
 #pragma unroll
@@ -378,12 +426,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
       }
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kCsWarps + 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kCsTmemCols);
-  }
+  tc_teardown(tmem, kCsTmemCols);
 }
 
 // dst(j, k) = scale sum_z part[z][j][k]; part has r16 = 16 ceil(r / 16) rows
@@ -450,14 +493,14 @@ cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4]
   static DeviceOnce configured;
   e = configured.run(dev, [] {
     return cudaFuncSetAttribute(act8_colsum_kernel<kFormat>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kCsSmem<kFormat>);
+                                tc_smem<kFormat>(kCsStage));
   });
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.cols + kCsCols - 1) / kCsCols), static_cast<unsigned>(splits));
   if (overlap)
-    return launch_dependent(act8_colsum_kernel<kFormat>, grid, kCsThreads, kCsSmem<kFormat>, stream, x, maps[0], maps[1],
+    return launch_dependent(act8_colsum_kernel<kFormat>, grid, kTcThreads, tc_smem<kFormat>(kCsStage), stream, x, maps[0], maps[1],
                             maps[2], maps[3], r16, splits, part, status);
-  act8_colsum_kernel<kFormat><<<grid, kCsThreads, kCsSmem<kFormat>, stream>>>(x, maps[0], maps[1], maps[2], maps[3], r16,
+  act8_colsum_kernel<kFormat><<<grid, kTcThreads, tc_smem<kFormat>(kCsStage), stream>>>(x, maps[0], maps[1], maps[2], maps[3], r16,
                                                                              splits, part, status);
   return cudaGetLastError();
 }
@@ -499,221 +542,149 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
 }
 
 // ---------------------------------------------------------------------------
-// skinny: part[z][m][j] = sum_{k in split z} X^[m][k] A[j][k]
+// rowsum: part[z][m][j] = sum_{k in split z} X^[m][k] W(j, k)
 // ---------------------------------------------------------------------------
-// m16n8k16 MMAs with D = [16 tokens][8 j], K = the columns.  Which column a K
-// slot stands for is free as long as both operands agree: in each half (32
-// columns) of a 64-column block lane (g, t) takes columns 8t .. 8t + 7, of its
-// token rows (8 code bytes) and of its rows of A (16 bytes), and MMA step s of
-// the half takes columns 8t + 4s .. + 3 as the lane's four slots.  Every load
-// is 8 or 16 bytes and feeds its registers as it is.
-//
-// A CTA is kSkWT groups of 32 tokens x kSkWK column shares.  The shares' blocks
-// of A come through a ring in shared memory (read through L1, the rows of a
-// block, 2 K bytes apart, evict each other where K is a power of two: five
-// times slower at K = 8192), and the shares' sums are added in shared memory
-// in a fixed order.  The codes and steps of a warp's next block are loaded
-// before its current one is multiplied.
+// D[tokens][j] with the columns as K: A, the X^ tile, is K-major; B is K-major
+// from W [r][K] (U = X^ A^T) or MN-major from W [K][r] (V = dY B, with dY plain
+// bf16).  A CTA takes 128 tokens and a range of the columns, 128 per step.  One
+// MMA of N = 64 per 16 columns: what W lacks of 64 j is zero-filled by TMA.
+// Bounded as colsum is: 13.2 us at 1999 x 8192 (16.8 MB of codes), 7.6 us for V
+// from dY 1999 x 2048, where warp-level MMAs took 20.4 and 16.2 us.
 namespace {
 
-constexpr int kSkWT = 4, kSkWK = 2;
-constexpr int kSkWarps = kSkWT * kSkWK;
-constexpr int kSkMT = 2;  // 16-token tiles of a warp
-constexpr int kSkWarpTokens = kSkMT * 16, kSkTokens = kSkWT * kSkWarpTokens;
-constexpr int kSkStages = 3;
+constexpr int kRsTok = 128;                 // tokens of a CTA
+constexpr int kRsCols = 128;                // columns per step
+constexpr int kRsXBox = kRsTok * 128;       // [128 tokens][64 columns]
+constexpr int kRsWBox = kRankPad * 128;     // [64 j][64 columns] or [64 columns][64 j]
+constexpr int kRsXTile = kRsCols / 64 * kRsXBox;
+constexpr int kRsStage = kRsXTile + kRsCols / 64 * kRsWBox;
+constexpr uint32_t kRsTmemCols = 64;
 
-template <int NT>
-struct SkinnyShape {
-  static constexpr int kTile = NT * 8 * 128;  // one block of A: [j][64 columns]
-  static constexpr int kRing = kSkStages * kSkWK * kTile;
-  static constexpr int kPitch = NT * 8 + 8;   // floats: rows g apart by 8 banks, so the lanes' pairs never meet
-  static constexpr int kSums = kSkWK * kSkTokens * kPitch * static_cast<int>(sizeof(float));
-  static constexpr int kSmem = kRing > kSums ? kRing : kSums;
-};
-
-// Byte offset of 16-byte chunk c of row j in a block of A: odd rows have their
-// halves exchanged, so that two rows' 64 bytes make a conflict-free read.
-__device__ __forceinline__ int sk_chunk(int j, int c) { return j * 128 + (c ^ ((j & 1) << 2)) * 16; }
-
-int act8_skinny_splits(int64_t M, int64_t K) {
-  const int64_t tiles = (M + kSkTokens - 1) / kSkTokens, blocks = K / kBlock;
+int rs_splits(int64_t M, int64_t K) {
+  const int64_t tiles = (M + kRsTok - 1) / kRsTok, steps = (K + kRsCols - 1) / kRsCols;
   int64_t s = 148 / tiles;  // one wave of a CTA per SM
-  if (s < 1) s = 1;
-  const int64_t most = (blocks + kSkWK - 1) / kSkWK;  // a block per warp at least
-  if (s > most) s = most;
+  if (s > steps) s = steps;
   const int64_t room = skinny_splits(M, K);  // what the workspace's partials are sized for
-  return static_cast<int>(s < room ? s : room);
+  if (s > room) s = room;
+  return static_cast<int>(s < 1 ? 1 : s);
 }
-
-template <int kFormat>
-struct SkinnyX {  // one lane's part of a 64-column block of 32 tokens
-  uint2 c[kSkMT][2][2];     // [tile][row g, g + 8][half]
-  uint32_t s[kSkMT][2];     // packed steps
-
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint16_t* step, int64_t M, int64_t K, int64_t m0,
-                                       int64_t kb, bool live) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int a = 0; a < kSkMT; ++a)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t row = m0 + a * 16 + h * 8 + g;
-        const bool ok = live && row < M;
-        const uint2* src = reinterpret_cast<const uint2*>(codes + (ok ? row * K + kb * kBlock + t * 8 : 0));
-        c[a][h][0] = ok ? __ldg(src) : make_uint2(0, 0);
-        c[a][h][1] = ok ? __ldg(src + 4) : make_uint2(0, 0);
-        s[a][h] = ok ? __ldg(step + row * (K / kBlock) + kb) : 0u;
-      }
-  }
-};
 
 }  // namespace
 
-template <int kFormat, int NT>
-__global__ void __launch_bounds__(32 * kSkWarps) act8_skinny_kernel(const uint8_t* __restrict__ codes,
-                                                                    const uint16_t* __restrict__ step,
-                                                                    const uint16_t* __restrict__ A, int64_t M,
-                                                                    int64_t K, int r, int splits,
-                                                                    float* __restrict__ part) {
-  using S = SkinnyShape<NT>;
-  constexpr int kPitch = S::kPitch;
-  extern __shared__ __align__(16) uint8_t ring[];
+template <int kFormat>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    act8_rowsum_kernel(Act8View x, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       int r16, int splits, float* __restrict__ part, int* status) {
+  constexpr bool kDense = kFormat == kAct8Dense;
+  extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TcBarriers* bars = reinterpret_cast<TcBarriers*>(smem + kTcStages * kRsStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3, wt = warp % kSkWT, wk = warp / kSkWT;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSkTokens + wt * kSkWarpTokens;
+  const int64_t M = x.rows, K = x.cols;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRsTok;
   const int z = blockIdx.y;
-  const int64_t kblocks = K / kBlock;
-  const int64_t first = kblocks * z / splits, b1 = kblocks * (z + 1) / splits;
-  const int steps = static_cast<int>((b1 - first + kSkWK - 1) / kSkWK);  // of kSkWK blocks
+  const int64_t total = (K + kRsCols - 1) / kRsCols, first = total * z / splits;
+  const int n = static_cast<int>(total * (z + 1) / splits - first);  // steps, at least one
+  const uint32_t tmem = tc_setup(bars, kRsTmemCols);
 
-  auto issue = [&](int i) {
-    if (i < steps) {
-      uint8_t* st = ring + (i % kSkStages) * (kSkWK * S::kTile);
+  if (warp == kTcWarps) {
+    if (lane == 0)
+      tc_produce(smem, kRsStage, bars, n, kDense ? kRsStage : kRsStage - kRsXTile, status,
+                 [&](uint8_t* st, uint64_t* bar, int i) {
+                   const int k = static_cast<int>((first + i) * kRsCols), m = static_cast<int>(m0);
+                   for (int g = 0; g < kRsCols / 64; ++g) {
+                     if constexpr (kDense) {  // V: W [K][r]
+                       tma_load_2d(st + g * kRsXBox, &tmX, bar, k + g * 64, m);
+                       tma_load_2d(st + kRsXTile + g * kRsWBox, &tmW, bar, 0, k + g * 64);
+                     } else {  // U: W [r][K]
+                       tma_load_2d(st + kRsXTile + g * kRsWBox, &tmW, bar, k + g * 64, 0);
+                     }
+                   }
+                 });
+  } else if (warp == kTcWarps + 1) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kRankPad, kDense);
+    const uint32_t st = smem_u32(smem);
+    // K = 16 columns: 32 bytes along a K-major row; 16 rows = 2 KB of an MN-major box.
+    const uint64_t a = smem_desc_k128(st);
+    const uint64_t b = kDense ? smem_desc_mn128(st + kRsXTile, kRsWBox, 1024) : smem_desc_k128(st + kRsXTile);
+    if (lane == 0)
+      tc_issue<kDense>(bars, n, status, [&](int s, int i) {
 #pragma unroll
-      for (int q = 0; q < kSkWK * S::kTile / 16 / (32 * kSkWarps); ++q) {
-        const int chunk = q * (32 * kSkWarps) + threadIdx.x;
-        const int share = chunk / (S::kTile / 16), rest = chunk % (S::kTile / 16), j = rest / 8, c = rest % 8;
-        const int64_t kb = first + static_cast<int64_t>(i) * kSkWK + share;
-        const bool ok = j < r && kb < b1;
-        cp_async_16(st + share * S::kTile + sk_chunk(j, c), A + (ok ? j * K + kb * kBlock + c * 8 : 0), ok);
-      }
-    }
-    cp_async_commit();
-  };
-
-  float acc[kSkMT][NT][4];
-#pragma unroll
-  for (int a = 0; a < kSkMT; ++a)
-#pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.0f;
-
-#pragma unroll
-  for (int i = 0; i < kSkStages - 1; ++i) issue(i);
-  SkinnyX<kFormat> next;
-  next.load(codes, step, M, K, m0, first + wk, first + wk < b1);
-  for (int i = 0; i < steps; ++i) {
-    const int64_t kb = first + static_cast<int64_t>(i) * kSkWK + wk;
-    SkinnyX<kFormat> x = next;
-    next.load(codes, step, M, K, m0, kb + kSkWK, kb + kSkWK < b1);
-    cp_async_wait<kSkStages - 2>();
-    __syncthreads();  // everyone's copies of this stage are there, and the one before is read
-    issue(i + kSkStages - 1);
-    const uint8_t* tile = ring + (i % kSkStages) * (kSkWK * S::kTile) + wk * S::kTile;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint4 av[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        av[nt] = *reinterpret_cast<const uint4*>(tile + sk_chunk(nt * 8 + g, half * 4 + t));
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {  // columns 8t + 4w .. + 3 of the half
-        uint32_t af[kSkMT][4];
-#pragma unroll
-        for (int a = 0; a < kSkMT; ++a)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t word = w == 0 ? x.c[a][h][half].x : x.c[a][h][half].y;
-            const uint32_t s2 = x.s[a][h] | (x.s[a][h] << 16);
-            af[a][h] = act8_decode2<kFormat, 0>(word, s2);
-            af[a][h + 2] = act8_decode2<kFormat, 2>(word, s2);
-          }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t bf[2] = {w == 0 ? av[nt].x : av[nt].z, w == 0 ? av[nt].y : av[nt].w};
-#pragma unroll
-          for (int a = 0; a < kSkMT; ++a) mma_16816(acc[a][nt], af[a], bf);
+        for (int kk = 0; kk < kRsCols / 16; ++kk) {
+          const int box = kk / 4, sub = kk % 4;
+          tc_mma_bf16_ss(tmem, a + static_cast<uint64_t>((s * kRsStage + box * kRsXBox + sub * 32) >> 4),
+                         b + static_cast<uint64_t>((s * kRsStage + box * kRsWBox + sub * (kDense ? 2048 : 32)) >> 4),
+                         idesc, (i > 0 || kk > 0) ? 1u : 0u);
         }
+      });
+  } else {
+    bool ok = true;
+    if constexpr (!kDense) {
+      const int rows = static_cast<int>(min(M - m0, static_cast<int64_t>(kRsTok)));
+      const int cols = static_cast<int>(min(K - first * kRsCols, static_cast<int64_t>(n) * kRsCols));
+      ok = tc_decode<kFormat, kRsCols / 16, kRsTok, kRsStage>(
+          x, m0, first * kRsCols, kRsCols, n, smem, smem + kTcStages * kRsStage + kTcBarriers, bars, status,
+          [&](int i, int row, int col) { return row < rows && i * kRsCols + col < cols; });
+    }
+    pdl_wait_prior();  // an overlapped launch ends after the kernel before it
+    const int quad = warp & 3, j0 = warp / 4 * 16;  // TMEM lanes (tokens) 32 quad .. + 31, 16 j
+    if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status) && j0 < r16) {
+      tc_fence_after();
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(j0), v);
+      tc_wait_ld(v);
+      const int64_t m = m0 + quad * 32 + lane;
+      if (m < M) {
+        float4* dst = reinterpret_cast<float4*>(part + (static_cast<int64_t>(z) * M + m) * kRankPad + j0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
+                               __uint_as_float(v[4 * q + 3]));
       }
     }
   }
-  cp_async_wait<0>();
-  __syncthreads();  // the ring's space takes the sums
-  float* sums = reinterpret_cast<float*>(ring);  // [kSkWK][kSkTokens][kPitch]
-#pragma unroll
-  for (int a = 0; a < kSkMT; ++a)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<float2*>(sums + ((wk * kSkTokens) + wt * kSkWarpTokens + a * 16 + h * 8 + g) * kPitch + nt * 8 +
-                                   2 * t) = make_float2(acc[a][nt][2 * h], acc[a][nt][2 * h + 1]);
-  __syncthreads();
-  constexpr int kOut = kSkTokens * NT * 2;  // in fours
-  for (int i = threadIdx.x; i < kOut; i += 32 * kSkWarps) {
-    const int m = i / (NT * 2), j = i % (NT * 2) * 4;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kSkTokens + m;
-    if (row >= M) break;
-    float4 s = *reinterpret_cast<const float4*>(sums + m * kPitch + j);
-#pragma unroll
-    for (int w = 1; w < kSkWK; ++w) {
-      const float4 o = *reinterpret_cast<const float4*>(sums + (w * kSkTokens + m) * kPitch + j);
-      s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
-    }
-    *reinterpret_cast<float4*>(part + (static_cast<int64_t>(z) * M + row) * kRankPad + j) = s;
-  }
+  tc_teardown(tmem, kRsTmemCols);
 }
 
 namespace {
 
-template <int kFormat, int NT>
-cudaError_t launch_skinny_nt(const Act8View& x, const uint16_t* A, int r, int splits, float* part,
-                             cudaStream_t stream) {
-  constexpr int smem = SkinnyShape<NT>::kSmem;
+template <int kFormat>
+cudaError_t launch_rowsum_format(const Act8View& x, const CUtensorMap& tx, const CUtensorMap& tw, int r16, int splits,
+                                 float* part, bool overlap, int* status, cudaStream_t stream) {
+  constexpr int smem = tc_smem<kFormat>(kRsStage);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static DeviceOnce configured;
   e = configured.run(dev, [] {
-    return cudaFuncSetAttribute(act8_skinny_kernel<kFormat, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(act8_rowsum_kernel<kFormat>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((x.rows + kSkTokens - 1) / kSkTokens), static_cast<unsigned>(splits));
-  act8_skinny_kernel<kFormat, NT><<<grid, 32 * kSkWarps, smem, stream>>>(x.codes, x.step, A, x.rows, x.cols, r, splits,
-                                                                        part);
+  const dim3 grid(static_cast<unsigned>((x.rows + kRsTok - 1) / kRsTok), static_cast<unsigned>(splits));
+  if (overlap)
+    return launch_dependent(act8_rowsum_kernel<kFormat>, grid, kTcThreads, smem, stream, x, tx, tw, r16, splits, part,
+                            status);
+  act8_rowsum_kernel<kFormat><<<grid, kTcThreads, smem, stream>>>(x, tx, tw, r16, splits, part, status);
   return cudaGetLastError();
-}
-
-template <int kFormat>
-cudaError_t launch_skinny_format(const Act8View& x, const uint16_t* A, int r, int splits, float* part,
-                                 cudaStream_t stream) {
-  switch ((r + 15) / 16) {
-    case 1: return launch_skinny_nt<kFormat, 2>(x, A, r, splits, part, stream);
-    case 2: return launch_skinny_nt<kFormat, 4>(x, A, r, splits, part, stream);
-    case 3: return launch_skinny_nt<kFormat, 6>(x, A, r, splits, part, stream);
-    default: return launch_skinny_nt<kFormat, 8>(x, A, r, splits, part, stream);
-  }
 }
 
 }  // namespace
 
-cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, int* splits,
-                               cudaStream_t stream) {
-  *splits = act8_skinny_splits(x.rows, x.cols);
-  return x.format == kAct8Int8 ? launch_skinny_format<kAct8Int8>(x, A, r, *splits, part, stream)
-                               : launch_skinny_format<kAct8E4m3>(x, A, r, *splits, part, stream);
+cudaError_t launch_act8_rowsum(const Act8View& x, const uint16_t* W, int64_t ldw, int r, float* part, int* splits,
+                               bool overlap, int* status, cudaStream_t stream) {
+  *splits = rs_splits(x.rows, x.cols);
+  const int r16 = (r + 15) / 16 * 16;
+  CUtensorMap tx, tw;
+  if (x.format == kAct8Dense) {
+    if (!encode_tensor_map_2d(&tx, x.codes, x.rows, x.cols, kRsTok, 64)) return cudaErrorInvalidValue;
+    if (!encode_tensor_map_2d(&tw, W, x.cols, r, 64, kRankPad, true, ldw)) return cudaErrorInvalidValue;
+    return launch_rowsum_format<kAct8Dense>(x, tx, tw, r16, *splits, part, overlap, status, stream);
+  }
+  if (!encode_tensor_map_2d(&tw, W, r, x.cols, kRankPad, 64)) return cudaErrorInvalidValue;
+  return x.format == kAct8Int8
+             ? launch_rowsum_format<kAct8Int8>(x, tw, tw, r16, *splits, part, overlap, status, stream)
+             : launch_rowsum_format<kAct8E4m3>(x, tw, tw, r16, *splits, part, overlap, status, stream);
 }
 
 }  // namespace qnf4

@@ -937,7 +937,8 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     Timed tm(kFamSide, s, 2);
     if (x8 != nullptr) {
       SkinnyJob job{at<float>(ws, lay.part), 0, uo};
-      const cudaError_t err = launch_act8_skinny(view_of(x8), A, r, at<float>(ws, lay.part), &job.splits, s);
+      const cudaError_t err = launch_act8_rowsum(view_of(x8), A, K, r, at<float>(ws, lay.part), &job.splits, false,
+                                                 status, s);
       return err != cudaSuccess ? err : launch_skinny_finalize(&job, 1, M, r, s);
     }
     return launch_skinny(X, M, K, A, true, r, 0, at<float>(ws, lay.skpart), uo, status, s);
@@ -977,22 +978,27 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     vo.olo = at<uint16_t>(ws, lay.vlo);
     vo.olo2 = vlo2;
     vo.scale = scale;
-    if (x8 != nullptr && dB != nullptr && U == nullptr) {
+    const bool u_done = x8 != nullptr && dB != nullptr && U == nullptr;
+    if (u_done) {
       // U too: V's product runs beside U's, and one reduction ends both.
       Timed tm(kFamSide, s, 3);
       SkinnyJob jobs[2] = {{at<float>(ws, lay.part), 0, uo}, {at<float>(ws, lay.skpart), 0, vo}};
-      e = launch_act8_skinny(view_of(x8), A, r, at<float>(ws, lay.part), &jobs[0].splits, s);
+      e = launch_act8_rowsum(view_of(x8), A, K, r, at<float>(ws, lay.part), &jobs[0].splits, false, status, s);
       if (e == cudaSuccess)
-        e = launch_skinny_partials(dY, M, N, Bk, false, r, ldbk, at<float>(ws, lay.skpart), &jobs[1].splits, true, status,
-                                   s);
+        e = launch_act8_rowsum(dense_view(dY, M, N), Bk, ldbk, r, at<float>(ws, lay.skpart), &jobs[1].splits, true, status,
+                               s);
       if (e == cudaSuccess) e = launch_skinny_finalize(jobs, 2, M, r, s);
     } else {
-      {
-        Timed tm(kFamSide, s, 2);
+      Timed tm(kFamSide, s, 2);
+      if (x8 != nullptr) {
+        SkinnyJob job{at<float>(ws, lay.skpart), 0, vo};
+        e = launch_act8_rowsum(dense_view(dY, M, N), Bk, ldbk, r, at<float>(ws, lay.skpart), &job.splits, false, status, s);
+        if (e == cudaSuccess) e = launch_skinny_finalize(&job, 1, M, r, s);
+      } else {
         e = launch_skinny(dY, M, N, Bk, false, r, ldbk, at<float>(ws, lay.skpart), vo, status, s);
       }
-      if (e == cudaSuccess && dB != nullptr) e = u_hilo();
     }
+    if (e == cudaSuccess && dB != nullptr && !u_done) e = u_hilo();
     if (e != cudaSuccess) return from_cuda(e);
     if (dB != nullptr && x8 != nullptr) {  // dB = s dY^T U, with dA beside it
       const ColsumJob jobs[2] = {db_job, da_job};

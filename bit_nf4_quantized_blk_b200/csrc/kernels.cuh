@@ -214,12 +214,6 @@ struct SkinnyJob {
   SkinnyOut out;
 };
 cudaError_t launch_skinny_finalize(const SkinnyJob* jobs, int count, int64_t M, int r, cudaStream_t stream);
-// launch_skinny's product alone, its reduction left to launch_skinny_finalize.
-// `overlap`: may run beside the previous kernel of the stream, which writes
-// nothing that this one reads (it ends after that kernel in any case).
-cudaError_t launch_skinny_partials(const uint16_t* In, int64_t M, int64_t C, const uint16_t* Wt, bool wt_is_rc, int r,
-                                   int64_t ldw, float* part, int* splits, bool overlap, int* status,
-                                   cudaStream_t stream);
 // hi/lo (and, unless null, lo2) bf16 split of a compact fp32 [M][r] matrix into [M][64] buffers.
 cudaError_t launch_split_hilo(const float* src, int64_t M, int r, uint16_t* hi, uint16_t* lo, uint16_t* lo2,
                               cudaStream_t stream);
@@ -301,10 +295,14 @@ struct ColsumJob {
 size_t act8_colsum_partial_bytes(int64_t M, int64_t C);
 cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, int* status,
                                 cudaStream_t stream);
-// launch_skinny_partials' product X^ A^T from a checkpoint (A [r][K] bf16,
-// 16-byte aligned rows); `part` as for launch_skinny.
-cudaError_t launch_act8_skinny(const Act8View& x, const uint16_t* A, int r, float* part, int* splits,
-                               cudaStream_t stream);
+// part[z][m][j] = sum over the columns k of split z of X^[m][k] W(j, k): W is
+// [r][cols] for a checkpoint, [cols][r] of pitch ldw for plain bf16 values (both
+// 16-byte aligned rows); `part` as for launch_skinny, reduced by
+// launch_skinny_finalize.  `overlap`: may run beside the previous kernel of the
+// stream, which writes nothing that this one reads (it ends after that kernel in
+// any case).
+cudaError_t launch_act8_rowsum(const Act8View& x, const uint16_t* W, int64_t ldw, int r, float* part, int* splits,
+                               bool overlap, int* status, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Residual sum between two norms (residual_norm.cu)

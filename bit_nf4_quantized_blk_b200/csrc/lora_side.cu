@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(const __grid_constant_
     if (lane == 0) mbar_arrive(&bars->empty[s]);
   }
 
-  pdl_wait_prior();  // an overlapped launch ends after the kernel before it
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -185,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(const __grid_constant_
 
 // out(m, j) = sum_z part[z][m][j] (fixed order); j >= r gives 0.
 // Threads past the M * 32 pairs run out.bs (the GEMM's block scales) when set.
+// blockIdx.y: the job.
 __global__ void skinny_finalize_kernel(const __grid_constant__ SkinnyJob job0, const __grid_constant__ SkinnyJob job1,
                                        int64_t M, int r) {
   pdl_wait_prior();
@@ -263,7 +263,7 @@ size_t skinny_partial_bytes(int64_t M, int64_t C) {
 
 template <bool kRowLayout, int NT>
 cudaError_t launch_skinny_nt(const CUtensorMap& tin, const CUtensorMap& tw, int64_t M, int64_t C, int splits,
-                             float* part, bool overlap, int* status, cudaStream_t stream) {
+                             float* part, int* status, cudaStream_t stream) {
   constexpr int kStage = kInTile + 128 * NT * 8;
   constexpr int smem = 1024 + kStages * kStage + static_cast<int>(sizeof(PipeBarriers));
   int dev = 0;
@@ -275,40 +275,36 @@ cudaError_t launch_skinny_nt(const CUtensorMap& tin, const CUtensorMap& tw, int6
   });
   if (e != cudaSuccess) return e;
   dim3 grid(static_cast<unsigned>((M + kTileRows - 1) / kTileRows), static_cast<unsigned>(splits));
-  if (overlap)
-    return launch_dependent(skinny_kernel<kRowLayout, NT>, grid, kThreads, smem, stream, tin, tw, M, C, splits, part,
-                            status);
   skinny_kernel<kRowLayout, NT><<<grid, kThreads, smem, stream>>>(tin, tw, M, C, splits, part, status);
   return cudaGetLastError();
 }
 
-cudaError_t launch_skinny_partials(const uint16_t* In, int64_t M, int64_t C, const uint16_t* Wt, bool wt_is_rc, int r,
-                                   int64_t ldw, float* part, int* splits_out, bool overlap, int* status,
-                                   cudaStream_t stream) {
-  const int splits = *splits_out = skinny_splits(M, C);
+cudaError_t launch_skinny(const uint16_t* In, int64_t M, int64_t C, const uint16_t* Wt, bool wt_is_rc, int r,
+                          int64_t ldw, float* part, const SkinnyOut& out, int* status, cudaStream_t stream) {
+  const int splits = skinny_splits(M, C);
   const int nt = ((r + 15) / 16) * 2;
   CUtensorMap tin, tw;
   if (!encode_tensor_map_2d(&tin, In, M, C, kTileRows, kTileCols)) return cudaErrorInvalidValue;
   if (wt_is_rc) {
     if (!encode_tensor_map_2d(&tw, Wt, r, C, nt * 8, kTileCols)) return cudaErrorInvalidValue;
-    return nt == 2   ? launch_skinny_nt<true, 2>(tin, tw, M, C, splits, part, overlap, status, stream)
-           : nt == 4 ? launch_skinny_nt<true, 4>(tin, tw, M, C, splits, part, overlap, status, stream)
-           : nt == 6 ? launch_skinny_nt<true, 6>(tin, tw, M, C, splits, part, overlap, status, stream)
-                     : launch_skinny_nt<true, 8>(tin, tw, M, C, splits, part, overlap, status, stream);
+  } else {
+    if (!encode_tensor_map_2d(&tw, Wt, C, r, kTileCols, nt * 8, false, ldw)) return cudaErrorInvalidValue;
   }
-  if (!encode_tensor_map_2d(&tw, Wt, C, r, kTileCols, nt * 8, false, ldw)) return cudaErrorInvalidValue;
-  return nt == 2   ? launch_skinny_nt<false, 2>(tin, tw, M, C, splits, part, overlap, status, stream)
-         : nt == 4 ? launch_skinny_nt<false, 4>(tin, tw, M, C, splits, part, overlap, status, stream)
-         : nt == 6 ? launch_skinny_nt<false, 6>(tin, tw, M, C, splits, part, overlap, status, stream)
-                   : launch_skinny_nt<false, 8>(tin, tw, M, C, splits, part, overlap, status, stream);
-}
-
-cudaError_t launch_skinny(const uint16_t* In, int64_t M, int64_t C, const uint16_t* Wt, bool wt_is_rc, int r,
-                          int64_t ldw, float* part, const SkinnyOut& out, int* status, cudaStream_t stream) {
-  SkinnyJob job{part, 0, out};
-  const cudaError_t e =
-      launch_skinny_partials(In, M, C, Wt, wt_is_rc, r, ldw, part, &job.splits, false, status, stream);
-  return e != cudaSuccess ? e : launch_skinny_finalize(&job, 1, M, r, stream);
+  cudaError_t e;
+  if (wt_is_rc) {
+    e = nt == 2   ? launch_skinny_nt<true, 2>(tin, tw, M, C, splits, part, status, stream)
+        : nt == 4 ? launch_skinny_nt<true, 4>(tin, tw, M, C, splits, part, status, stream)
+        : nt == 6 ? launch_skinny_nt<true, 6>(tin, tw, M, C, splits, part, status, stream)
+                  : launch_skinny_nt<true, 8>(tin, tw, M, C, splits, part, status, stream);
+  } else {
+    e = nt == 2   ? launch_skinny_nt<false, 2>(tin, tw, M, C, splits, part, status, stream)
+        : nt == 4 ? launch_skinny_nt<false, 4>(tin, tw, M, C, splits, part, status, stream)
+        : nt == 6 ? launch_skinny_nt<false, 6>(tin, tw, M, C, splits, part, status, stream)
+                  : launch_skinny_nt<false, 8>(tin, tw, M, C, splits, part, status, stream);
+  }
+  if (e != cudaSuccess) return e;
+  const SkinnyJob job{part, splits, out};
+  return launch_skinny_finalize(&job, 1, M, r, stream);
 }
 
 cudaError_t launch_skinny_finalize(const SkinnyJob* jobs, int count, int64_t M, int r, cudaStream_t stream) {
