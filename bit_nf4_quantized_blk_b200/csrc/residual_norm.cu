@@ -598,11 +598,12 @@ cudaError_t launch_bwd(const ResidualNormBwd& p, cudaStream_t stream) {
 }  // namespace
 
 int residual_norm_bwd_ctas(int64_t M, int64_t D) {
-  // Every CTA leaves a partial row of the column sums: with few rows, four or
-  // more per CTA keep those below the operands themselves.
-  const int64_t full = norm_ctas(M, D, kBwdResident);
-  const int64_t few = std::max<int64_t>(std::min<int64_t>(full, 148), M / 4);
-  return static_cast<int>(std::min(full, few));
+  // Every CTA leaves a partial row of the column sums: with few rows, the same
+  // number of CTAs on each SM and three or more rows for each keep those below
+  // the operands themselves (999 x 2048: 296 CTAs 16.4 us, 148 17.4, 249 18.4,
+  // 444 18.5, 499 20.5).
+  return static_cast<int>(
+      std::min<int64_t>(norm_ctas(M, D, kBwdResident), 148 * std::max<int64_t>(1, M / (148 * 3))));
 }
 
 cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cudaStream_t stream) {
