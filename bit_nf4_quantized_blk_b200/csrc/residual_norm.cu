@@ -40,8 +40,8 @@ constexpr int kWarpRowCtas = 8;  // rows (warps) of a CTA when a warp takes a ro
 template <int TPR>
 constexpr int kNormThreads = TPR == 32 ? 32 * kWarpRowCtas : TPR;
 
-// Threads that share an SM: what the registers allow (about 80 and 128 per thread).
-constexpr int kFwdResident = 768, kBwdResident = 512;
+// Threads that share an SM: what the registers allow (64 and 128 per thread).
+constexpr int kFwdResident = 1024, kBwdResident = 512;
 
 // Whether the backward keeps its channel factors in shared memory: read from
 // L1 for every row their latency was a third of its stalls.  The longest rows
@@ -143,6 +143,27 @@ struct RowSlot {
   }
 };
 
+// w_pre (0 unless `has_pre`) and scale gate w_post of the eight channels at `at`.
+template <typename Params>
+__device__ __forceinline__ void read_factors(const Params& p, int at, bool has_pre, F2 (&pre)[4], F2 (&branch)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pre[i] = splat2(0.0f), branch[i] = splat2(p.scale);
+  if (at < p.D) {
+    F2 f[4];
+    if (p.w_post != nullptr) {
+      load8(p.w_post, at, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) branch[i] = mul2(branch[i], f[i]);
+    }
+    if (p.gate != nullptr) {
+      load8(p.gate, at, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) branch[i] = mul2(branch[i], f[i]);
+    }
+    if (has_pre) load8(p.w_pre, at, pre);
+  }
+}
+
 }  // namespace
 
 template <typename TRes, int TPR, int NC>
@@ -153,6 +174,9 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
   constexpr int kRows = kNormThreads<TPR> / TPR;
   extern __shared__ __align__(16) uint8_t slots_h[];
   uint8_t* slots_y = slots_h + H::kBytes;
+  using W = RowSlot<float, TPR, NC>;
+  uint8_t* factor_pre = slots_y + Y::kBytes;
+  uint8_t* factor_branch = factor_pre + W::kBytes;
   __shared__ __align__(16) float sums[4][32];
   const int tid = threadIdx.x % TPR;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
@@ -169,27 +193,16 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
     cp_async_commit();
   };
   fetch(row);
-  // The branch's factor scale gate w_post and w_pre stay in registers: read
-  // from L1 for every row they were half of the kernel's L1 traffic.
-  F2 coef[NC][4], w_pre[NC][4];
+  // w_pre and the branch's factor scale gate w_post, each thread's own share, in
+  // shared memory: read from L1 for every row they were half of the kernel's L1
+  // traffic, and in registers they cost a quarter of the resident threads
+  // (8192 x 4096 with a checkpoint: 60 us, so 56 to 59).
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int at = (c * TPR + tid) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) coef[c][i] = splat2(p.scale), w_pre[c][i] = splat2(0.0f);
-    if (at >= p.D) continue;
-    F2 w[4];
-    if (p.w_post != nullptr) {
-      load8(p.w_post, at, w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) coef[c][i] = mul2(coef[c][i], w[i]);
-    }
-    if (p.gate != nullptr) {
-      load8(p.gate, at, w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) coef[c][i] = mul2(coef[c][i], w[i]);
-    }
-    if (p.w_pre != nullptr) load8(p.w_pre, at, w_pre[c]);
+    F2 pre[4], branch[4];
+    read_factors(p, (c * TPR + tid) * 8, p.w_pre != nullptr, pre, branch);
+    W::write(factor_pre, c, pre);
+    W::write(factor_branch, c, branch);
   }
   int turn = 0;  // row_sum arrays alternate from row to row: a row's are written again two barriers later
   for (; row < p.M; row += stride, turn ^= 1) {
@@ -214,9 +227,12 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
         if (p.rstd_post != nullptr && tid == 0) p.rstd_post[row] = rstd;
       }
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+      for (int c = 0; c < NC; ++c) {
+        F2 branch[4];
+        W::read(factor_branch, c, branch);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[c][i] = fma2(mul2(y[c][i], splat2(rstd)), coef[c][i], v[c][i]);
+        for (int i = 0; i < 4; ++i) v[c][i] = fma2(mul2(y[c][i], splat2(rstd)), branch[i], v[c][i]);
+      }
     }
     if (h_out != nullptr) {
 #pragma unroll
@@ -238,8 +254,10 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
       const int at = (c * TPR + tid) * 8;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (at < p.D) {
+        F2 w_pre[4];
+        W::read(factor_pre, c, w_pre);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], splat2(rstd)), w_pre[c][i]);
+        for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], splat2(rstd)), w_pre[i]);
         x = pack8(v[c]);
         *reinterpret_cast<uint4*>(p.x + base + at) = x;
       }
@@ -267,29 +285,6 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kFwdResident>
   }
   cp_async_wait<0>();
 }
-
-namespace {
-
-// w_pre (0 without one) and scale gate w_post of the eight channels at `at`.
-__device__ __forceinline__ void read_factors(const ResidualNormBwd& p, int at, F2 (&pre)[4], F2 (&branch)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) pre[i] = splat2(0.0f), branch[i] = splat2(p.scale);
-  if (at >= p.D) return;
-  if (p.dx != nullptr) load8(p.w_pre, at, pre);
-  F2 f[4];
-  if (p.w_post != nullptr) {
-    load8(p.w_post, at, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) branch[i] = mul2(branch[i], f[i]);
-  }
-  if (p.gate != nullptr) {
-    load8(p.gate, at, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) branch[i] = mul2(branch[i], f[i]);
-  }
-}
-
-}  // namespace
 
 template <typename TRes, int TPR, int NC>
 __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>)
@@ -356,7 +351,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     F2 f[4], b[4];
-    read_factors(p, (c * TPR + tid) * 8, f, b);
+    read_factors(p, (c * TPR + tid) * 8, p.dx != nullptr, f, b);
     if constexpr (kStash<TPR>) {
       W::write(factor_pre, c, f);
       W::write(factor_branch, c, b);
@@ -374,7 +369,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
       if constexpr (kStash<TPR>)
         W::read(factor_pre, c, w[c]);
       else
-        read_factors(p, (c * TPR + tid) * 8, w[c], other);
+        read_factors(p, (c * TPR + tid) * 8, p.dx != nullptr, w[c], other);
     }
     cp_async_wait<1>();
 #pragma unroll
@@ -414,7 +409,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, kMinCtas<TPR, kBwdResident>
       if constexpr (kStash<TPR>)
         W::read(factor_branch, c, w[c]);
       else
-        read_factors(p, (c * TPR + tid) * 8, other, w[c]);
+        read_factors(p, (c * TPR + tid) * 8, p.dx != nullptr, other, w[c]);
     }
     if (dh != nullptr) {
 #pragma unroll
@@ -576,7 +571,8 @@ template <typename TRes>
 cudaError_t launch_fwd(const ResidualNormFwd& p, cudaStream_t stream) {
   return with_shape(p.D, [&](auto tpr, auto nc) {
     constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
-    constexpr int smem = RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes;
+    constexpr int smem =
+        RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes + 2 * RowSlot<float, TPR, NC>::kBytes;
     static DeviceOnce configured;
     const int ctas = static_cast<int>(norm_ctas(p.M, p.D, kFwdResident));
     return launch_norm(residual_norm_fwd_kernel<TRes, TPR, NC>, configured, ctas, kNormThreads<TPR>, smem, p, stream);
