@@ -558,7 +558,8 @@ constexpr int kRsXBox = kRsTok * 128;       // [128 tokens][64 columns]
 constexpr int kRsWBox = kRankPad * 128;     // [64 j][64 columns] or [64 columns][64 j]
 constexpr int kRsXTile = kRsCols / 64 * kRsXBox;
 constexpr int kRsStage = kRsXTile + kRsCols / 64 * kRsWBox;
-constexpr uint32_t kRsTmemCols = 64;
+constexpr int kRsSums = 4;                  // accumulators: the tensor core truncates, so its chains are kept short
+constexpr uint32_t kRsTmemCols = kRsSums * kRankPad;
 
 int rs_splits(int64_t M, int64_t K) {
   const int64_t tiles = (M + kRsTok - 1) / kRsTok, steps = (K + kRsCols - 1) / kRsCols;
@@ -612,10 +613,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc_issue<kDense>(bars, n, status, [&](int s, int i) {
 #pragma unroll
         for (int kk = 0; kk < kRsCols / 16; ++kk) {
-          const int box = kk / 4, sub = kk % 4;
-          tc_mma_bf16_ss(tmem, a + static_cast<uint64_t>((s * kRsStage + box * kRsXBox + sub * 32) >> 4),
+          const int box = kk / 4, sub = kk % 4;  // sub: also which accumulator
+          static_assert(kRsSums == 4, "one per K step of a box");
+          tc_mma_bf16_ss(tmem + static_cast<uint32_t>(sub * kRankPad),
+                         a + static_cast<uint64_t>((s * kRsStage + box * kRsXBox + sub * 32) >> 4),
                          b + static_cast<uint64_t>((s * kRsStage + box * kRsWBox + sub * (kDense ? 2048 : 32)) >> 4),
-                         idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                         idesc, (i > 0 || box > 0) ? 1u : 0u);
         }
       });
   } else {
@@ -631,16 +634,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int quad = warp & 3, j0 = warp / 4 * 16;  // TMEM lanes (tokens) 32 quad .. + 31, 16 j
     if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status) && j0 < r16) {
       tc_fence_after();
-      uint32_t v[16];
-      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(j0), v);
-      tc_wait_ld(v);
+      uint32_t w[kRsSums][16];
+#pragma unroll
+      for (int i = 0; i < kRsSums; ++i)
+        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(i * kRankPad + j0), w[i]);
+#pragma unroll
+      for (int i = 0; i < kRsSums; ++i) tc_wait_ld(w[i]);
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        v[j] = (__uint_as_float(w[0][j]) + __uint_as_float(w[1][j])) +
+               (__uint_as_float(w[2][j]) + __uint_as_float(w[3][j]));
       const int64_t m = m0 + quad * 32 + lane;
       if (m < M) {
         float4* dst = reinterpret_cast<float4*>(part + (static_cast<int64_t>(z) * M + m) * kRankPad + j0);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
-                               __uint_as_float(v[4 * q + 3]));
+          dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       }
     }
   }

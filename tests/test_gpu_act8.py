@@ -108,7 +108,8 @@ def _checkpoint(x, fmt):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M, N, K, r", [(1, 64, 64, 1), (16, 72, 128, 5), (17, 136, 192, 8), (33, 40, 4160, 24),
                                         (130, 64, 1088, 16), (300, 72, 576, 33), (257, 128, 1536, 48),
-                                        (1000, 256, 2048, 64), (2050, 64, 64, 12)])
+                                        (1000, 256, 2048, 64), (2050, 64, 64, 12), (700, 8, 64, 64),
+                                        (1500, 1032, 2112, 40)])
 @pytest.mark.parametrize("saved_u", [True, False])
 def test_linear_backward(M, N, K, r, fmt, saved_u):
     s = 2.0
@@ -140,11 +141,18 @@ def test_linear_backward(M, N, K, r, fmt, saved_u):
     tol = (3 * M + 2 + (0 if saved_u else K)) * 2.0**-24 * s * np.abs(g).T @ absu + 1e-30
     assert (np.abs(_f64(dB[:N]) - ref) <= tol).all()
 
-    # dX does not depend on X: the same bits as from the bf16 activation.
+    # dX does not depend on X.  Ranks up to 16 share V's kernel with the bf16 path: the same bits.  Above, V is summed in
+    # another order: both are within e = N 2^-24 sum |dY| |B| of the exact V, so their bf16 roundings (2^-8 each) differ
+    # by at most 2^-7 (|V| + e) + 2 e; and dX is rounded once on each side.
     dX2 = torch.empty_like(dX)
     dA2, dB2 = torch.empty((r, K), device="cuda"), torch.empty((N, r), device="cuda")
     binding.qlora_linear_bwd(w, x.cuda(), dYc, Ac, Bc, r, s, dX2, 0, dA2, dB2, ws, U=U)
-    assert torch.equal(dX, dX2)
+    if r <= 16 and M > 16:
+        assert torch.equal(dX, dX2)
+    else:
+        e = N * 2.0**-24 * absv
+        apart = s * (2.0**-7 * (np.abs(g @ b64) + e) + 2 * e) @ np.abs(_f64(A))
+        assert (np.abs(_f64(dX) - _f64(dX2)) <= apart + 2.0**-7 * np.abs(_f64(dX)) + 1e-30).all()
     if saved_u:  # the bf16 path splits U in two parts
         assert (dB[:N] - dB2).norm() <= 4e-6 * dB2.norm()
 
