@@ -406,7 +406,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           x, first * kCsTok, c0, kCsTok * C, n, smem, smem + kTcStages * kCsStage + kTcBarriers, bars, status,
           [&](int i, int row, int col) { return i * kCsTok + row < rows && col < cols; });
     }
-    pdl_wait_prior();  // an overlapped launch ends after the kernel before it
     if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status)) {
       tc_fence_after();
       const int quad = warp & 3, h = (warp >> 2) & 1;  // TMEM lanes 32 quad .. + 31 of column tile h
@@ -427,6 +426,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   tc_teardown(tmem, kCsTmemCols);
+  pdl_wait_prior();  // an overlapped launch ends after the kernel before it
 }
 
 // dst(j, k) = scale sum_z part[z][j][k]; part has r16 = 16 ceil(r / 16) rows
@@ -511,7 +511,7 @@ size_t act8_colsum_partial_bytes(int64_t M, int64_t C) {
   return static_cast<size_t>(cs_splits(M, C)) * kRankPad * static_cast<size_t>(C) * sizeof(float);
 }
 
-cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, int* status,
+cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, bool overlap_first, int* status,
                                 cudaStream_t stream) {
   const int rt = (r + 15) / 16;
   ColsumReduceJob reduce[2];
@@ -519,7 +519,7 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
   for (int i = 0; i < count; ++i) {
     const ColsumJob& job = jobs[i];
     const Act8View& x = job.x;
-    const bool dense = x.format == kAct8Dense, overlap = i > 0;
+    const bool dense = x.format == kAct8Dense, overlap = i > 0 || overlap_first;
     const uint16_t* parts[kCsParts] = {job.hi, job.lo, job.lo2};
     CUtensorMap maps[4];  // X (plain bf16 only; else any valid map) and the parts of V
     for (int q = 0; q < kCsParts; ++q)
@@ -630,7 +630,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           x, m0, first * kRsCols, kRsCols, n, smem, smem + kTcStages * kRsStage + kTcBarriers, bars, status,
           [&](int i, int row, int col) { return row < rows && i * kRsCols + col < cols; });
     }
-    pdl_wait_prior();  // an overlapped launch ends after the kernel before it
     const int quad = warp & 3, j0 = warp / 4 * 16;  // TMEM lanes (tokens) 32 quad .. + 31, 16 j
     if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status) && j0 < r16) {
       tc_fence_after();
@@ -655,6 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   tc_teardown(tmem, kRsTmemCols);
+  pdl_wait_prior();  // an overlapped launch ends after the kernel before it
 }
 
 namespace {

@@ -1004,7 +1004,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
       const ColsumJob jobs[2] = {db_job, da_job};
       da_done = dA != nullptr;
       Timed tm(kFamSide, s, da_done ? 3 : 2);
-      e = launch_act8_colsums(jobs, da_done ? 2 : 1, r, scale, status, s);
+      e = launch_act8_colsums(jobs, da_done ? 2 : 1, r, scale, false, status, s);
       if (e != cudaSuccess) return from_cuda(e);
     } else if (dB != nullptr) {  // dB = s dY^T U
       Timed tm(kFamSide, s, 2);
@@ -1050,8 +1050,8 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   if (dA != nullptr && !da_done) {  // dA = s V^T X
     {
       Timed tm(kFamSide, s, 2);
-      if (x8 != nullptr)
-        e = launch_act8_colsums(&da_job, 1, r, scale, status, s);
+      if (x8 != nullptr)  // beside the dX GEMM, on the SMs that it leaves
+        e = launch_act8_colsums(&da_job, 1, r, scale, dX != nullptr, status, s);
       else
         e = launch_colsum(X, M, K, at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), r, scale,
                           at<float>(ws, lay.part), dA, true, status, s);

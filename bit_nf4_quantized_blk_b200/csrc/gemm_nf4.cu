@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmP,
                     const __grid_constant__ CUtensorMap tmS, const __grid_constant__ Nf4GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  pdl_launch_dependents();  // a kernel that does not read D may use the SMs that are left
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * A_STAGE;

@@ -284,7 +284,8 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 // [r][cols] (dst_rc) or [cols][r].  `part` is scratch of
 // act8_colsum_partial_bytes(rows, cols), enough for every rank and format.
 // One or two jobs: the second product starts where the first leaves room, and
-// one reduction ends both.
+// one reduction ends both.  `overlap_first`: so may the first one beside the
+// previous kernel of the stream, which writes nothing that it reads.
 struct ColsumJob {
   Act8View x;
   const uint16_t *hi, *lo, *lo2;
@@ -293,7 +294,7 @@ struct ColsumJob {
   bool dst_rc;
 };
 size_t act8_colsum_partial_bytes(int64_t M, int64_t C);
-cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, int* status,
+cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, bool overlap_first, int* status,
                                 cudaStream_t stream);
 // part[z][m][j] = sum over the columns k of split z of X^[m][k] W(j, k): W is
 // [r][cols] for a checkpoint, [cols][r] of pitch ldw for plain bf16 values (both
