@@ -229,18 +229,20 @@ def test_nan_stays_in_its_block():
     assert nan[:, 128:192].all() and not nan[:, :128].any() and not nan[:, 192:].any()
 
 
-def test_captured_and_on_another_stream():
+@pytest.mark.parametrize("r, with_dx", [(16, False), (40, False), (8, True), (40, True)])
+def test_captured_and_on_another_stream(r, with_dx):
     """A captured backward replays to the eager result, on a stream of its own, with new inputs in place."""
-    M, N, K, r = 200, 128, 512, 16
+    M, N, K = 200, 128, 512
     W, A, B, dY, x = _linear(M, N, K, r, 21)
     w, ws = gpu_quantize(W), workspace(M, N, K, r)
     a = binding.Act8.empty(M, K)
     xc, dYc, Ac, Bc = x.cuda(), dY.cuda(), A.cuda(), B.cuda()
     dA, dB = torch.zeros((r, K), device="cuda"), torch.zeros((N, r), device="cuda")
+    dX = torch.empty((M, K), dtype=torch.bfloat16, device="cuda") if with_dx else None
 
     def step():
         binding.qlora_act8_quantize(xc, a)
-        binding.qlora_linear_bwd_act8(w, a, dYc, Ac, Bc, r, 1.0, None, 0, dA, dB, ws)
+        binding.qlora_linear_bwd_act8(w, a, dYc, Ac, Bc, r, 1.0, dX, 0, dA, dB, ws)
 
     step()
     torch.cuda.synchronize()
@@ -260,3 +262,32 @@ def test_captured_and_on_another_stream():
         step()
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(dA, want[0]) and torch.equal(dB, want[1])
+
+
+@pytest.mark.parametrize("r", [8, 24, 64])
+def test_calls_in_a_row_share_a_workspace(r):
+    """Two problems in turn on one workspace, nothing waited for in between: each call's kernels overlap, the calls do
+    not."""
+    M, N, K = 1300, 264, 1088
+    problems = []
+    for seed in (1, 2):
+        W, A, B, dY, x = _linear(M, N, K, r, seed)
+        w, a = gpu_quantize(W), _checkpoint(x, list(FORMATS)[seed - 1])
+        problems.append((w, a, dY.cuda(), A.cuda(), B.cuda()))
+    ws = workspace(M, N, K, r)
+
+    def call(problem):
+        w, a, dY, A, B = problem
+        out = (torch.empty((M, K), dtype=torch.bfloat16, device="cuda"), torch.empty((r, K), device="cuda"),
+               torch.empty((N, r), device="cuda"))
+        binding.qlora_linear_bwd_act8(w, a, dY, A, B, r, 1.0, out[0], 0, out[1], out[2], ws)
+        return out
+
+    want = []
+    for problem in problems:
+        want.append(call(problem))
+        torch.cuda.synchronize()
+    got = [call(problems[i % 2]) for i in range(24)]
+    assert binding.qlora_workspace_status(ws) == 0
+    for i, out in enumerate(got):
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i % 2])), i
