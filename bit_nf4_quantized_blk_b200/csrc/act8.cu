@@ -18,6 +18,8 @@
 //  act8_rowsum_kernel      part[z][m][j] = sum over the columns of split z of
 //                          X^[m][k] A[j][k] (U), or of dY[m][k] B[k][j] (V).
 // Deterministic: every sum runs in a fixed order; no atomics.
+#include <algorithm>
+
 #include "act8.cuh"
 #include "kernels.cuh"
 
@@ -129,6 +131,32 @@ constexpr int kTcStages = 3;      // tiles, and code slots, in flight
 constexpr int kTcPasses = 2;      // runs of 16 codes per thread and step
 constexpr int kTcSlot = kTcPasses * kTcDecoders * 16;
 constexpr int kTcBarriers = 256;
+
+// The CTAs of one or two products: `tiles` independent ones, each with `splits`
+// CTAs that share its `steps`.  `splits` enters as what one wave of a CTA per SM
+// (148) would hold of that product alone.
+struct TcWork {
+  int64_t tiles, steps;
+  bool dense;
+  int splits;
+};
+
+// Two products share one wave where that takes no longer than one after the
+// other: nothing then waits for the first to end, and fewer splits leave fewer
+// partials.  In units of half a microsecond a step of plain bf16 takes 1, one
+// with decoding 2, and a second wave's start 4.  (1999 tokens, 2048 x 8192,
+// rank 64: U and V 18 us one after the other, dB and dA 20.)
+void tc_share_wave(TcWork& a, TcWork& b) {
+  auto time = [](const TcWork& w, int64_t splits) { return (w.steps + splits - 1) / splits * (w.dense ? 1 : 2); };
+  int64_t best = time(a, a.splits) + time(b, b.splits) + 4;
+  const TcWork a0 = a, b0 = b;
+  for (int64_t s = 1; s <= a0.splits; ++s) {
+    const int64_t left = (148 - a0.tiles * s) / b0.tiles, sb = left < b0.splits ? left : b0.splits;
+    if (a0.tiles * s >= 148 || sb < 1) break;
+    const int64_t ta = time(a0, s), tb = time(b0, sb), t = ta > tb ? ta : tb;
+    if (t < best) best = t, a.splits = static_cast<int>(s), b.splits = static_cast<int>(sb);
+  }
+}
 
 struct TcBarriers {
   uint64_t x_full[kTcStages];  // decoded: one arrival per decoder warp
@@ -341,12 +369,10 @@ constexpr int kCsStage = kCsXTile + kCsParts * kCsBox;
 constexpr int kCsN = kCsParts * kRankPad;           // MMA N
 constexpr uint32_t kCsTmemCols = 512;               // two tiles of kCsN, in a power of two
 
-// Splits of the tokens: one wave of one CTA per SM on a 148-SM B200.
-int cs_splits(int64_t M, int64_t C) {
-  const int64_t cols = (C + kCsCols - 1) / kCsCols, steps = (M + kCsTok - 1) / kCsTok;
-  int64_t s = 148 / cols;
-  if (s > steps) s = steps;
-  return static_cast<int>(s < 1 ? 1 : s);
+TcWork cs_work(int64_t M, int64_t C, bool dense) {
+  TcWork w{(C + kCsCols - 1) / kCsCols, (M + kCsTok - 1) / kCsTok, dense, 0};
+  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(148 / w.tiles, w.steps)));
+  return w;
 }
 
 }  // namespace
@@ -508,7 +534,7 @@ cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4]
 }  // namespace
 
 size_t act8_colsum_partial_bytes(int64_t M, int64_t C) {
-  return static_cast<size_t>(cs_splits(M, C)) * kRankPad * static_cast<size_t>(C) * sizeof(float);
+  return static_cast<size_t>(cs_work(M, C, true).splits) * kRankPad * static_cast<size_t>(C) * sizeof(float);
 }
 
 cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, bool overlap_first, int* status,
@@ -516,6 +542,9 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
   const int rt = (r + 15) / 16;
   ColsumReduceJob reduce[2];
   unsigned blocks[2] = {0, 0};
+  TcWork work[2];
+  for (int i = 0; i < count; ++i) work[i] = cs_work(jobs[i].x.rows, jobs[i].x.cols, jobs[i].x.format == kAct8Dense);
+  if (count == 2) tc_share_wave(work[0], work[1]);
   for (int i = 0; i < count; ++i) {
     const ColsumJob& job = jobs[i];
     const Act8View& x = job.x;
@@ -526,7 +555,7 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
       if (!encode_tensor_map_2d(&maps[1 + q], parts[q], x.rows, kRankPad, kCsTok, 64)) return cudaErrorInvalidValue;
     maps[0] = maps[1];
     if (dense && !encode_tensor_map_2d(&maps[0], x.codes, x.rows, x.cols, kCsTok, 64)) return cudaErrorInvalidValue;
-    const int splits = cs_splits(x.rows, x.cols);
+    const int splits = work[i].splits;
     const cudaError_t e =
         dense ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, job.part, overlap, status, stream)
         : x.format == kAct8Int8
@@ -561,13 +590,11 @@ constexpr int kRsStage = kRsXTile + kRsCols / 64 * kRsWBox;
 constexpr int kRsSums = 4;                  // accumulators: the tensor core truncates, so its chains are kept short
 constexpr uint32_t kRsTmemCols = kRsSums * kRankPad;
 
-int rs_splits(int64_t M, int64_t K) {
-  const int64_t tiles = (M + kRsTok - 1) / kRsTok, steps = (K + kRsCols - 1) / kRsCols;
-  int64_t s = 148 / tiles;  // one wave of a CTA per SM
-  if (s > steps) s = steps;
+TcWork rs_work(int64_t M, int64_t K, bool dense) {
+  TcWork w{(M + kRsTok - 1) / kRsTok, (K + kRsCols - 1) / kRsCols, dense, 0};
   const int64_t room = skinny_splits(M, K);  // what the workspace's partials are sized for
-  if (s > room) s = room;
-  return static_cast<int>(s < 1 ? 1 : s);
+  w.splits = static_cast<int>(std::max<int64_t>(1, std::min({148 / w.tiles, w.steps, room})));
+  return w;
 }
 
 }  // namespace
@@ -681,20 +708,30 @@ cudaError_t launch_rowsum_format(const Act8View& x, const CUtensorMap& tx, const
 
 }  // namespace
 
-cudaError_t launch_act8_rowsum(const Act8View& x, const uint16_t* W, int64_t ldw, int r, float* part, int* splits,
-                               bool overlap, int* status, cudaStream_t stream) {
-  *splits = rs_splits(x.rows, x.cols);
+cudaError_t launch_act8_rowsums(RowsumJob* jobs, int count, int r, int* status, cudaStream_t stream) {
   const int r16 = (r + 15) / 16 * 16;
-  CUtensorMap tx, tw;
-  if (x.format == kAct8Dense) {
-    if (!encode_tensor_map_2d(&tx, x.codes, x.rows, x.cols, kRsTok, 64)) return cudaErrorInvalidValue;
-    if (!encode_tensor_map_2d(&tw, W, x.cols, r, 64, kRankPad, true, ldw)) return cudaErrorInvalidValue;
-    return launch_rowsum_format<kAct8Dense>(x, tx, tw, r16, *splits, part, overlap, status, stream);
+  TcWork work[2];
+  for (int i = 0; i < count; ++i) work[i] = rs_work(jobs[i].x.rows, jobs[i].x.cols, jobs[i].x.format == kAct8Dense);
+  if (count == 2) tc_share_wave(work[0], work[1]);
+  for (int i = 0; i < count; ++i) {
+    RowsumJob& job = jobs[i];
+    const Act8View& x = job.x;
+    const bool dense = x.format == kAct8Dense, overlap = i > 0;
+    job.splits = work[i].splits;
+    CUtensorMap tx, tw;
+    if (dense ? !encode_tensor_map_2d(&tw, job.W, x.cols, r, 64, kRankPad, true, job.ldw)
+              : !encode_tensor_map_2d(&tw, job.W, r, x.cols, kRankPad, 64))
+      return cudaErrorInvalidValue;
+    tx = tw;
+    if (dense && !encode_tensor_map_2d(&tx, x.codes, x.rows, x.cols, kRsTok, 64)) return cudaErrorInvalidValue;
+    const cudaError_t e =
+        dense ? launch_rowsum_format<kAct8Dense>(x, tx, tw, r16, job.splits, job.part, overlap, status, stream)
+        : x.format == kAct8Int8
+            ? launch_rowsum_format<kAct8Int8>(x, tx, tw, r16, job.splits, job.part, overlap, status, stream)
+            : launch_rowsum_format<kAct8E4m3>(x, tx, tw, r16, job.splits, job.part, overlap, status, stream);
+    if (e != cudaSuccess) return e;
   }
-  if (!encode_tensor_map_2d(&tw, W, r, x.cols, kRankPad, 64)) return cudaErrorInvalidValue;
-  return x.format == kAct8Int8
-             ? launch_rowsum_format<kAct8Int8>(x, tw, tw, r16, *splits, part, overlap, status, stream)
-             : launch_rowsum_format<kAct8E4m3>(x, tw, tw, r16, *splits, part, overlap, status, stream);
+  return cudaSuccess;
 }
 
 }  // namespace qnf4

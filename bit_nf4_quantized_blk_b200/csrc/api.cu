@@ -928,6 +928,17 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   uo.olo = at<uint16_t>(ws, lay.ulo);
   uo.olo2 = ulo2;
   uo.scale = 1.0f;
+  // The products from a checkpoint.
+  RowsumJob u_job{}, v_job{};
+  ColsumJob da_job{}, db_job{};
+  if (x8 != nullptr) {
+    u_job = RowsumJob{view_of(x8), A, K, at<float>(ws, lay.part), 0};
+    v_job = RowsumJob{dense_view(dY, M, N), Bk, ldbk, at<float>(ws, lay.skpart), 0};
+    da_job = ColsumJob{view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, at<float>(ws, lay.part),
+                       dA, true};
+    db_job = ColsumJob{dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2,
+                       at<float>(ws, lay.dbpart), dB, false};
+  }
   // U = X A^T in its bf16 parts (from the saved fp32 U, or recomputed).
   auto u_hilo = [&]() -> cudaError_t {
     if (U != nullptr) {
@@ -936,21 +947,12 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     }
     Timed tm(kFamSide, s, 2);
     if (x8 != nullptr) {
-      SkinnyJob job{at<float>(ws, lay.part), 0, uo};
-      const cudaError_t err = launch_act8_rowsum(view_of(x8), A, K, r, at<float>(ws, lay.part), &job.splits, false,
-                                                 status, s);
-      return err != cudaSuccess ? err : launch_skinny_finalize(&job, 1, M, r, s);
+      e = launch_act8_rowsums(&u_job, 1, r, status, s);
+      const SkinnyJob job{u_job.part, u_job.splits, uo};
+      return e != cudaSuccess ? e : launch_skinny_finalize(&job, 1, M, r, s);
     }
     return launch_skinny(X, M, K, A, true, r, 0, at<float>(ws, lay.skpart), uo, status, s);
   };
-  // The column sums from a checkpoint.
-  ColsumJob da_job{}, db_job{};
-  if (x8 != nullptr) {
-    da_job = ColsumJob{view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, at<float>(ws, lay.part),
-                       dA, true};
-    db_job = ColsumJob{dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2,
-                       at<float>(ws, lay.dbpart), dB, false};
-  }
   bool da_done = false;
   BlockScalesJob bs{};  // the dX GEMM's block scales, when a kernel before it carries them
   if (dB != nullptr && r <= kVdbMaxRank && M > kGemvMaxM) {
@@ -982,17 +984,15 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     if (u_done) {
       // U too: V's product runs beside U's, and one reduction ends both.
       Timed tm(kFamSide, s, 3);
-      SkinnyJob jobs[2] = {{at<float>(ws, lay.part), 0, uo}, {at<float>(ws, lay.skpart), 0, vo}};
-      e = launch_act8_rowsum(view_of(x8), A, K, r, at<float>(ws, lay.part), &jobs[0].splits, false, status, s);
-      if (e == cudaSuccess)
-        e = launch_act8_rowsum(dense_view(dY, M, N), Bk, ldbk, r, at<float>(ws, lay.skpart), &jobs[1].splits, true, status,
-                               s);
+      RowsumJob products[2] = {u_job, v_job};
+      e = launch_act8_rowsums(products, 2, r, status, s);
+      const SkinnyJob jobs[2] = {{u_job.part, products[0].splits, uo}, {v_job.part, products[1].splits, vo}};
       if (e == cudaSuccess) e = launch_skinny_finalize(jobs, 2, M, r, s);
     } else {
       Timed tm(kFamSide, s, 2);
       if (x8 != nullptr) {
-        SkinnyJob job{at<float>(ws, lay.skpart), 0, vo};
-        e = launch_act8_rowsum(dense_view(dY, M, N), Bk, ldbk, r, at<float>(ws, lay.skpart), &job.splits, false, status, s);
+        e = launch_act8_rowsums(&v_job, 1, r, status, s);
+        const SkinnyJob job{v_job.part, v_job.splits, vo};
         if (e == cudaSuccess) e = launch_skinny_finalize(&job, 1, M, r, s);
       } else {
         e = launch_skinny(dY, M, N, Bk, false, r, ldbk, at<float>(ws, lay.skpart), vo, status, s);

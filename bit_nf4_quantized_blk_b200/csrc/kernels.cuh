@@ -298,12 +298,17 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
                                 cudaStream_t stream);
 // part[z][m][j] = sum over the columns k of split z of X^[m][k] W(j, k): W is
 // [r][cols] for a checkpoint, [cols][r] of pitch ldw for plain bf16 values (both
-// 16-byte aligned rows); `part` as for launch_skinny, reduced by
-// launch_skinny_finalize.  `overlap`: may run beside the previous kernel of the
-// stream, which writes nothing that this one reads (it ends after that kernel in
-// any case).
-cudaError_t launch_act8_rowsum(const Act8View& x, const uint16_t* W, int64_t ldw, int r, float* part, int* splits,
-                               bool overlap, int* status, cudaStream_t stream);
+// 16-byte aligned rows); `part` as for launch_skinny, to be reduced by
+// launch_skinny_finalize over the `splits` that the launch chooses.  One or two
+// jobs, the second beside the first.
+struct RowsumJob {
+  Act8View x;
+  const uint16_t* W;
+  int64_t ldw;
+  float* part;
+  int splits;
+};
+cudaError_t launch_act8_rowsums(RowsumJob* jobs, int count, int r, int* status, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Residual sum between two norms (residual_norm.cu)
