@@ -206,6 +206,7 @@ __device__ __forceinline__ void tc_teardown(uint32_t tmem, uint32_t columns) {
 }
 
 __device__ __forceinline__ bool tc_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, status);
   ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -264,30 +265,35 @@ __device__ __forceinline__ void tc_issue(TcBarriers* bars, int n, int* status, M
 
 // The decoders: n tiles of kRows rows x 16 kSegs columns, the first one's
 // corner at (row0, col0) and `advance` elements from one to the next, as
-// [box of 64 columns][row][64 bf16] at the start of each stage.  in(i, row,
-// col): whether a run of 16 at (row, col) of tile i exists; others are zero.
-template <int kFormat, int kSegs, int kRows, int kStage, typename In>
+// [box of 64 columns][row][64 bf16] at the start of each stage.  last(row, col):
+// the first tile in which the run of 16 at (row, col) does not exist; zeros
+// stand there.
+template <int kFormat, int kSegs, int kRows, int kStage, typename Last>
 __device__ __forceinline__ bool tc_decode(const Act8View& x, int64_t row0, int64_t col0, int64_t advance, int n,
-                                          uint8_t* smem, uint8_t* slots, TcBarriers* bars, int* status, In&& in) {
+                                          uint8_t* smem, uint8_t* slots, TcBarriers* bars, int* status, Last&& last) {
   constexpr int kPassRows = kTcDecoders / kSegs;
   static_assert(kPassRows * kTcPasses == kRows && kPassRows % 8 == 0, "whole passes, one swizzle key for all of them");
   const int seg = threadIdx.x % kSegs, tok = threadIdx.x / kSegs;
   const int64_t C = x.cols, at = (row0 + tok) * C + col0 + seg * 16;
   uint8_t* const slot = slots + threadIdx.x * 16;
-  auto fetch = [&](int i, int sl) {
-    const uint8_t* src = x.codes + at + i * advance;
+  int end[kTcPasses];
 #pragma unroll
-    for (int q = 0; q < kTcPasses; ++q) {
-      const bool ok = i < n && in(i, tok + q * kPassRows, seg * 16);
-      cp_async_16(slot + sl * kTcSlot + q * (kTcDecoders * 16), ok ? src + q * (kPassRows * C) : x.codes, ok);
-    }
-    cp_async_commit();
-  };
-  auto load_steps = [&](int i, uint32_t (&s)[kTcPasses]) {
-    const uint16_t* src = x.step + (at + i * advance) / kBlock;
+  for (int q = 0; q < kTcPasses; ++q) end[q] = min(n, last(tok + q * kPassRows, seg * 16));
+  // Tile by tile in turn: running pointers.
+  const uint8_t* code = x.codes + at;
+  const uint16_t* step = x.step + at / kBlock;
+  const int64_t code_pass = kPassRows * C, step_pass = code_pass / kBlock, step_advance = advance / kBlock;
+  auto fetch = [&](int i, int sl) {
 #pragma unroll
     for (int q = 0; q < kTcPasses; ++q)
-      s[q] = i < n && in(i, tok + q * kPassRows, seg * 16) ? __ldg(src + q * (kPassRows * C / kBlock)) : 0u;
+      cp_async_16(slot + sl * kTcSlot + q * (kTcDecoders * 16), i < end[q] ? code + q * code_pass : x.codes, i < end[q]);
+    cp_async_commit();
+    code += advance;
+  };
+  auto load_steps = [&](int i, uint32_t (&s)[kTcPasses]) {
+#pragma unroll
+    for (int q = 0; q < kTcPasses; ++q) s[q] = i < end[q] ? __ldg(step + q * step_pass) : 0u;
+    step += step_advance;
   };
   // Odd boxes take their second eight columns first, so that the boxes of a
   // store meet no bank twice.
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int cols = static_cast<int>(min(C - c0, static_cast<int64_t>(kCsCols)));
       ok = tc_decode<kFormat, kCsCols / 16, kCsTok, kCsStage>(
           x, first * kCsTok, c0, kCsTok * C, n, smem, smem + kTcStages * kCsStage + kTcBarriers, bars, status,
-          [&](int i, int row, int col) { return i * kCsTok + row < rows && col < cols; });
+          [&](int row, int col) { return col < cols ? (rows - row + kCsTok - 1) / kCsTok : 0; });
     }
     if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status)) {
       tc_fence_after();
@@ -655,7 +661,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int cols = static_cast<int>(min(K - first * kRsCols, static_cast<int64_t>(n) * kRsCols));
       ok = tc_decode<kFormat, kRsCols / 16, kRsTok, kRsStage>(
           x, m0, first * kRsCols, kRsCols, n, smem, smem + kTcStages * kRsStage + kTcBarriers, bars, status,
-          [&](int i, int row, int col) { return row < rows && i * kRsCols + col < cols; });
+          [&](int row, int col) { return row < rows ? (cols - col + kRsCols - 1) / kRsCols : 0; });
     }
     const int quad = warp & 3, j0 = warp / 4 * 16;  // TMEM lanes (tokens) 32 quad .. + 31, 16 j
     if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status) && j0 < r16) {
