@@ -144,8 +144,8 @@ struct TcWork {
 // Two products share one wave where that takes no longer than one after the
 // other: nothing then waits for the first to end, and fewer splits leave fewer
 // partials.  In units of half a microsecond a step of plain bf16 takes 1, one
-// with decoding 2, and a second wave's start 4.  (1999 tokens, 2048 x 8192,
-// rank 64: U and V 18 us one after the other, dB and dA 20.)
+// with decoding 2, and a second wave's start 4.  (Backward of 1999 tokens, 2048 x
+// 8192, rank 64: 50.5 us with both pairs in turn, 38.5 so.)
 void tc_share_wave(TcWork& a, TcWork& b) {
   auto time = [](const TcWork& w, int64_t splits) { return (w.steps + splits - 1) / splits * (w.dense ? 1 : 2); };
   int64_t best = time(a, a.splits) + time(b, b.splits) + 4;
@@ -360,9 +360,10 @@ __device__ __forceinline__ bool tc_decode(const Act8View& x, int64_t row0, int64
 // way.  In the epilogue a lane is a column, so each j leaves as 128 contiguous
 // bytes per warp.
 //
-// The decoders' instructions bound it (about 1,500 cycles per step, the MMAs
-// take 640), and some 6 us of launch, first loads and epilogue: 14.8 us at
-// 1999 x 8192 and rank 64 (16.8 MB of codes), 7.4 us for dY at 1999 x 2048.
+// Shared memory bounds it: a step's MMAs read 80 KB, its codes and decoded tile
+// take another 100 KB (about 1,500 cycles a step; 900 for plain bf16), and some
+// 6 us go to the first loads and the epilogue.  14.8 us at 1999 x 8192 and rank
+// 64 (16.8 MB of codes), 7.4 us for dY at 1999 x 2048, each alone on the GPU.
 // Warp-level MMAs from registers, the same sums: 29.9 and 12 us.
 namespace {
 
@@ -387,10 +388,10 @@ template <int kFormat>
 __global__ void __launch_bounds__(kTcThreads, 1)
     act8_colsum_kernel(Act8View x, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmHi,
                        const __grid_constant__ CUtensorMap tmLo, const __grid_constant__ CUtensorMap tmLo2, int r16,
-                       int splits, float* __restrict__ part, int* status) {
+                       int splits, float* __restrict__ part, bool after, int* status) {
   constexpr bool kDense = kFormat == kAct8Dense;
   extern __shared__ uint8_t smem_raw[];
-  pdl_launch_dependents();
+  if (!after) pdl_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TcBarriers* bars = reinterpret_cast<TcBarriers*>(smem + kTcStages * kCsStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -402,7 +403,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = tc_setup(bars, kCsTmemCols);
 
   if (warp == kTcWarps) {
-    if (lane == 0)
+    if (lane == 0) {
+      if (after) {  // V is the previous kernel's; what overlaps this one may read it too
+        pdl_wait_prior();
+        pdl_launch_dependents();
+      }
       tc_produce(smem, kCsStage, bars, n, kDense ? kCsStage : kCsParts * kCsBox, status,
                  [&](uint8_t* st, uint64_t* bar, int i) {
                    const int m = static_cast<int>((first + i) * kCsTok);
@@ -413,6 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                    tma_load_2d(st + kCsXTile + kCsBox, &tmLo, bar, 0, m);
                    tma_load_2d(st + kCsXTile + 2 * kCsBox, &tmLo2, bar, 0, m);
                  });
+    }
   } else if (warp == kTcWarps + 1) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, kCsN, true) | (1u << 15);  // A and B MN-major
     // Groups of 64 columns (or of 64 j: one part) are a box apart, groups of
@@ -518,7 +524,7 @@ namespace {
 
 template <int kFormat>
 cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4], int r16, int splits, float* part,
-                                 bool overlap, int* status, cudaStream_t stream) {
+                                 bool after, int* status, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -529,12 +535,8 @@ cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4]
   });
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.cols + kCsCols - 1) / kCsCols), static_cast<unsigned>(splits));
-  if (overlap)
-    return launch_dependent(act8_colsum_kernel<kFormat>, grid, kTcThreads, tc_smem<kFormat>(kCsStage), stream, x, maps[0], maps[1],
-                            maps[2], maps[3], r16, splits, part, status);
-  act8_colsum_kernel<kFormat><<<grid, kTcThreads, tc_smem<kFormat>(kCsStage), stream>>>(x, maps[0], maps[1], maps[2], maps[3], r16,
-                                                                             splits, part, status);
-  return cudaGetLastError();
+  return launch_dependent(act8_colsum_kernel<kFormat>, grid, kTcThreads, tc_smem<kFormat>(kCsStage), stream, x, maps[0],
+                          maps[1], maps[2], maps[3], r16, splits, part, after, status);
 }
 
 }  // namespace
@@ -554,7 +556,7 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
   for (int i = 0; i < count; ++i) {
     const ColsumJob& job = jobs[i];
     const Act8View& x = job.x;
-    const bool dense = x.format == kAct8Dense, overlap = i > 0 || overlap_first;
+    const bool dense = x.format == kAct8Dense, after = i == 0 && !overlap_first;
     const uint16_t* parts[kCsParts] = {job.hi, job.lo, job.lo2};
     CUtensorMap maps[4];  // X (plain bf16 only; else any valid map) and the parts of V
     for (int q = 0; q < kCsParts; ++q)
@@ -563,10 +565,10 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
     if (dense && !encode_tensor_map_2d(&maps[0], x.codes, x.rows, x.cols, kCsTok, 64)) return cudaErrorInvalidValue;
     const int splits = work[i].splits;
     const cudaError_t e =
-        dense ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, job.part, overlap, status, stream)
+        dense ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, job.part, after, status, stream)
         : x.format == kAct8Int8
-            ? launch_colsum_format<kAct8Int8>(x, maps, 16 * rt, splits, job.part, overlap, status, stream)
-            : launch_colsum_format<kAct8E4m3>(x, maps, 16 * rt, splits, job.part, overlap, status, stream);
+            ? launch_colsum_format<kAct8Int8>(x, maps, 16 * rt, splits, job.part, after, status, stream)
+            : launch_colsum_format<kAct8E4m3>(x, maps, 16 * rt, splits, job.part, after, status, stream);
     if (e != cudaSuccess) return e;
     reduce[i] = ColsumReduceJob{job.part, x.cols, splits, job.dst, job.dst_rc ? 1 : 0};
     blocks[i] = static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols);

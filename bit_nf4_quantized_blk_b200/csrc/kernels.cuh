@@ -284,8 +284,9 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 // [r][cols] (dst_rc) or [cols][r].  `part` is scratch of
 // act8_colsum_partial_bytes(rows, cols), enough for every rank and format.
 // One or two jobs: the second product starts where the first leaves room, and
-// one reduction ends both.  `overlap_first`: so may the first one beside the
-// previous kernel of the stream, which writes nothing that it reads.
+// one reduction ends both.  The first one's launch overlaps the previous kernel
+// of the stream; `overlap_first`: so may its work, as that kernel writes nothing
+// that it reads.
 struct ColsumJob {
   Act8View x;
   const uint16_t *hi, *lo, *lo2;

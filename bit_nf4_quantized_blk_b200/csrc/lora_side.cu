@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(const __grid_constant_
 // blockIdx.y: the job.
 __global__ void skinny_finalize_kernel(const __grid_constant__ SkinnyJob job0, const __grid_constant__ SkinnyJob job1,
                                        int64_t M, int r) {
+  pdl_launch_dependents();
   pdl_wait_prior();
   const SkinnyJob& job = blockIdx.y == 0 ? job0 : job1;
   const SkinnyOut& out = job.out;
@@ -509,6 +510,7 @@ __global__ void vdb_finalize_kernel(const float* __restrict__ vpart, int ncb, co
                                     int ntb, int64_t M, int64_t N, int r, int r16, float scale,
                                     uint16_t* __restrict__ vs, uint16_t* __restrict__ vhi, uint16_t* __restrict__ vlo,
                                     uint16_t* __restrict__ vlo2, float* __restrict__ dB, BlockScalesJob bs) {
+  pdl_launch_dependents();
   pdl_wait_prior();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t nv = M * (kRankPad / 2);
