@@ -1164,7 +1164,8 @@ extern "C" qlora_status qlora_residual_norm_fwd(const void* h, const uint16_t* y
 
 extern "C" size_t qlora_residual_norm_ws_bytes(int64_t M, int64_t D) {
   if (check_norm_shape(M, D, 0) != QLORA_OK) return 0;
-  return kWsHeader + 2 * static_cast<size_t>(residual_norm_bwd_ctas(M, D)) * static_cast<size_t>(D) * sizeof(float);
+  const int ctas = std::max(residual_norm_bwd_ctas(M, D, false), residual_norm_bwd_ctas(M, D, true));
+  return kWsHeader + 2 * static_cast<size_t>(ctas) * static_cast<size_t>(D) * sizeof(float);
 }
 
 extern "C" qlora_status qlora_residual_norm_bwd(const void* dh_out, const uint16_t* dx, const void* h_out,

@@ -351,10 +351,10 @@ struct ResidualNormBwd {
   float* dw_post;        // [D] each, may be null
   float* dgate;
   float* dw_pre;
-  float* part;           // [2][residual_norm_bwd_ctas(M, D)][D]
+  float* part;           // [2][residual_norm_bwd_ctas(M, D, fp32)][D]
 };
 
-int residual_norm_bwd_ctas(int64_t M, int64_t D);
+int residual_norm_bwd_ctas(int64_t M, int64_t D, bool res_fp32);
 cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cudaStream_t stream);
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cudaStream_t stream);
 

@@ -17,8 +17,8 @@
 // registers of its threads between the two reductions, and nothing is read
 // twice.  A thread holds NC groups of 8 consecutive values, TPR groups apart
 // (16-byte accesses, lanes side by side; 8 lanes hold one 64-value checkpoint
-// block).  Rows of up to 512 values take one warp (reductions by shuffles
-// alone), longer ones a CTA.  All arithmetic is fp32.  CTAs stay for many
+// block).  Rows of up to 512 values (256 of an fp32 stream) take one warp
+// (reductions by shuffles alone), longer ones a CTA.  All arithmetic is fp32.  CTAs stay for many
 // rows: while a row is computed, the next one's operands travel to shared
 // memory (cp.async), so the two reductions' waits do not stop the loads.
 //
@@ -515,41 +515,48 @@ __global__ void __launch_bounds__(1024) residual_norm_finish_kernel(ResidualNorm
 namespace {
 
 // Threads per row (TPR) and 8-value groups per thread (NC), by the row's length.
+// An fp32 stream has more bytes in flight per thread and runs better with one
+// group up to 4096 values (8192 x 4096: forward 92 us with two, 81 with one,
+// backward 139 and 137; 8192 x 2048: 51 and 45, 78 and 73; 4096 x 8192, where one
+// takes 1024 threads: backward 147 and 206).  bf16 rows run better with two
+// (8192 x 2048: backward 41 us, 45 with one).
 struct NormShape {
   int tpr, nc;
 };
 
-constexpr NormShape norm_shape(int64_t D) {
-  return D <= 256    ? NormShape{32, 1}
-         : D <= 512  ? NormShape{32, 2}
-         : D <= 1024 ? NormShape{64, 2}
-         : D <= 2048 ? NormShape{128, 2}
-         : D <= 4096 ? NormShape{256, 2}
-         : D <= 8192 ? NormShape{512, 2}
-                     : NormShape{1024, 2};
+constexpr NormShape norm_shape(int64_t D, bool fp32) {
+  const int nc = D <= 256 || (fp32 && D <= 4096) ? 1 : 2;
+  int tpr = 32;
+  while (tpr * nc * 8 < D) tpr *= 2;
+  return NormShape{tpr, nc};
 }
 
-template <typename F>
+template <typename TRes, typename F>
 cudaError_t with_shape(int64_t D, F&& f) {
   using std::integral_constant;
-  switch (norm_shape(D).tpr) {
+  constexpr bool kFp32 = sizeof(TRes) == 4;
+  constexpr int kMid = kFp32 ? 1 : 2;  // groups of the shapes in between
+  const NormShape shape = norm_shape(D, kFp32);
+  switch (shape.tpr) {
     case 32:
-      switch (norm_shape(D).nc) {
-        case 1: return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-        default: return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-      }
-    case 64: return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    case 128: return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
-    case 256: return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    case 512: return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+      if constexpr (!kFp32)
+        if (shape.nc == 2) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+      return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+    case 64: return f(integral_constant<int, 64>{}, integral_constant<int, kMid>{});
+    case 128: return f(integral_constant<int, 128>{}, integral_constant<int, kMid>{});
+    case 256: return f(integral_constant<int, 256>{}, integral_constant<int, kMid>{});
+    case 512:
+      if constexpr (kFp32)
+        if (shape.nc == 1) return f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+      return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
     default: return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   }
 }
 
 // CTAs of one wave on a 148-SM B200 with `threads` resident threads per SM,
 // or as many as the rows need.
-int64_t norm_ctas(int64_t M, int64_t D, int64_t resident) {
-  const int64_t tpr = norm_shape(D).tpr, rows = tpr == 32 ? kWarpRowCtas : 1;
+int64_t norm_ctas(int64_t M, int64_t D, bool fp32, int64_t resident) {
+  const int64_t tpr = norm_shape(D, fp32).tpr, rows = tpr == 32 ? kWarpRowCtas : 1;
   const int64_t threads = tpr * rows, want = (M + rows - 1) / rows;
   const int64_t most = 148 * (threads >= resident ? 1 : resident / threads);
   return want < most ? want : most;
@@ -569,37 +576,37 @@ cudaError_t launch_norm(Kernel kernel, DeviceOnce& configured, int ctas, int thr
 
 template <typename TRes>
 cudaError_t launch_fwd(const ResidualNormFwd& p, cudaStream_t stream) {
-  return with_shape(p.D, [&](auto tpr, auto nc) {
+  return with_shape<TRes>(p.D, [&](auto tpr, auto nc) {
     constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
     constexpr int smem =
         RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes + 2 * RowSlot<float, TPR, NC>::kBytes;
     static DeviceOnce configured;
-    const int ctas = static_cast<int>(norm_ctas(p.M, p.D, kFwdResident));
+    const int ctas = static_cast<int>(norm_ctas(p.M, p.D, sizeof(TRes) == 4, kFwdResident));
     return launch_norm(residual_norm_fwd_kernel<TRes, TPR, NC>, configured, ctas, kNormThreads<TPR>, smem, p, stream);
   });
 }
 
 template <typename TRes>
 cudaError_t launch_bwd(const ResidualNormBwd& p, cudaStream_t stream) {
-  return with_shape(p.D, [&](auto tpr, auto nc) {
+  return with_shape<TRes>(p.D, [&](auto tpr, auto nc) {
     constexpr int TPR = decltype(tpr)::value, NC = decltype(nc)::value;
     constexpr int smem = 2 * (RowSlot<TRes, TPR, NC>::kBytes + RowSlot<uint16_t, TPR, NC>::kBytes) +
                          (kStash<TPR> ? 2 * RowSlot<float, TPR, NC>::kBytes : 0);
     static DeviceOnce configured;
-    const int ctas = residual_norm_bwd_ctas(p.M, p.D);
+    const int ctas = residual_norm_bwd_ctas(p.M, p.D, sizeof(TRes) == 4);
     return launch_norm(residual_norm_bwd_kernel<TRes, TPR, NC>, configured, ctas, kNormThreads<TPR>, smem, p, stream);
   });
 }
 
 }  // namespace
 
-int residual_norm_bwd_ctas(int64_t M, int64_t D) {
+int residual_norm_bwd_ctas(int64_t M, int64_t D, bool res_fp32) {
   // Every CTA leaves a partial row of the column sums: with few rows, the same
   // number of CTAs on each SM and three or more rows for each keep those below
-  // the operands themselves (999 x 2048: 296 CTAs 16.4 us, 148 17.4, 249 18.4,
-  // 444 18.5, 499 20.5).
+  // the operands themselves (999 x 2048, 128 threads each: 296 CTAs 16.4 us, 148
+  // 17.4, 249 18.4, 444 18.5, 499 20.5).
   return static_cast<int>(
-      std::min<int64_t>(norm_ctas(M, D, kBwdResident), 148 * std::max<int64_t>(1, M / (148 * 3))));
+      std::min<int64_t>(norm_ctas(M, D, res_fp32, kBwdResident), 148 * std::max<int64_t>(1, M / (148 * 3))));
 }
 
 cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& p, int res_fp32, cudaStream_t stream) {
@@ -610,7 +617,7 @@ cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& p, int res_fp32, cud
   const cudaError_t e = res_fp32 ? launch_bwd<float>(p, stream) : launch_bwd<uint16_t>(p, stream);
   if (e != cudaSuccess || (!p.dw_pre && !p.dgate && !p.dw_post)) return e;
   return launch_dependent(residual_norm_finish_kernel, dim3(static_cast<unsigned>(p.D / 32), 2), 1024, 0, stream, p,
-                          residual_norm_bwd_ctas(p.M, p.D));
+                          residual_norm_bwd_ctas(p.M, p.D, res_fp32 != 0));
 }
 
 }  // namespace qnf4
