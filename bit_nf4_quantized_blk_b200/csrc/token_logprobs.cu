@@ -18,7 +18,9 @@
 // copies (cp.async into slots that it alone reads, so without barriers) across
 // the rows' ends: the next row arrives while this one is reduced.  With few
 // rows a cluster of up to 8 CTAs shares each row and joins over distributed
-// shared memory, still one launch without a workspace.
+// shared memory, still one launch without a workspace.  Measured, bf16: 4096 x
+// 50257 without alternatives 80 us (412 MB, 5.1 TB/s), with 5 of them 102 to 106,
+// with 20 112; 2048 x 131072 93, 102 and 108 us; one row of 131072 6 to 12 us.
 //
 // The k largest come from the same pass.  The k-th largest (or a little less)
 // of the threads' maxima is a bound that at least k logits reach, and only
@@ -30,7 +32,8 @@
 // logits sitting in a few threads), they are taken one by one.
 //
 // The gradient  dx_j = c (g (1[j = t] - p_j) - g_H p_j (log p_j + H)) is
-// elementwise from the saved m, log s and H: one read, one write.
+// elementwise from the saved m, log s and H: one read, one write; 2048 x 131072
+// in 186 us (1.07 GB, 5.8 TB/s).
 #include <algorithm>
 #include <type_traits>
 
