@@ -265,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmP,
                     const __grid_constant__ CUtensorMap tmS, const __grid_constant__ Nf4GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  pdl_launch_dependents();  // a kernel that does not read D may use the SMs that are left
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * A_STAGE;
@@ -319,6 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // both CTAs' barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait_prior();         // the reduction before it (the setup above overlaps that)
+  pdl_launch_dependents();  // a kernel that does not read D may use the SMs that are left
 
   if (warp == 0) {
     if (lane == 0) {
@@ -736,13 +737,16 @@ cudaError_t launch_gemm_nf4(const Nf4GemmArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // Each call launches a kernel of its own before this one, whose end it waits for.
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (bwd) return cudaLaunchKernelEx(&cfg, gemm_nf4_kernel<true>, tA, tA2, tB2, tP, tS, p);
   return cudaLaunchKernelEx(&cfg, gemm_nf4_kernel<false>, tA, tA2, tB2, tP, tS, p);
 }
