@@ -355,7 +355,9 @@ __device__ __forceinline__ bool tc_decode(const Act8View& x, int64_t row0, int64
 // rows of tokens go to shared memory as they are: A is the X^ tile, B the three
 // parts of V side by side (N = 192), so that A, whose reads bound the MMA at a
 // small N, is read once for all three.  Their sums stay apart in tensor memory
-// until the epilogue adds them.  A CTA takes 256 columns (two M = 128 tiles)
+// until the epilogue adds them, and those of V's first part are two, of every
+// other 16 tokens each: the tensor core truncates, and one chain over 1,000
+// tokens cost dB 1.2e-6 of its size.  A CTA takes 256 columns (two M = 128 tiles)
 // and a range of the tokens, 64 per step; it takes dY and U for dB the same
 // way.  In the epilogue a lane is a column, so each j leaves as 128 contiguous
 // bytes per warp.
@@ -374,7 +376,8 @@ constexpr int kCsBox = kCsTok * 128;                // [64 tokens][64 columns or
 constexpr int kCsXTile = kCsCols / 64 * kCsBox;
 constexpr int kCsStage = kCsXTile + kCsParts * kCsBox;
 constexpr int kCsN = kCsParts * kRankPad;           // MMA N
-constexpr uint32_t kCsTmemCols = 512;               // two tiles of kCsN, in a power of two
+constexpr int kCsSums = 4;                          // accumulators: hi, lo, lo2, hi
+constexpr uint32_t kCsTmemCols = 2 * kCsSums * kRankPad;
 
 TcWork cs_work(int64_t M, int64_t C, bool dense) {
   TcWork w{(C + kCsCols - 1) / kCsCols, (M + kCsTok - 1) / kCsTok, dense, 0};
@@ -420,7 +423,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                  });
     }
   } else if (warp == kTcWarps + 1) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, kCsN, true) | (1u << 15);  // A and B MN-major
+    constexpr uint32_t kMn = 1u << 15;  // A MN-major, as B
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kCsN, true) | kMn;
+    constexpr uint32_t idesc_hi = idesc_bf16_f32(128, kRankPad, true) | kMn;
+    constexpr uint32_t idesc_lo = idesc_bf16_f32(128, kCsN - kRankPad, true) | kMn;
     // Groups of 64 columns (or of 64 j: one part) are a box apart, groups of
     // 8 tokens 1 KB; a K = 16 step is 16 tokens = 2 KB.
     const uint64_t base = smem_desc_mn128(smem_u32(smem), kCsBox, 1024);
@@ -429,11 +435,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int kk = 0; kk < kCsTok / 16; ++kk)
-            tc_mma_bf16_ss(tmem + static_cast<uint32_t>(h * 256),
-                           base + static_cast<uint64_t>((s * kCsStage + h * 2 * kCsBox + kk * 2048) >> 4),
-                           base + static_cast<uint64_t>((s * kCsStage + kCsXTile + kk * 2048) >> 4), idesc,
-                           (i > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kCsTok / 16; ++kk) {
+            const uint32_t d = tmem + static_cast<uint32_t>(h * kCsSums * kRankPad);
+            const uint64_t a = base + static_cast<uint64_t>((s * kCsStage + h * 2 * kCsBox + kk * 2048) >> 4);
+            const uint64_t b = base + static_cast<uint64_t>((s * kCsStage + kCsXTile + kk * 2048) >> 4);
+            if (kk % 2 == 0) {  // hi, lo, lo2
+              tc_mma_bf16_ss(d, a, b, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+            } else {  // lo, lo2, and the other hi
+              tc_mma_bf16_ss(d + kRankPad, a, b + (kCsBox >> 4), idesc_lo, 1u);
+              tc_mma_bf16_ss(d + 3 * kRankPad, a, b, idesc_hi, (i > 0 || kk > 1) ? 1u : 0u);
+            }
+          }
       });
   } else {
     bool ok = true;
@@ -447,19 +459,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (ok && tc_warp_wait(&bars->done, 0, &bars->abort_flag, status)) {
       tc_fence_after();
       const int quad = warp & 3, h = (warp >> 2) & 1;  // TMEM lanes 32 quad .. + 31 of column tile h
-      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(h * 256);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(h * kCsSums * kRankPad);
       const int64_t k = c0 + h * 128 + quad * 32 + lane;
       for (int j0 = warp / 8 * 16; j0 < r16; j0 += kTcWarps / 8 * 16) {
-        uint32_t v[kCsParts][16];
+        uint32_t v[kCsSums][16];
 #pragma unroll
-        for (int i = 0; i < kCsParts; ++i) tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(i * kRankPad + j0), v[i]);
+        for (int i = 0; i < kCsSums; ++i) tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(i * kRankPad + j0), v[i]);
 #pragma unroll
-        for (int i = 0; i < kCsParts; ++i) tc_wait_ld(v[i]);
+        for (int i = 0; i < kCsSums; ++i) tc_wait_ld(v[i]);
         if (k >= C) continue;
         float* dst = part + (static_cast<int64_t>(z) * r16 + j0) * C + k;
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          dst[j * C] = __uint_as_float(v[0][j]) + (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+          dst[j * C] = (__uint_as_float(v[0][j]) + __uint_as_float(v[3][j])) +
+                       (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
       }
     }
   }
