@@ -133,8 +133,8 @@ constexpr int kTcSlot = kTcPasses * kTcDecoders * 16;
 constexpr int kTcBarriers = 256;
 
 // The CTAs of one or two products: `tiles` independent ones, each with `splits`
-// CTAs that share its `steps`.  `splits` enters as what one wave of a CTA per SM
-// (148) would hold of that product alone.
+// CTAs that share its `steps`.  `splits` enters as that product alone would have
+// it: whole waves of a CTA per SM (148).
 struct TcWork {
   int64_t tiles, steps;
   bool dense;
@@ -147,7 +147,9 @@ struct TcWork {
 // with decoding 2, and a second wave's start 4.  (Backward of 1999 tokens, 2048 x
 // 8192, rank 64: 50.5 us with both pairs in turn, 38.5 so.)
 void tc_share_wave(TcWork& a, TcWork& b) {
-  auto time = [](const TcWork& w, int64_t splits) { return (w.steps + splits - 1) / splits * (w.dense ? 1 : 2); };
+  auto time = [](const TcWork& w, int64_t splits) {
+    return (w.tiles * splits + 147) / 148 * ((w.steps + splits - 1) / splits) * (w.dense ? 1 : 2);
+  };
   int64_t best = time(a, a.splits) + time(b, b.splits) + 4;
   const TcWork a0 = a, b0 = b;
   for (int64_t s = 1; s <= a0.splits; ++s) {
@@ -383,7 +385,11 @@ constexpr uint32_t kCsTmemCols = 2 * kCsSums * kRankPad;
 
 TcWork cs_work(int64_t M, int64_t C, bool dense) {
   TcWork w{(C + kCsCols - 1) / kCsCols, (M + kCsTok - 1) / kCsTok, dense, 0};
-  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(148 / w.tiles, w.steps)));
+  // Whole waves, as many as keep a CTA at 24 steps (48 additions in a row: dA of
+  // 8192 tokens and 8192 columns is off by 1.0e-6 with 32 steps in one wave).
+  int64_t waves = (w.tiles + 147) / 148;
+  while (148 * waves / w.tiles < w.steps && (w.steps + 148 * waves / w.tiles - 1) / (148 * waves / w.tiles) > 24) ++waves;
+  w.splits = static_cast<int>(std::min<int64_t>(148 * waves / w.tiles, w.steps));
   return w;
 }
 

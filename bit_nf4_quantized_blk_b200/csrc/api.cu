@@ -379,13 +379,13 @@ LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
   l.bpad = take(static_cast<size_t>(N) * kRankPad * 2);
   const size_t p1 = colsum_partial_bytes(M, N), p2 = colsum_partial_bytes(M, K);
   const size_t s1 = skinny_partial_bytes(M, N), s2 = skinny_partial_bytes(M, K);
-  // From a checkpoint, U's partials and later dA's share `part`, while V's and dB's have their own.
+  // From a checkpoint, U's partials and later dA's share `part`.
   l.part = take(std::max({p1, p2, s2, act8_colsum_partial_bytes(M, K)}));
-  l.dbpart = take(act8_colsum_partial_bytes(M, N));
   l.skpart = take(s1 > s2 ? s1 : s2);
   // The tensor-core V / dB pass: its partials and the transposed B and U split.
   const bool vdb = M > kGemvMaxM;
-  l.vdbpart = take(vdb ? vdb_tc_partial_bytes(M, N) : 0);
+  l.vdbpart = take(std::max(vdb ? vdb_tc_partial_bytes(M, N) : 0, act8_colsum_partial_bytes(M, N)));
+  l.dbpart = l.vdbpart;  // dB's partials from a checkpoint: where the V / dB pass does not run
   l.bt = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(N) * 2 : 0);
   l.uht = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
   l.ult = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
