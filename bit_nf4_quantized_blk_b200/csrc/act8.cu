@@ -489,9 +489,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // dst(j, k) = scale sum_z part[z][j][k]; part has r16 = 16 ceil(r / 16) rows
-// per split.  A CTA takes 32 columns of 16 j: four columns of one j per
-// thread.  [cols][r] outputs leave through shared memory, 16 j side by side.
-// The CTAs of a second job follow the first's.
+// per split.  A CTA takes 32 columns of 16 j, four columns of one j per thread;
+// kGroups groups of threads take every kGroups-th split each and are joined in
+// order.  A narrow matrix has few CTAs and up to 148 splits: more than 8 of them
+// take four groups (backward of 5000 x 256 x 256, rank 40: 35 us with one group,
+// 27 with four; of 1999 x 2048 x 8192, which has up to 4 splits: 36.9 and 37.7).
+// [cols][r] outputs leave through shared memory, 16 j side by side.  The CTAs of a
+// second job follow the first's.
 constexpr int kCrCols = 32;
 
 struct ColsumReduceJob {
@@ -502,10 +506,12 @@ struct ColsumReduceJob {
   int dst_rc;
 };
 
-__global__ void __launch_bounds__(128)
+template <int kGroups>
+__global__ void __launch_bounds__(128 * kGroups)
     act8_colsum_reduce_kernel(const __grid_constant__ ColsumReduceJob job0, const __grid_constant__ ColsumReduceJob job1,
                               unsigned first, int r, float scale) {
   __shared__ float tile[kCrCols][17];
+  __shared__ float4 sums[kGroups][128];
   pdl_wait_prior();
   const ColsumReduceJob& job = blockIdx.x < first ? job0 : job1;
   const float* __restrict__ part = job.part;
@@ -513,14 +519,27 @@ __global__ void __launch_bounds__(128)
   const int64_t C = job.C;
   const int splits = job.splits, dst_rc = job.dst_rc;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x < first ? blockIdx.x : blockIdx.x - first) * kCrCols;
-  const int jj = threadIdx.x / (kCrCols / 4), cc = threadIdx.x % (kCrCols / 4) * 4, j = blockIdx.y * 16 + jj;
+  const int group = threadIdx.x / 128, t = threadIdx.x % 128;
+  const int jj = t / (kCrCols / 4), cc = t % (kCrCols / 4) * 4, j = blockIdx.y * 16 + jj;
   const int64_t slice = static_cast<int64_t>(gridDim.y) * 16 * C;
-  if (j < r && c0 + cc < C) {
+  const bool in = j < r && c0 + cc < C;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (in) {
     const float* src = part + j * C + c0 + cc;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-    for (int z = 0; z < splits; ++z) {
+    for (int z = group; z < splits; z += kGroups) {
       const float4 p = *reinterpret_cast<const float4*>(src + z * slice);
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+  }
+  if constexpr (kGroups > 1) {
+    sums[group][t] = s;
+    __syncthreads();
+  }
+  if (group == 0 && in) {
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+      const float4 p = sums[g][t];
       s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
     }
     const float v[4] = {scale * s.x, scale * s.y, scale * s.z, scale * s.w};
@@ -535,7 +554,7 @@ __global__ void __launch_bounds__(128)
   if (dst_rc) return;
   __syncthreads();
 #pragma unroll
-  for (int i = threadIdx.x; i < kCrCols * 16; i += 128) {
+  for (int i = threadIdx.x; i < kCrCols * 16; i += 128 * kGroups) {
     const int c = i / 16, q = i % 16;
     if (c0 + c < C && blockIdx.y * 16 + q < r) dst[(c0 + c) * r + blockIdx.y * 16 + q] = tile[c][q];
   }
@@ -595,8 +614,9 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
     blocks[i] = static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols);
   }
   const dim3 grid(blocks[0] + blocks[1], static_cast<unsigned>(rt));
-  return launch_dependent(act8_colsum_reduce_kernel, grid, 128, 0, stream, reduce[0], reduce[count - 1], blocks[0], r,
-                          scale);
+  const bool many = std::max(reduce[0].splits, reduce[count - 1].splits) > 8;
+  return launch_dependent(many ? act8_colsum_reduce_kernel<4> : act8_colsum_reduce_kernel<1>, grid, many ? 512 : 128, 0,
+                          stream, reduce[0], reduce[count - 1], blocks[0], r, scale);
 }
 
 // ---------------------------------------------------------------------------
