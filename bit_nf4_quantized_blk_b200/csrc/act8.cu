@@ -382,13 +382,16 @@ constexpr int kCsStage = kCsXTile + kCsParts * kCsBox;
 constexpr int kCsN = kCsParts * kRankPad;           // MMA N
 constexpr int kCsSums = 4;                          // accumulators: hi, lo, lo2, hi
 constexpr uint32_t kCsTmemCols = 2 * kCsSums * kRankPad;
+constexpr int64_t kCsSteps = 24;                    // most steps of a CTA, where there is room for the splits
 
 TcWork cs_work(int64_t M, int64_t C, bool dense) {
   TcWork w{(C + kCsCols - 1) / kCsCols, (M + kCsTok - 1) / kCsTok, dense, 0};
   // Whole waves, as many as keep a CTA at 24 steps (48 additions in a row: dA of
   // 8192 tokens and 8192 columns is off by 1.0e-6 with 32 steps in one wave).
   int64_t waves = (w.tiles + 147) / 148;
-  while (148 * waves / w.tiles < w.steps && (w.steps + 148 * waves / w.tiles - 1) / (148 * waves / w.tiles) > 24) ++waves;
+  while (148 * waves / w.tiles < w.steps &&
+         (w.steps + 148 * waves / w.tiles - 1) / (148 * waves / w.tiles) > kCsSteps)
+    ++waves;
   w.splits = static_cast<int>(std::min<int64_t>(148 * waves / w.tiles, w.steps));
   return w;
 }
@@ -581,8 +584,38 @@ cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4]
 
 }  // namespace
 
-size_t act8_colsum_partial_bytes(int64_t M, int64_t C) {
-  return static_cast<size_t>(cs_work(M, C, true).splits) * kRankPad * static_cast<size_t>(C) * sizeof(float);
+bool plan_act8_colsums(ColsumJob* jobs, int count, int r, float* pool, size_t room) {
+  TcWork work[2];
+  size_t split[2] = {0, 0};  // bytes of one
+  for (int i = 0; i < count; ++i) {
+    const Act8View& x = jobs[i].x;
+    work[i] = cs_work(x.rows, x.cols, x.format == kAct8Dense);
+    split[i] = static_cast<size_t>((r + 15) / 16 * 16) * static_cast<size_t>(x.cols) * sizeof(float);
+  }
+  if (count == 2) {
+    tc_share_wave(work[0], work[1]);
+    // Fewer splits where they take most room, while the chains stay short.
+    auto bytes = [&](int i) { return static_cast<size_t>(work[i].splits) * split[i]; };
+    auto spare = [&](int i) {
+      const int fewer = work[i].splits - 1;
+      return fewer > 0 && (work[i].steps + fewer - 1) / fewer <= kCsSteps;
+    };
+    while (bytes(0) + bytes(1) > room) {
+      int i = bytes(1) > bytes(0) ? 1 : 0;
+      if (!spare(i)) i = 1 - i;
+      if (!spare(i)) return false;
+      --work[i].splits;
+    }
+  } else {
+    work[0].splits = static_cast<int>(std::min<size_t>(work[0].splits, room / split[0]));
+    if (work[0].splits < 1) return false;
+  }
+  for (int i = 0; i < count; ++i) {
+    jobs[i].splits = work[i].splits;
+    jobs[i].part = pool;
+    pool += static_cast<size_t>(work[i].splits) * split[i] / sizeof(float);
+  }
+  return true;
 }
 
 cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, bool overlap_first, int* status,
@@ -590,9 +623,6 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
   const int rt = (r + 15) / 16;
   ColsumReduceJob reduce[2];
   unsigned blocks[2] = {0, 0};
-  TcWork work[2];
-  for (int i = 0; i < count; ++i) work[i] = cs_work(jobs[i].x.rows, jobs[i].x.cols, jobs[i].x.format == kAct8Dense);
-  if (count == 2) tc_share_wave(work[0], work[1]);
   for (int i = 0; i < count; ++i) {
     const ColsumJob& job = jobs[i];
     const Act8View& x = job.x;
@@ -603,7 +633,7 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
       if (!encode_tensor_map_2d(&maps[1 + q], parts[q], x.rows, kRankPad, kCsTok, 64)) return cudaErrorInvalidValue;
     maps[0] = maps[1];
     if (dense && !encode_tensor_map_2d(&maps[0], x.codes, x.rows, x.cols, kCsTok, 64)) return cudaErrorInvalidValue;
-    const int splits = work[i].splits;
+    const int splits = job.splits;
     const cudaError_t e =
         dense ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, job.part, after, status, stream)
         : x.format == kAct8Int8
@@ -641,8 +671,7 @@ constexpr uint32_t kRsTmemCols = kRsSums * kRankPad;
 
 TcWork rs_work(int64_t M, int64_t K, bool dense) {
   TcWork w{(M + kRsTok - 1) / kRsTok, (K + kRsCols - 1) / kRsCols, dense, 0};
-  const int64_t room = skinny_splits(M, K);  // what the workspace's partials are sized for
-  w.splits = static_cast<int>(std::max<int64_t>(1, std::min({148 / w.tiles, w.steps, room})));
+  w.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({148 / w.tiles, w.steps, 64})));
   return w;
 }
 
@@ -763,16 +792,33 @@ cudaError_t launch_rowsum_format(const Act8View& x, const CUtensorMap& tx, const
 
 }  // namespace
 
-cudaError_t launch_act8_rowsums(RowsumJob* jobs, int count, int r, int* status, cudaStream_t stream) {
-  const int r16 = (r + 15) / 16 * 16;
+bool plan_act8_rowsums(RowsumJob* jobs, int count, float* pool, size_t room) {
+  const int64_t M = jobs[0].x.rows;
+  const size_t split = static_cast<size_t>(M) * kRankPad * sizeof(float);
+  const int64_t most = static_cast<int64_t>(room / split);
   TcWork work[2];
-  for (int i = 0; i < count; ++i) work[i] = rs_work(jobs[i].x.rows, jobs[i].x.cols, jobs[i].x.format == kAct8Dense);
-  if (count == 2) tc_share_wave(work[0], work[1]);
+  for (int i = 0; i < count; ++i) work[i] = rs_work(M, jobs[i].x.cols, jobs[i].x.format == kAct8Dense);
+  if (count == 2) {
+    tc_share_wave(work[0], work[1]);
+    if (work[0].splits + work[1].splits > most) return false;
+  } else {
+    work[0].splits = static_cast<int>(std::min<int64_t>(work[0].splits, most));
+    if (work[0].splits < 1) return false;
+  }
   for (int i = 0; i < count; ++i) {
-    RowsumJob& job = jobs[i];
+    jobs[i].splits = work[i].splits;
+    jobs[i].part = pool;
+    pool += static_cast<size_t>(work[i].splits) * split / sizeof(float);
+  }
+  return true;
+}
+
+cudaError_t launch_act8_rowsums(const RowsumJob* jobs, int count, int r, int* status, cudaStream_t stream) {
+  const int r16 = (r + 15) / 16 * 16;
+  for (int i = 0; i < count; ++i) {
+    const RowsumJob& job = jobs[i];
     const Act8View& x = job.x;
     const bool dense = x.format == kAct8Dense, overlap = i > 0;
-    job.splits = work[i].splits;
     CUtensorMap tx, tw;
     if (dense ? !encode_tensor_map_2d(&tw, job.W, x.cols, r, 64, kRankPad, true, job.ldw)
               : !encode_tensor_map_2d(&tw, job.W, r, x.cols, kRankPad, 64))

@@ -351,7 +351,7 @@ int64_t max_group_chunks(const qlora_nf4_weight* outs, int32_t count) {
 
 // Linear workspace layout.
 struct LinearWs {
-  size_t wbf, scales, us, uhi, ulo, ulo2, vs, vhi, vlo, vlo2, bpad, part, dbpart, skpart, vdbpart, bt, uht, ult, ult2, gu, gy, total;
+  size_t wbf, scales, us, uhi, ulo, vs, vhi, vlo, bpad, part, skpart, vdbpart, bt, uht, ult, gu, gy, total;
 };
 
 LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
@@ -371,25 +371,20 @@ LinearWs linear_ws_layout(int64_t M, int64_t N, int64_t K, bool dense) {
   l.us = take(mr * 2);
   l.uhi = take(mr * 2);
   l.ulo = take(mr * 2);
-  l.ulo2 = take(mr * 2);  // third parts: the backward from a checkpoint
   l.vs = take(mr * 2);
   l.vhi = take(mr * 2);
   l.vlo = take(mr * 2);
-  l.vlo2 = take(mr * 2);
   l.bpad = take(static_cast<size_t>(N) * kRankPad * 2);
   const size_t p1 = colsum_partial_bytes(M, N), p2 = colsum_partial_bytes(M, K);
+  l.part = take(p1 > p2 ? p1 : p2);
   const size_t s1 = skinny_partial_bytes(M, N), s2 = skinny_partial_bytes(M, K);
-  // From a checkpoint, U's partials and later dA's share `part`.
-  l.part = take(std::max({p1, p2, s2, act8_colsum_partial_bytes(M, K)}));
   l.skpart = take(s1 > s2 ? s1 : s2);
   // The tensor-core V / dB pass: its partials and the transposed B and U split.
   const bool vdb = M > kGemvMaxM;
-  l.vdbpart = take(std::max(vdb ? vdb_tc_partial_bytes(M, N) : 0, act8_colsum_partial_bytes(M, N)));
-  l.dbpart = l.vdbpart;  // dB's partials from a checkpoint: where the V / dB pass does not run
+  l.vdbpart = take(vdb ? vdb_tc_partial_bytes(M, N) : 0);
   l.bt = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(N) * 2 : 0);
   l.uht = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
   l.ult = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
-  l.ult2 = take(vdb ? static_cast<size_t>(16) * static_cast<size_t>(vdb_tc_ldm(M)) * 2 : 0);
   // Decode path (M <= 16): U partials and, for K > 4096, per-chunk fp32 outputs.
   const bool decode = M <= kGemvMaxM;
   l.gu = take(decode ? static_cast<size_t>(gemv_upart_count(K)) * kGemvMaxM * kRankPad * 4 : 0);
@@ -918,11 +913,25 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   }
   const uint16_t* Bk = b_direct ? B : at<uint16_t>(ws, lay.bpad);
   const int64_t ldbk = b_direct ? r : kRankPad;
+  // V with dB from one pass over dY; elsewhere each product has its own kernel.
+  const bool vdb_pass = dB != nullptr && r <= kVdbMaxRank && M > kGemvMaxM;
   // From a checkpoint U and V are split into three bf16 parts, which hold all
   // of their fp32 values: dA and dB then keep fp32 accuracy (2 10^-6 with two
-  // parts, against the 10^-3 that the checkpoint itself costs at most).
-  uint16_t* const ulo2 = x8 != nullptr ? at<uint16_t>(ws, lay.ulo2) : nullptr;
-  uint16_t* const vlo2 = x8 != nullptr ? at<uint16_t>(ws, lay.vlo2) : nullptr;
+  // parts, against the 10^-3 that the checkpoint itself costs at most).  These
+  // parts and the products' partials live in the same workspace: U's third part
+  // where the forward keeps s U, V's there too where U has done its work by then
+  // (the rank transposes of the V / dB pass), else at the workspace's end, and
+  // the partials between (U's and V's, then dB's and dA's; bpad is free again
+  // once V is summed).
+  uint16_t* const ulo2 = x8 != nullptr ? at<uint16_t>(ws, lay.us) : nullptr;
+  const size_t pool_end = lay.total - (vdb_pass ? 0 : align_up(static_cast<size_t>(M) * kRankPad * 2, 256));
+  uint16_t* const vlo2 = x8 == nullptr ? nullptr : vdb_pass ? ulo2 : at<uint16_t>(ws, pool_end);
+  auto plan_rowsums = [&](RowsumJob* jobs, int count) {
+    return plan_act8_rowsums(jobs, count, at<float>(ws, lay.part), pool_end - lay.part);
+  };
+  auto plan_colsums = [&](ColsumJob* jobs, int count) {
+    return plan_act8_colsums(jobs, count, r, at<float>(ws, lay.bpad), pool_end - lay.bpad);
+  };
   SkinnyOut uo{};
   uo.ohi = at<uint16_t>(ws, lay.uhi);
   uo.olo = at<uint16_t>(ws, lay.ulo);
@@ -932,12 +941,11 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   RowsumJob u_job{}, v_job{};
   ColsumJob da_job{}, db_job{};
   if (x8 != nullptr) {
-    u_job = RowsumJob{view_of(x8), A, K, at<float>(ws, lay.part), 0};
-    v_job = RowsumJob{dense_view(dY, M, N), Bk, ldbk, at<float>(ws, lay.skpart), 0};
-    da_job = ColsumJob{view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, at<float>(ws, lay.part),
-                       dA, true};
-    db_job = ColsumJob{dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2,
-                       at<float>(ws, lay.dbpart), dB, false};
+    u_job = RowsumJob{view_of(x8), A, K, nullptr, 0};
+    v_job = RowsumJob{dense_view(dY, M, N), Bk, ldbk, nullptr, 0};
+    da_job = ColsumJob{view_of(x8), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, dA, true, nullptr, 0};
+    db_job = ColsumJob{dense_view(dY, M, N), at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, dB, false,
+                       nullptr, 0};
   }
   // U = X A^T in its bf16 parts (from the saved fp32 U, or recomputed).
   auto u_hilo = [&]() -> cudaError_t {
@@ -947,6 +955,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     }
     Timed tm(kFamSide, s, 2);
     if (x8 != nullptr) {
+      if (!plan_rowsums(&u_job, 1)) return cudaErrorInvalidValue;
       e = launch_act8_rowsums(&u_job, 1, r, status, s);
       const SkinnyJob job{u_job.part, u_job.splits, uo};
       return e != cudaSuccess ? e : launch_skinny_finalize(&job, 1, M, r, s);
@@ -955,7 +964,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   };
   bool da_done = false;
   BlockScalesJob bs{};  // the dX GEMM's block scales, when a kernel before it carries them
-  if (dB != nullptr && r <= kVdbMaxRank && M > kGemvMaxM) {
+  if (vdb_pass) {
     // V = dY B (s*V for the dX rank step, hi/lo for dA) and dB = s dY^T U in one pass over dY.
     // A saved fp32 U goes straight to the rank transposes, which split it
     // themselves; otherwise U is recomputed as its hi/lo split first.
@@ -968,7 +977,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     Timed tm(kFamSide, s, 3);  // the rank transposes, the pass, the reduction
     e = launch_vdb_tc(dY, M, N, Bk, ldbk, at<uint16_t>(ws, lay.uhi), at<uint16_t>(ws, lay.ulo), ulo2, U, r, scale,
                       at<float>(ws, lay.vdbpart), at<uint16_t>(ws, lay.bt), at<uint16_t>(ws, lay.uht),
-                      at<uint16_t>(ws, lay.ult), x8 != nullptr ? at<uint16_t>(ws, lay.ult2) : nullptr,
+                      at<uint16_t>(ws, lay.ult), x8 != nullptr ? at<uint16_t>(ws, lay.skpart) : nullptr,
                       at<uint16_t>(ws, lay.vs), at<uint16_t>(ws, lay.vhi), at<uint16_t>(ws, lay.vlo), vlo2, dB, bs,
                       status, s);
     if (e != cudaSuccess) return from_cuda(e);
@@ -980,17 +989,18 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     vo.olo = at<uint16_t>(ws, lay.vlo);
     vo.olo2 = vlo2;
     vo.scale = scale;
-    const bool u_done = x8 != nullptr && dB != nullptr && U == nullptr;
+    RowsumJob products[2] = {u_job, v_job};
+    const bool u_done = x8 != nullptr && dB != nullptr && U == nullptr && plan_rowsums(products, 2);
     if (u_done) {
       // U too: V's product runs beside U's, and one reduction ends both.
       Timed tm(kFamSide, s, 3);
-      RowsumJob products[2] = {u_job, v_job};
       e = launch_act8_rowsums(products, 2, r, status, s);
-      const SkinnyJob jobs[2] = {{u_job.part, products[0].splits, uo}, {v_job.part, products[1].splits, vo}};
+      const SkinnyJob jobs[2] = {{products[0].part, products[0].splits, uo}, {products[1].part, products[1].splits, vo}};
       if (e == cudaSuccess) e = launch_skinny_finalize(jobs, 2, M, r, s);
     } else {
       Timed tm(kFamSide, s, 2);
       if (x8 != nullptr) {
+        if (!plan_rowsums(&v_job, 1)) return QLORA_ERR_WORKSPACE;
         e = launch_act8_rowsums(&v_job, 1, r, status, s);
         const SkinnyJob job{v_job.part, v_job.splits, vo};
         if (e == cudaSuccess) e = launch_skinny_finalize(&job, 1, M, r, s);
@@ -1001,8 +1011,9 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
     if (e == cudaSuccess && dB != nullptr && !u_done) e = u_hilo();
     if (e != cudaSuccess) return from_cuda(e);
     if (dB != nullptr && x8 != nullptr) {  // dB = s dY^T U, with dA beside it
-      const ColsumJob jobs[2] = {db_job, da_job};
-      da_done = dA != nullptr;
+      ColsumJob jobs[2] = {db_job, da_job};
+      da_done = dA != nullptr && plan_colsums(jobs, 2);
+      if (!da_done && !plan_colsums(jobs, 1)) return QLORA_ERR_WORKSPACE;
       Timed tm(kFamSide, s, da_done ? 3 : 2);
       e = launch_act8_colsums(jobs, da_done ? 2 : 1, r, scale, false, status, s);
       if (e != cudaSuccess) return from_cuda(e);
@@ -1049,6 +1060,7 @@ qlora_status linear_bwd(const qlora_nf4_weight* w, const uint16_t* X, const qlor
   }
   if (dA != nullptr && !da_done) {  // dA = s V^T X
     {
+      if (x8 != nullptr && !plan_colsums(&da_job, 1)) return QLORA_ERR_WORKSPACE;
       Timed tm(kFamSide, s, 2);
       if (x8 != nullptr)  // beside the dX GEMM, on the SMs that it leaves
         e = launch_act8_colsums(&da_job, 1, r, scale, dX != nullptr, status, s);

@@ -281,35 +281,38 @@ cudaError_t launch_act8_quantize(const uint16_t* X, int64_t n, int format, uint8
 cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t stream);
 // out(j, k) = scale sum_m (hi + lo + lo2)[m][j] X^[m][k] over the rows m of x
 // (a checkpoint, or bf16 values with 16-byte aligned rows), written to dst as
-// [r][cols] (dst_rc) or [cols][r].  `part` is scratch of
-// act8_colsum_partial_bytes(rows, cols), enough for every rank and format.
-// One or two jobs: the second product starts where the first leaves room, and
-// one reduction ends both.  The first one's launch overlaps the previous kernel
-// of the stream; `overlap_first`: so may its work, as that kernel writes nothing
-// that it reads.
+// [r][cols] (dst_rc) or [cols][r].  One or two jobs: the second product starts
+// where the first leaves room, and one reduction ends both.  The first one's
+// launch overlaps the previous kernel of the stream; `overlap_first`: so may its
+// work, as that kernel writes nothing that it reads.
+// plan_act8_colsums sets the jobs' splits and gives their partials places in
+// `room` bytes of scratch from `pool` on.  False where two do not fit together
+// (or not even one split does): they then run in turn, each planned alone.
 struct ColsumJob {
   Act8View x;
   const uint16_t *hi, *lo, *lo2;
-  float* part;
   float* dst;
   bool dst_rc;
+  float* part;  // [splits][16 ceil(r / 16)][cols]
+  int splits;
 };
-size_t act8_colsum_partial_bytes(int64_t M, int64_t C);
+bool plan_act8_colsums(ColsumJob* jobs, int count, int r, float* pool, size_t room);
 cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float scale, bool overlap_first, int* status,
                                 cudaStream_t stream);
 // part[z][m][j] = sum over the columns k of split z of X^[m][k] W(j, k): W is
 // [r][cols] for a checkpoint, [cols][r] of pitch ldw for plain bf16 values (both
 // 16-byte aligned rows); `part` as for launch_skinny, to be reduced by
-// launch_skinny_finalize over the `splits` that the launch chooses.  One or two
-// jobs, the second beside the first.
+// launch_skinny_finalize.  One or two jobs, the second beside the first.
+// plan_act8_rowsums: as plan_act8_colsums.
 struct RowsumJob {
   Act8View x;
   const uint16_t* W;
   int64_t ldw;
-  float* part;
+  float* part;  // [splits][rows][64]
   int splits;
 };
-cudaError_t launch_act8_rowsums(RowsumJob* jobs, int count, int r, int* status, cudaStream_t stream);
+bool plan_act8_rowsums(RowsumJob* jobs, int count, float* pool, size_t room);
+cudaError_t launch_act8_rowsums(const RowsumJob* jobs, int count, int r, int* status, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Residual sum between two norms (residual_norm.cu)
