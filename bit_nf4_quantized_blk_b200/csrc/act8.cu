@@ -478,12 +478,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < kCsSums; ++i) tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(i * kRankPad + j0), v[i]);
 #pragma unroll
         for (int i = 0; i < kCsSums; ++i) tc_wait_ld(v[i]);
-        if (k >= C) continue;
-        float* dst = part + (static_cast<int64_t>(z) * r16 + j0) * C + k;
+        if (k < C) {
+          float* dst = part + (static_cast<int64_t>(z) * r16 + j0) * C + k;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          dst[j * C] = (__uint_as_float(v[0][j]) + __uint_as_float(v[3][j])) +
-                       (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+          for (int j = 0; j < 16; ++j)
+            dst[j * C] = (__uint_as_float(v[0][j]) + __uint_as_float(v[3][j])) +
+                         (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+        }
+        __syncwarp();  // the next load is the whole warp's
       }
     }
   }

@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
         tmem_wait_ld16(v);
         const int64_t n = static_cast<int64_t>(tc0 + tc) * kVtCol + q * 32 + lane;
         if (n < N) store16(dbpart + (static_cast<int64_t>(zm) * N + n) * 16, v);
+        __syncwarp();  // the next load is the whole warp's
       }
     }
   }

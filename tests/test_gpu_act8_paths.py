@@ -81,6 +81,17 @@ class Problem:
             assert ((db.double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("N", [8, 24, 136, 264, 1032])
+@pytest.mark.parametrize("r", [33, 48, 64])
+def test_columns_that_end_inside_a_warp(N, r):
+    """Ranks above 32 take a warp of the column sums' epilogue twice through its loop, and the columns of dB may end
+    within the warp: its lanes load the second accumulators together all the same."""
+    p = Problem(300, N, 192, r, "int8")
+    for saved_u in (True, False):
+        _, da, db = p.run(saved_u)
+        p.check(saved_u, da, db)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M, N, K, r", [
     (1, 64, 64, 64), (2, 128, 64, 64), (16, 40, 64, 64),  # dB's and dA's partials have no room side by side
