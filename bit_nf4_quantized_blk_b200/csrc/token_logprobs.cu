@@ -665,6 +665,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(TokenLog
   const F2 A = splat2(-c * (g + (p.g_entropy != nullptr ? gh * p.entropy[r] : 0.0f))), B = splat2(-c * gh * kLn2);
   const F2 minus = splat2(-m), c2 = splat2(c * kLog2e), shift = splat2(-log_sum * kLog2e);
   const bool empty = m == kNegInf;
+  const float empty_row = target >= p.V ? g : 0.0f;  // NaN, as everywhere for such a target
 #pragma unroll
   for (int i = 0; i < kLpVecs; ++i) {
     const int64_t vec = v0 + i * kLpThreads, first = vec * P;
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(TokenLog
     }
     if (empty) {  // every logit is -inf
 #pragma unroll
-      for (int j = 0; j < P; ++j) x[j] = 0.0f;
+      for (int j = 0; j < P; ++j) x[j] = empty_row;
     }
     if (first + P <= p.V) {
       if constexpr (sizeof(T) == 2)

@@ -521,7 +521,9 @@ qlora_status qlora_residual_norm_bwd(const void *dh_out, const uint16_t *dx, con
  * A row whose logits are all -inf has row_max -inf, log_sum 0, entropy 0 and log
  * probabilities -inf; a row masked to a finite value is an ordinary one.  A row
  * with a NaN or +inf has NaN outputs (row_max: NaN or +inf); NaN ranks above
- * every number among the alternatives.  Sums are fp32.  No workspace.
+ * every number among the alternatives.  A target's rule comes before its row's:
+ * logprob is 0 for a negative one and NaN for one of V or more in every row.
+ * Sums are fp32.  No workspace.
  */
 qlora_status qlora_token_logprobs_fwd(const void *logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
                                       const int64_t *targets, float inv_temperature, float *logprob, float *entropy,
@@ -540,7 +542,8 @@ qlora_status qlora_token_logprobs_fwd(const void *logits, int32_t dtype, int64_t
  *             logits; may be logits itself (with ldd = ld).  Columns from V on are
  *             left alone: for the dY of a linear call whose rows are padded past
  *             V, clear them once.
- * Rows whose logits are all -inf get zeros, rows with NaN or +inf NaN.
+ * Rows whose logits are all -inf get zeros (NaN if their target is V or more),
+ * rows with NaN or +inf NaN.
  */
 qlora_status qlora_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t M, int64_t V, int64_t ld,
                                       const int64_t *targets, float inv_temperature, const float *row_max,

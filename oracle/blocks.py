@@ -96,7 +96,7 @@ def token_logprobs(logits, targets, inv_temperature, k=0):
 
 
 def token_logprobs_backward(logits, targets, inv_temperature, g_logprob, g_entropy=None):
-    """dlogits: zero for rows whose logits are all -inf, NaN for rows with NaN or +inf or a target of V or more."""
+    """dlogits: NaN for rows with NaN or +inf or a target of V or more, zero for other rows whose logits are all -inf."""
     x = _f64(logits)
     M, V = x.shape
     out = np.zeros((M, V))

@@ -253,6 +253,25 @@ def test_backward_in_place_and_masked(dtype):
     _check_backward(x.clone(memory_format=torch.preserve_format) if x.is_contiguous() else x, t, in_place=True)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("logprob", [True, False])
+def test_targets_past_the_end_of_masked_rows(dtype, logprob):
+    """A target of V or more gives NaN in every row, an empty one too; a negative one 0 in every row."""
+    V = 700
+    x = _logits(9, V, dtype, 12)
+    x[:4] = float("-inf")
+    x[4:7, 5] = float("nan")
+    t = torch.tensor([V, -1, 3, V + 100, V, -1, 4, V, -1], device="cuda")
+    got, ref = _check_forward(x, t, k=2)
+    assert np.isnan(ref["logprob"][[0, 3, 4, 7]]).all() and (ref["logprob"][[1, 5, 8]] == 0).all()
+    _check_backward(x, t, logprob=logprob)
+    if logprob:
+        g = torch.ones(9, device="cuda")
+        d = torch.empty((9, 704), dtype=dtype, device="cuda")[:, :V]
+        binding.qlora_token_logprobs_bwd(x, t, 1.0, got["row_max"], got["log_sum"], None, g, None, d)
+        assert torch.isnan(d[[0, 3, 4, 5, 6, 7]]).all() and (d[[1, 2]] == 0).all() and torch.isfinite(d[8]).all()
+
+
 def test_gradient_against_differences():
     """The formula itself: central differences of the fp64 forward."""
     rng = np.random.RandomState(0)
