@@ -20,7 +20,10 @@
 // token-tile major.  The V accumulator (16 TMEM columns) is double-buffered
 // and drained to the partial vpart[zc][m][16] after each token tile; the dB
 // accumulators (16 columns per column tile) live across the CTA's token
-// tiles and are drained to dbpart[zm][n][16] at the end.  Two CTAs share an
+// tiles and are drained to dbpart[zm][n][16] at the end.  With U in three parts
+// they are drained every kVtRun token tiles and the CTA adds the runs in fp32:
+// the tensor core truncates, so that a chain of additions over all tokens of a
+// long input would cost dB the accuracy that the third part is there for.  Two CTAs share an
 // SM (two-stage rings): two producer threads keep the SM's TMA busier than one
 // with a four-stage ring did (0.89 -> 0.83 ms for the step's side family).
 // Partial sums are
@@ -48,6 +51,13 @@ template <int kParts>  // of U: 2 or 3
 constexpr int kVtStage = kVtGTile + (1 + kParts) * kVtSmall;  // 44 or 48 KB
 constexpr int kVtCTMax = 8;                    // column tiles per CTA
 constexpr int kVtThreads = 192;
+// Token tiles whose products are added in one chain: all of them or, with three
+// parts of U (24 additions per tile), 2.  Backward without dX, rank 16, dB's
+// error and the time with all in one chain, with 4 tiles and with 2: 8192 x 14336
+// x 4096 1.7e-6 101 us, 1.7e-6 99, 8.7e-7 100; 65536 x 14336 x 64 1.1e-5 413 us,
+// 1.7e-6 430, 8.7e-7 449 (an fp32 product: 1.6e-6 and 4.6e-6).
+template <int kParts>
+constexpr int kVtRun = kParts == 3 ? 2 : 1 << 30;
 constexpr uint32_t kVtTmemCols = 256;          // V: 2 x 16, dB: up to 8 x 16
 template <int kParts>
 constexpr int kVtSmem = 1024 + kVtStages * kVtStage<kParts> + 256;
@@ -57,11 +67,14 @@ struct VtBarriers {
   uint64_t empty[kVtStages];
   uint64_t v_full[2];
   uint64_t v_empty[2];
-  uint64_t db_full;
+  uint64_t db_full[kVtCTMax];   // a column tile's run of token tiles is summed
+  uint64_t db_empty[kVtCTMax];  // and drained
   uint64_t drain;
   uint32_t tmem;
   int abort_flag;
 };
+
+static_assert(sizeof(VtBarriers) <= 256, "room for the barriers");
 
 __device__ __forceinline__ bool vt_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   bool ok = true;
@@ -91,6 +104,19 @@ __device__ __forceinline__ void store16(float* dst, const uint32_t (&v)[16]) {
                         __uint_as_float(v[4 * q + 3]));
 }
 
+// v += the 16 fp32 values at src.
+__device__ __forceinline__ void add16(const float* src, uint32_t (&v)[16]) {
+  const float4* s4 = reinterpret_cast<const float4*>(src);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4 s = s4[q];
+    v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + s.x);
+    v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + s.y);
+    v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + s.z);
+    v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + s.w);
+  }
+}
+
 }  // namespace
 
 template <int kParts>
@@ -99,7 +125,7 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
                   const __grid_constant__ CUtensorMap tmUh, const __grid_constant__ CUtensorMap tmUl,
                   const __grid_constant__ CUtensorMap tmUl2, int64_t M, int64_t N, int ct, int tt,
                   float* __restrict__ vpart, float* __restrict__ dbpart, int* status) {
-  constexpr int kStage = kVtStage<kParts>;
+  constexpr int kStage = kVtStage<kParts>, kRun = kVtRun<kParts>;
   pdl_launch_dependents();  // the reduction's launch
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -122,7 +148,10 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
       mbar_init(&bars->v_full[b], 1);
       mbar_init(&bars->v_empty[b], 4);  // the four epilogue warps
     }
-    mbar_init(&bars->db_full, 1);
+    for (int t = 0; t < kVtCTMax; ++t) {
+      mbar_init(&bars->db_full[t], 1);
+      mbar_init(&bars->db_empty[t], 4);
+    }
     mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -182,6 +211,11 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
           ok = false;
           break;
         }
+        const bool fresh = tm % kRun == 0;  // a new run's chains
+        if (tm > 0 && fresh && !mbar_wait(&bars->db_empty[tc], (tm / kRun - 1) & 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t st = smem_u32(smem + s * kStage);
         // dY tile as the MN-major A of dB: 64-column groups 16 KB apart
@@ -200,7 +234,7 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
           const uint64_t b_hi = smem_desc_k128(st + kVtGTile + kVtSmall + box * kVtSmallBox) + 2 * sub;
           const uint64_t b_lo = smem_desc_k128(st + kVtGTile + 2 * kVtSmall + box * kVtSmallBox) + 2 * sub;
           const uint32_t acc_db = tmem + 32u + static_cast<uint32_t>(tc * 16);
-          tc_mma_bf16_ss(acc_db, a_db, b_hi, idesc_db, (tm > 0 || kk > 0) ? 1u : 0u);
+          tc_mma_bf16_ss(acc_db, a_db, b_hi, idesc_db, (!fresh || kk > 0) ? 1u : 0u);
           tc_mma_bf16_ss(acc_db, a_db, b_lo, idesc_db, 1u);
           if constexpr (kParts == 3) {
             const uint64_t b_lo2 = smem_desc_k128(st + kVtGTile + 3 * kVtSmall + box * kVtSmallBox) + 2 * sub;
@@ -208,9 +242,9 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
           }
         }
         tc_commit(&bars->empty[s]);
+        if (tm % kRun == kRun - 1 || tm == ntm - 1) tc_commit(&bars->db_full[tc]);
         if (tc == ntc - 1) tc_commit(&bars->v_full[vb]);
       }
-      if (ok) tc_commit(&bars->db_full);
       tc_commit(&bars->drain);
       mbar_wait_teardown(&bars->drain, 0, status);
     }
@@ -221,10 +255,31 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
     bool ok = true;
     for (int tm = 0; tm < ntm && ok; ++tm) {
       const int vb = tm & 1;
+      uint32_t v[16];
+      if (tm % kRun == kRun - 1 || tm == ntm - 1) {  // dB's run ends, column tile by column tile
+        const int run = tm / kRun;
+        for (int tc = 0; tc < ntc && ok; ++tc) {
+          ok = vt_warp_wait(&bars->db_full[tc], run & 1, abort_flag, status);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_ld_32x32b_x16(tmem + lane_off + 32u + static_cast<uint32_t>(tc * 16), v);
+          tmem_wait_ld16(v);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->db_empty[tc]);
+          const int64_t n = static_cast<int64_t>(tc0 + tc) * kVtCol + q * 32 + lane;
+          float* dst = dbpart + (static_cast<int64_t>(zm) * N + n) * 16;
+          if (n < N) {
+            if (run > 0) add16(dst, v);
+            store16(dst, v);
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+        if (!ok) break;
+      }
       ok = vt_warp_wait(&bars->v_full[vb], (tm >> 1) & 1, abort_flag, status);
       if (!ok) break;
       tc_fence_after();
-      uint32_t v[16];
       tmem_ld_32x32b_x16(tmem + lane_off + static_cast<uint32_t>(vb * 16), v);
       tmem_wait_ld16(v);
       const int64_t m = static_cast<int64_t>(tm0 + tm) * kVtTok + q * 32 + lane;
@@ -232,17 +287,6 @@ __global__ void __launch_bounds__(kVtThreads, kVtPerSm)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->v_empty[vb]);
-    }
-    if (ok && vt_warp_wait(&bars->db_full, 0, abort_flag, status)) {
-      tc_fence_after();
-      for (int tc = 0; tc < ntc; ++tc) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(tmem + lane_off + 32u + static_cast<uint32_t>(tc * 16), v);
-        tmem_wait_ld16(v);
-        const int64_t n = static_cast<int64_t>(tc0 + tc) * kVtCol + q * 32 + lane;
-        if (n < N) store16(dbpart + (static_cast<int64_t>(zm) * N + n) * 16, v);
-        __syncwarp();  // the next load is the whole warp's
-      }
     }
   }
   tc_fence_before();

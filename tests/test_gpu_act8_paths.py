@@ -81,6 +81,41 @@ class Problem:
             assert ((db.double() - ref).abs() <= tol).all()
 
 
+def test_long_inputs_keep_short_chains_of_additions():
+    """The tensor core truncates: an addition loses half a unit in the last place of its sum on average, at most 2^-24 of
+    it, always in one direction.  dB of 4096 tokens and 131072 outputs adds 48 times in a row (two token tiles, three
+    parts), then 8 runs and the token blocks in fp32; all values are positive, so that no sum is larger than its
+    result."""
+    p = Problem(4096, 131072, 64, 16, "int8")
+    for t in (p.dY, p.A, p.B, p.U, p.x):
+        t.abs_()
+    binding.qlora_act8_quantize(p.x, p.a)
+    binding.qlora_act8_dequantize(p.a, p.x)
+    for saved_u in (True, False):
+        _, _, db = p.run(saved_u, da=False)
+        u = p.U.double() if saved_u else p.x.double() @ p.A.double().t()
+        ref = torch.zeros_like(db, dtype=torch.float64)
+        for i in range(0, p.M, 512):
+            ref += p.s * p.dY[i:i + 512].double().t() @ u[i:i + 512]
+        terms = 48 + 8 + 2 + (0 if saved_u else 64)
+        assert (db.double() - ref).norm() <= terms * 2.0**-24 * ref.norm()
+
+
+def test_wide_inputs_keep_short_chains_of_additions():
+    """V of 65536 outputs at a rank above 16: 64 additions in a row, then 8 sums of those and 8 splits.  X^ has one
+    value per column, so that dA is V itself."""
+    p = Problem(9600, 65536, 64, 40, "int8")
+    p.dY.abs_()
+    p.B.abs_()
+    p.a.codes.zero_()
+    p.a.step.fill_(1.0)
+    rows = torch.arange(p.K, device="cuda") * 149
+    p.a.codes[rows, torch.arange(p.K, device="cuda")] = 1
+    _, da, _ = p.run(True, db=False)
+    ref = p.s * (p.dY[rows].double() @ p.B.double()).t()
+    assert (da.double() - ref).norm() <= (64 + 8 + 8 + 4) * 2.0**-24 * ref.norm()
+
+
 @pytest.mark.parametrize("N", [8, 24, 136, 264, 1032])
 @pytest.mark.parametrize("r", [33, 48, 64])
 def test_columns_that_end_inside_a_warp(N, r):
