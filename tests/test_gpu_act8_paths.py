@@ -155,3 +155,92 @@ def test_everything_fits_the_linear_workspace(M, N, K, r, fmt):
         v = (p.dY.double() @ p.B.double()).abs()
         apart = p.s * (2.0**-7 * (v + e) + 2 * e) @ p.A.double().abs()
         assert ((dx.double() - want.double()).abs() <= apart + 2.0**-7 * want.double().abs() + 1e-30).all()
+
+
+# Steps of a CTA (64 tokens each for dA and dB, 128 columns for U and V), of which three are in flight.
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M, N, K, r", [
+    (1999, 2048, 8192, 64),  # U 8, V 16, dB 16, dA 8 steps
+    (1987, 2056, 8128, 40),  # the same with ragged ends everywhere; V 17
+    (1987, 2056, 8128, 11),  # dA 7 or 8; V and dB from one pass
+    (6300, 136, 8192, 24),   # dA in two waves of CTAs, 11 steps each
+])
+def test_products_of_many_steps(M, N, K, r, fmt):
+    """Every stage of a product's pipeline is used several times over, the last ones not all equally often."""
+    p = Problem(M, N, K, r, fmt)
+    ws = torch.empty(binding.qlora_linear_ws_bytes(M, N, K, r), dtype=torch.uint8, device="cuda")
+    binding.qlora_workspace_reset(ws)
+    first = {}
+    for saved_u in (True, False):
+        _, da, db = first[saved_u] = p.run(saved_u, ws=ws)
+        p.check(saved_u, da, db)
+        _, da, _ = p.run(saved_u, db=False, ws=ws)
+        p.check(saved_u, da, None)
+    for i in range(8):  # in a row on one workspace
+        _, da, db = p.run(i % 2 == 0, ws=ws)
+        assert torch.equal(da, first[i % 2 == 0][1]) and torch.equal(db, first[i % 2 == 0][2])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M, r", [(2, 3), (16, 8), (16, 64), (32, 8), (32, 40), (66, 16), (200, 64), (1000, 12)])
+def test_third_parts_of_u_and_v(M, r, fmt):
+    """V and U of token 2 i are those of token 2 i + 1 and 2^-19 more, which their first two bf16 parts do not hold, and
+    the other factor is that of token 2 i + 1 negated: what is left of dA and dB is the third parts' product alone.
+
+    Each token's V is base + b1 + 2^-19 with base a bf16 in [1, 2) and b1 one in [2^-10, 2^-9): 2^-19 is below half of
+    b1's last place, 2^-17.  The first parts' products cancel exactly, 16 tokens at a time; added to the sum they can
+    cost it 2^-22 (one unit of a sum that passes 2 to 4) for each of the 17 terms (the tokens' and the sum).
+    """
+    N, K = 8, 64
+    g = torch.Generator().manual_seed(M + r)
+    base = 1 + torch.randint(0, 128, (r,), generator=g) / 128
+    b1 = (1 + torch.randint(0, 128, (r,), generator=g) / 128) * 2.0**-10
+    even = (torch.arange(M) % 2 == 0).double()
+    sign = 2 * even - 1
+    tol = (M + 15) // 16 * (min(M, 16) + 1) * 2.0**-22
+    one = {"int8": 1, "e4m3": 0x38}[fmt]  # the code of 1
+    w = binding.NF4Weight.empty(N, K)
+    for t in (w.packed, w.qscale, w.c2, w.mu):
+        t.zero_()
+
+    def run(x_codes, dY, A, B, U):
+        a = binding.Act8(M, K, x_codes.to(torch.uint8).cuda(), torch.ones((M, K // 64), dtype=BF16, device="cuda"),
+                         FORMATS[fmt])
+        ws = torch.empty(binding.qlora_linear_ws_bytes(M, N, K, r), dtype=torch.uint8, device="cuda")
+        binding.qlora_workspace_reset(ws)
+        dA, dB = torch.empty((r, K), device="cuda"), torch.empty((N, r), device="cuda")
+        f = lambda t: t.to(BF16).cuda().contiguous()  # noqa: E731
+        binding.qlora_linear_bwd_act8(w, a, f(dY), f(A), f(B), r, 1.0, None, 0, dA, dB, ws,
+                                      U=None if U is None else U.float().cuda())
+        assert binding.qlora_workspace_status(ws) == 0
+        return dA.double().cpu(), dB.double().cpu()
+
+    # dA: V from dY and B; X^ in +-[1, 2): int8 codes of +-1, E4M3 codes of 1 + i / 8
+    if fmt == "int8":
+        x = torch.ones((M, K), dtype=torch.float64)
+        codes = torch.where(even[:, None] > 0, 1, 255).expand(M, K)
+    else:
+        eighths = torch.randint(0, 8, (1 + M // 2, K), generator=g).repeat_interleave(2, 0)[:M]
+        x = 1 + eighths.double() / 8
+        codes = torch.where(even[:, None] > 0, 0x38 + eighths, 0xB8 + eighths)
+    dY = torch.zeros((M, N))
+    dY[:, :2], dY[:, 2] = 1.0, even
+    B = torch.zeros((N, r))
+    B[0], B[1], B[2] = base, b1, 2.0**-19
+    want = (2.0**-19 * even[:, None] * x).sum(0).expand(r, K)
+    assert (want > 2 * tol).all()  # a result without the third parts, zero, would not pass
+    dA, _ = run(codes, dY, torch.zeros((r, K)), B, torch.zeros((M, r)))
+    assert ((dA - want).abs() <= tol).all()
+
+    # dB: U saved, or from X^ and A; dY in +-[1, 2)
+    y = 1 + torch.randint(0, 128, (1 + M // 2, N), generator=g).repeat_interleave(2, 0)[:M].double() / 128
+    want = (2.0**-19 * even[:, None] * y).sum(0)[:, None].expand(N, r)
+    assert (want > 2 * tol).all()
+    codes = torch.zeros((M, K), dtype=torch.int64)
+    codes[:, :2], codes[:, 2] = one, (one * even).long()
+    A = torch.zeros((r, K))
+    A[:, 0], A[:, 1], A[:, 2] = base, b1, 2.0**-19
+    U = base.double() + b1.double() + 2.0**-19 * even[:, None]
+    for u in (U, None):
+        _, dB = run(codes, sign[:, None] * y, A, torch.zeros((N, r)), u)
+        assert ((dB - want).abs() <= tol).all()
