@@ -192,6 +192,13 @@ def test_backward(M, D, res):
     _forward_backward(Case(M, D, res))
 
 
+@pytest.mark.parametrize("M, D, res", [(76001, 64, torch.bfloat16), (38001, 576, torch.bfloat16),
+                                       (5001, 4096, torch.float32)])
+def test_backward_of_many_rows(M, D, res):
+    """More than 32 rows for a CTA (or a warp), so that it fetches their scalars a second time, with every column sum."""
+    _forward_backward(Case(M, D, res))
+
+
 @pytest.mark.parametrize("post, gate", list(itertools.product([True, False], repeat=2)))
 def test_backward_parts(post, gate):
     _forward_backward(Case(11, 576, post=post, gate=gate))

@@ -183,6 +183,29 @@ def test_largest_logits_in_one_place():
         _check_forward((x / 64).to(dtype).cuda(), _targets(5, V, 1), k=20)
 
 
+def _mixed_rows(M, V, dtype, seed):
+    """Ordinary rows with masked, tied, empty and NaN ones between them."""
+    x, t = _logits(M, V, dtype, seed, pad=1), _targets(M, V, seed + 1)
+    g = torch.Generator().manual_seed(seed + 2)
+    kind = torch.randint(0, 12, (M,), generator=g).cuda()
+    x[kind == 0] = 0.5  # ties everywhere: more at the bound than a list holds
+    x[kind == 1] = float("-inf")
+    x[kind == 2, V // 3] = float("nan")
+    half = (kind == 3).nonzero().ravel()
+    x[half, : V // 2] = float("-inf")
+    x[(kind == 4).nonzero().ravel(), V - 1] = 60.0
+    t[kind == 5] = V + 3
+    return x, t
+
+
+@pytest.mark.parametrize("M, V, k, dtype", [(2000, 3001, 0, BF16), (2000, 3001, 5, FP32), (1300, 3001, 32, BF16),
+                                            (20000, 40, 5, BF16), (20000, 40, 0, FP32)])
+def test_rows_that_follow_each_other(M, V, k, dtype):
+    """More rows than CTAs: a CTA's copies run across rows' ends, its counts and lists are used again, and past 32 of
+    its rows (20000) its targets are fetched again."""
+    _check_forward(*_mixed_rows(M, V, dtype, M + k), k=k)
+
+
 def test_outputs_left_out():
     x, t = _logits(6, 777, BF16, 9), _targets(6, 777, 1)
     full = _forward(x, t, 0.7, 5)
