@@ -144,8 +144,11 @@ struct TcWork {
 // Two products share one wave where that takes no longer than one after the
 // other: nothing then waits for the first to end, and fewer splits leave fewer
 // partials.  In units of half a microsecond a step of plain bf16 takes 1, one
-// with decoding 2, and a second wave's start 4.  (Backward of 1999 tokens, 2048 x
-// 8192, rank 64: 50.5 us with both pairs in turn, 38.5 so.)
+// with decoding 2, and a second wave's start 4.  GPU time of the backward without
+// dX, U recomputed, both pairs in turn and so: 1999 x 2048 x 8192, rank 64, 41.9
+// and 33.6 us; 512 x 4096 x 4096, rank 64, 30.3 and 24.1; 2048 x 1024 x 4096, rank
+// 32, 29.7 and 25.3.  A second wave's start of 0 units leaves the second of these
+// at 30.2, one of 12 changes none by more than 1%.
 void tc_share_wave(TcWork& a, TcWork& b) {
   auto time = [](const TcWork& w, int64_t splits) {
     return (w.tiles * splits + 147) / 148 * ((w.steps + splits - 1) / splits) * (w.dense ? 1 : 2);
@@ -155,7 +158,9 @@ void tc_share_wave(TcWork& a, TcWork& b) {
   for (int64_t s = 1; s <= a0.splits; ++s) {
     const int64_t left = (148 - a0.tiles * s) / b0.tiles, sb = left < b0.splits ? left : b0.splits;
     if (a0.tiles * s >= 148 || sb < 1) break;
-    // 32 steps add 64 times in a row: 6 10^-7 of a sum that the tensor core truncates.
+    // 32 steps add 64 times in a row: 6 10^-7 of a sum that the tensor core truncates
+    // (8192 x 4096 x 4096, rank 64: 77.0 us, dB off by 5.9e-7; with up to 64 steps 73.3
+    // us and 1.5e-6, twice an fp32 product's 7.8e-7).
     if ((a0.steps + s - 1) / s > 32 || (b0.steps + sb - 1) / sb > 32) continue;
     const int64_t ta = time(a0, s), tb = time(b0, sb), t = ta > tb ? ta : tb;
     if (t <= best) best = t, a.splits = static_cast<int>(s), b.splits = static_cast<int>(sb);
@@ -386,8 +391,9 @@ constexpr int64_t kCsSteps = 24;                    // most steps of a CTA, wher
 
 TcWork cs_work(int64_t M, int64_t C, bool dense) {
   TcWork w{(C + kCsCols - 1) / kCsCols, (M + kCsTok - 1) / kCsTok, dense, 0};
-  // Whole waves, as many as keep a CTA at 24 steps (48 additions in a row: dA of
-  // 8192 tokens and 8192 columns is off by 1.0e-6 with 32 steps in one wave).
+  // Whole waves, as many as keep a CTA at 24 steps (48 additions in a row).  8192 x
+  // 8192 x 8192, rank 64: 125 us and dA off by 8.0e-7; with up to 48 steps 115 us
+  // and 1.3e-6, above an fp32 product's 1.1e-6; with 16 steps the same as with 24.
   int64_t waves = (w.tiles + 147) / 148;
   while (148 * waves / w.tiles < w.steps &&
          (w.steps + 148 * waves / w.tiles - 1) / (148 * waves / w.tiles) > kCsSteps)
@@ -498,7 +504,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // kGroups groups of threads take every kGroups-th split each and are joined in
 // order.  A narrow matrix has few CTAs and up to 148 splits: more than 8 of them
 // take four groups (backward of 5000 x 256 x 256, rank 40: 35 us with one group,
-// 27 with four; of 1999 x 2048 x 8192, which has up to 4 splits: 36.9 and 37.7).
+// 27 with four; GPU time of 8192 x 14336 x 4096 with 9 splits for dA, rank 16: 97.9
+// and 95.4, rank 64, where dB's 6 splits have most of the work: 133.0 and 136.7; of
+// 1999 x 2048 x 8192, rank 64, up to 4 splits: 33.6 and 34.0).
 // [cols][r] outputs leave through shared memory, 16 j side by side.  The CTAs of a
 // second job follow the first's.
 constexpr int kCrCols = 32;

@@ -5,9 +5,11 @@
 //   int8:  step = bf16(a / 127), q = round(x / step) in [-127, 127]
 //   E4M3:  step = bf16(a / 256), q = E4M3(x / step), saturating
 // and the block stands for x^ = bf16(q step).  Both roundings are to nearest
-// even.  A bf16 step (not the exact a / 127) makes the decode one bf16 product
-// of two bf16 numbers, q and step, rounded once: two values per instruction
-// and no fp32 detour in the kernels that feed the tensor cores from it.
+// even.  A bf16 step (not the exact a / 127) makes the decode one product of two
+// bf16 numbers, q and step, rounded once.  int8: a packed bf16 product, two
+// values per instruction, with no fp32 detour in the kernels that feed the tensor
+// cores from it.  E4M3: codes to fp16 two at a time, to fp32, the exact product
+// there, and one rounding to a bf16 pair.
 #pragma once
 
 #include "common.cuh"

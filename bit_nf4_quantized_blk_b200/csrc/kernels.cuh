@@ -7,8 +7,13 @@
 
 namespace qnf4 {
 
-// Launch a kernel that starts with pdl_wait_prior() behind one that lets its
-// dependents go early (pdl_launch_dependents): its launch overlaps that one.
+// Launch a kernel behind one that lets its dependents go early
+// (pdl_launch_dependents): its launch overlaps that one.  Most such kernels start
+// with pdl_wait_prior().  Those of act8.cu wait later: before the first load of
+// what the previous kernel wrote (act8_colsum_kernel: the producer alone, while
+// others already read the checkpoint), or only at their end (the second of two
+// products, dA beside the dX GEMM).  Until its wait such a kernel must neither
+// read what the previous kernel writes nor write what that one reads or writes.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
                              Args&&... args) {

@@ -607,8 +607,11 @@ cudaError_t launch_bwd(const ResidualNormBwd& p, cudaStream_t stream) {
 int residual_norm_bwd_ctas(int64_t M, int64_t D, bool res_fp32) {
   // Every CTA leaves a partial row of the column sums: with few rows, the same
   // number of CTAs on each SM and three or more rows for each keep those below
-  // the operands themselves (999 x 2048, 128 threads each: 296 CTAs 16.4 us, 148
-  // 17.4, 249 18.4, 444 18.5, 499 20.5).
+  // the operands themselves.  GPU time of bf16 rows: 999 x 2048 (128 threads each)
+  // 296 CTAs 11.3 us, 148 13.3, 444 12.3, all 592 12.9; 999 x 1024 (64 threads)
+  // 296 9.8, 148 12.5, all 12.6; 3000 x 2048 888, so all 592, 19.2, 148 27.1.
+  // Where few CTAs fit an SM anyway it makes no difference (fp32 rows, 999 x 2048,
+  // 256 threads: 148 14.0, 296 14.2).
   return static_cast<int>(
       std::min<int64_t>(norm_ctas(M, D, res_fp32, kBwdResident), 148 * std::max<int64_t>(1, M / (148 * 3))));
 }

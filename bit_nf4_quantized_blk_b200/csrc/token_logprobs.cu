@@ -13,7 +13,8 @@
 // with x is exact.
 //
 // HBM-bound: 2 or 4 bytes per logit against about 6 instructions (packed fp32
-// pairs) and one exponential, which is the tightest unit behind HBM.  CTAs
+// pairs) and one exponential.  Behind HBM the issue slots are the tightest (bf16,
+// top 5: 61% of active cycles), then the exponentials (46%).  CTAs
 // stay for many rows and every thread runs its own ring of asynchronous
 // copies (cp.async into slots that it alone reads, so without barriers) across
 // the rows' ends: the next row arrives while this one is reduced.  With few
