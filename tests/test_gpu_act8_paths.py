@@ -244,3 +244,52 @@ def test_third_parts_of_u_and_v(M, r, fmt):
     for u in (U, None):
         _, dB = run(codes, sign[:, None] * y, A, torch.zeros((N, r)), u)
         assert ((dB - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("M, N, K, r", [(16, 40, 64, 64), (1, 136, 192, 64), (2100, 264, 1088, 16), (1987, 2056, 512, 40)])
+@pytest.mark.parametrize("dx", [False, True])
+def test_captured_and_two_at_once(M, N, K, r, dx):
+    """A captured backward replays to the eager result, and two on streams of their own, each with its workspace, do
+    not meet."""
+    p, other = Problem(M, N, K, r, "int8"), Problem(M, N, K, r, "e4m3", seed=1)
+    size = binding.qlora_linear_ws_bytes(M, N, K, r)
+
+    def buffers():
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        binding.qlora_workspace_reset(ws)
+        return ws, (torch.empty((M, K), dtype=BF16, device="cuda") if dx else None, torch.empty((r, K), device="cuda"),
+                    torch.empty((N, r), device="cuda"))
+
+    def call(q, ws, out, stream=None):
+        binding.qlora_linear_bwd_act8(q.w, q.a, q.dY, q.A, q.B, r, q.s, out[0], 0, out[1], out[2], ws, stream=stream)
+
+    def same(a, b):
+        return all(x is None or torch.equal(x, y) for x, y in zip(a, b))
+
+    want = []
+    for q in (p, other):
+        ws, out = buffers()
+        call(q, ws, out)
+        want.append(out)
+    torch.cuda.synchronize()
+    ws, out = buffers()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(p, ws, out)
+        call(p, ws, out)  # on the same workspace
+    for _ in range(3):
+        for t in out:
+            if t is not None:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, want[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    pairs = [buffers() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for q, s, (ws, out) in zip((p, other), streams, pairs):
+            call(q, ws, out, stream=s)
+    torch.cuda.synchronize()
+    for (ws, out), w in zip(pairs, want):
+        assert binding.qlora_workspace_status(ws) == 0 and same(out, w)
