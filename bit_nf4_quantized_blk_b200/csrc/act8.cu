@@ -404,11 +404,13 @@ TcWork cs_work(int64_t M, int64_t C, bool dense) {
 
 }  // namespace
 
-template <int kFormat>
+// kDirect: a product with a single split leaves its scaled result, [r][cols], in
+// `out`, without partials and a reduction.
+template <int kFormat, bool kDirect>
 __global__ void __launch_bounds__(kTcThreads, 1)
     act8_colsum_kernel(Act8View x, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmHi,
                        const __grid_constant__ CUtensorMap tmLo, const __grid_constant__ CUtensorMap tmLo2, int r16,
-                       int splits, float* __restrict__ part, bool after, int* status) {
+                       int r, int splits, float scale, float* __restrict__ out, bool after, int* status) {
   constexpr bool kDense = kFormat == kAct8Dense;
   extern __shared__ uint8_t smem_raw[];
   if (!after) pdl_launch_dependents();
@@ -485,11 +487,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int i = 0; i < kCsSums; ++i) tc_wait_ld(v[i]);
         if (k < C) {
-          float* dst = part + (static_cast<int64_t>(z) * r16 + j0) * C + k;
+          float* dst = out + (static_cast<int64_t>(z) * r16 + j0) * C + k;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            dst[j * C] = (__uint_as_float(v[0][j]) + __uint_as_float(v[3][j])) +
-                         (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+          for (int j = 0; j < 16; ++j) {
+            const float sum = (__uint_as_float(v[0][j]) + __uint_as_float(v[3][j])) +
+                              (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
+            if constexpr (!kDirect)
+              dst[j * C] = sum;
+            else if (j0 + j < r)
+              dst[j * C] = scale * sum;
+          }
         }
         __syncwarp();  // the next load is the whole warp's
       }
@@ -575,21 +582,21 @@ __global__ void __launch_bounds__(128 * kGroups)
 
 namespace {
 
-template <int kFormat>
-cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4], int r16, int splits, float* part,
-                                 bool after, int* status, cudaStream_t stream) {
+template <int kFormat, bool kDirect>
+cudaError_t launch_colsum_format(const Act8View& x, const CUtensorMap (&maps)[4], int r, int splits, float scale,
+                                 float* out, bool after, int* status, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static DeviceOnce configured;
   e = configured.run(dev, [] {
-    return cudaFuncSetAttribute(act8_colsum_kernel<kFormat>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(act8_colsum_kernel<kFormat, kDirect>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 tc_smem<kFormat>(kCsStage));
   });
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((x.cols + kCsCols - 1) / kCsCols), static_cast<unsigned>(splits));
-  return launch_dependent(act8_colsum_kernel<kFormat>, grid, kTcThreads, tc_smem<kFormat>(kCsStage), stream, x, maps[0],
-                          maps[1], maps[2], maps[3], r16, splits, part, after, status);
+  return launch_dependent(act8_colsum_kernel<kFormat, kDirect>, grid, kTcThreads, tc_smem<kFormat>(kCsStage), stream, x,
+                          maps[0], maps[1], maps[2], maps[3], (r + 15) / 16 * 16, r, splits, scale, out, after, status);
 }
 
 }  // namespace
@@ -602,14 +609,25 @@ bool plan_act8_colsums(ColsumJob* jobs, int count, int r, float* pool, size_t ro
     work[i] = cs_work(x.rows, x.cols, x.format == kAct8Dense);
     split[i] = static_cast<size_t>((r + 15) / 16 * 16) * static_cast<size_t>(x.cols) * sizeof(float);
   }
+  // A single split in the result's own order needs no partials and, alone, no
+  // reduction (17 x 1024 x 4096, rank 16: 10.8 us, so 10.3).  Beside another product,
+  // whose reduction runs anyway, that costs 1 us and is done only where there is no
+  // room (up to 16 tokens, ranks above 48: 16 x 512 x 512, rank 64, 15.6 us; with room
+  // 14.8, one product after the other 18.4).  The other order, [cols][r], never: a row
+  // per lane costs the epilogue 5 us at rank 64.
+  bool want_direct = count == 1;
+  auto direct = [&](int i) {
+    return want_direct && jobs[i].dst_rc && jobs[i].x.format != kAct8Dense && work[i].splits == 1;
+  };
+  auto bytes = [&](int i) { return direct(i) ? 0 : static_cast<size_t>(work[i].splits) * split[i]; };
   if (count == 2) {
     tc_share_wave(work[0], work[1]);
     // Fewer splits where they take most room, while the chains stay short.
-    auto bytes = [&](int i) { return static_cast<size_t>(work[i].splits) * split[i]; };
     auto spare = [&](int i) {
       const int fewer = work[i].splits - 1;
       return fewer > 0 && (work[i].steps + fewer - 1) / fewer <= kCsSteps;
     };
+    want_direct = bytes(0) + bytes(1) > room;
     while (bytes(0) + bytes(1) > room) {
       int i = bytes(1) > bytes(0) ? 1 : 0;
       if (!spare(i)) i = 1 - i;
@@ -617,13 +635,14 @@ bool plan_act8_colsums(ColsumJob* jobs, int count, int r, float* pool, size_t ro
       --work[i].splits;
     }
   } else {
-    work[0].splits = static_cast<int>(std::min<size_t>(work[0].splits, room / split[0]));
-    if (work[0].splits < 1) return false;
+    const int64_t most = static_cast<int64_t>(room / split[0]);
+    work[0].splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(work[0].splits, most)));
+    if (bytes(0) > room) return false;
   }
   for (int i = 0; i < count; ++i) {
     jobs[i].splits = work[i].splits;
-    jobs[i].part = pool;
-    pool += static_cast<size_t>(work[i].splits) * split[i] / sizeof(float);
+    jobs[i].part = direct(i) ? nullptr : pool;
+    pool += bytes(i) / sizeof(float);
   }
   return true;
 }
@@ -633,6 +652,7 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
   const int rt = (r + 15) / 16;
   ColsumReduceJob reduce[2];
   unsigned blocks[2] = {0, 0};
+  int reductions = 0, most = 0;
   for (int i = 0; i < count; ++i) {
     const ColsumJob& job = jobs[i];
     const Act8View& x = job.x;
@@ -644,19 +664,26 @@ cudaError_t launch_act8_colsums(const ColsumJob* jobs, int count, int r, float s
     maps[0] = maps[1];
     if (dense && !encode_tensor_map_2d(&maps[0], x.codes, x.rows, x.cols, kCsTok, 64)) return cudaErrorInvalidValue;
     const int splits = job.splits;
-    const cudaError_t e =
-        dense ? launch_colsum_format<kAct8Dense>(x, maps, 16 * rt, splits, job.part, after, status, stream)
-        : x.format == kAct8Int8
-            ? launch_colsum_format<kAct8Int8>(x, maps, 16 * rt, splits, job.part, after, status, stream)
-            : launch_colsum_format<kAct8E4m3>(x, maps, 16 * rt, splits, job.part, after, status, stream);
+    const bool direct = job.part == nullptr;  // of a checkpoint
+    float* const out = direct ? job.dst : job.part;
+    const auto launch = dense                       ? launch_colsum_format<kAct8Dense, false>
+                        : x.format == kAct8Int8     ? direct ? launch_colsum_format<kAct8Int8, true>
+                                                             : launch_colsum_format<kAct8Int8, false>
+                        : direct                    ? launch_colsum_format<kAct8E4m3, true>
+                                                    : launch_colsum_format<kAct8E4m3, false>;
+    const cudaError_t e = launch(x, maps, r, splits, scale, out, after, status, stream);
     if (e != cudaSuccess) return e;
-    reduce[i] = ColsumReduceJob{job.part, x.cols, splits, job.dst, job.dst_rc ? 1 : 0};
-    blocks[i] = static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols);
+    if (direct) continue;
+    reduce[reductions] = ColsumReduceJob{job.part, x.cols, splits, job.dst, job.dst_rc ? 1 : 0};
+    blocks[reductions] = static_cast<unsigned>((x.cols + kCrCols - 1) / kCrCols);
+    most = std::max(most, splits);
+    ++reductions;
   }
+  if (reductions == 0) return cudaSuccess;
   const dim3 grid(blocks[0] + blocks[1], static_cast<unsigned>(rt));
-  const bool many = std::max(reduce[0].splits, reduce[count - 1].splits) > 8;
+  const bool many = most > 8;
   return launch_dependent(many ? act8_colsum_reduce_kernel<4> : act8_colsum_reduce_kernel<1>, grid, many ? 512 : 128, 0,
-                          stream, reduce[0], reduce[count - 1], blocks[0], r, scale);
+                          stream, reduce[0], reduce[reductions - 1], blocks[0], r, scale);
 }
 
 // ---------------------------------------------------------------------------

@@ -287,9 +287,10 @@ cudaError_t launch_act8_dequantize(const Act8View& a, uint16_t* X, cudaStream_t 
 // out(j, k) = scale sum_m (hi + lo + lo2)[m][j] X^[m][k] over the rows m of x
 // (a checkpoint, or bf16 values with 16-byte aligned rows), written to dst as
 // [r][cols] (dst_rc) or [cols][r].  One or two jobs: the second product starts
-// where the first leaves room, and one reduction ends both.  The first one's
-// launch overlaps the previous kernel of the stream; `overlap_first`: so may its
-// work, as that kernel writes nothing that it reads.
+// where the first leaves room, and one reduction ends both; one without partials
+// writes its result itself.  The first one's launch overlaps the
+// previous kernel of the stream; `overlap_first`: so may its work, as that kernel
+// writes nothing that it reads.
 // plan_act8_colsums sets the jobs' splits and gives their partials places in
 // `room` bytes of scratch from `pool` on.  False where two do not fit together
 // (or not even one split does): they then run in turn, each planned alone.
@@ -298,7 +299,7 @@ struct ColsumJob {
   const uint16_t *hi, *lo, *lo2;
   float* dst;
   bool dst_rc;
-  float* part;  // [splits][16 ceil(r / 16)][cols]
+  float* part;  // [splits][16 ceil(r / 16)][cols], or null: none needed
   int splits;
 };
 bool plan_act8_colsums(ColsumJob* jobs, int count, int r, float* pool, size_t room);

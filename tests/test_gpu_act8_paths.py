@@ -129,11 +129,11 @@ def test_columns_that_end_inside_a_warp(N, r):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M, N, K, r", [
-    (1, 64, 64, 64), (2, 128, 64, 64), (16, 40, 64, 64),  # dB's and dA's partials have no room side by side
-    (40000, 8, 64, 40),                                     # nor U's and V's
-    (8000, 128, 14336, 40),                                 # room with fewer splits
-    (8000, 8, 14336, 64),                                   # dA's alone with fewer splits
-    (40000, 8, 14336, 8),                                   # the same, ranks up to 16
+    (1, 64, 64, 64), (2, 128, 64, 64), (16, 40, 64, 64),  # single splits: no partials of dA
+    (40000, 8, 64, 40),                                   # no room for U's and V's partials side by side
+    (8000, 128, 14336, 40),                               # room for dB's and dA's with fewer splits
+    (8000, 8, 14336, 64),                                 # none side by side, for dA's alone with fewer splits
+    (40000, 8, 14336, 8),                                 # the same, ranks up to 16
     (33, 72, 192, 8), (300, 72, 576, 33)])
 def test_everything_fits_the_linear_workspace(M, N, K, r, fmt):
     p = Problem(M, N, K, r, fmt)
@@ -246,7 +246,8 @@ def test_third_parts_of_u_and_v(M, r, fmt):
         assert ((dB - want).abs() <= tol).all()
 
 
-@pytest.mark.parametrize("M, N, K, r", [(16, 40, 64, 64), (1, 136, 192, 64), (2100, 264, 1088, 16), (1987, 2056, 512, 40)])
+@pytest.mark.parametrize("M, N, K, r", [(16, 40, 64, 64), (1, 136, 192, 64), (2100, 264, 1088, 16),
+                                        (1987, 2056, 512, 40), (8000, 8, 14336, 64)])
 @pytest.mark.parametrize("dx", [False, True])
 def test_captured_and_two_at_once(M, N, K, r, dx):
     """A captured backward replays to the eager result, and two on streams of their own, each with its workspace, do
